@@ -18,13 +18,14 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp4moe.
 FMT = {"nvfp4": 0, "mxfp4": 1, "mxfp8": 2, "fp8_block": 3, "fp8_row": 4, "none": 5}
 RULE = {"rtn": 0, "4over6": 1, "sweep": 2}
 TS_DYNAMIC, TS_STATIC = 0, 1
-DT_BF16, DT_F32 = 0, 1
+DT_BF16, DT_F32, DT_E4M3 = 0, 1, 2
 STATUS = {0: "FP4_OK", -1: "FP4_ERR_INVALID_ARG", -2: "FP4_ERR_SHAPE",
           -3: "FP4_ERR_UNSUPPORTED", -4: "FP4_ERR_WORKSPACE", -5: "FP4_ERR_HIP"}
 
 EXPORTED = ["fp4_quantize", "fp4_quantize_hessian", "fp4_dequantize", "fp4_block_error", "moe_fp4_workspace_layout",
             "moe_fp4_workspace_size", "moe_fp4_forward", "moe_fp4_forward_profiled",
-            "moe_fp4_route", "moe_fp4_tile_weights", "moe_fp4_forward_noalloc", "fp4_status_string",
+            "moe_fp4_route", "moe_fp4_tile_weights", "moe_fp4_forward_noalloc",
+            "fp8_block_matmul_workspace_size", "fp8_block_matmul", "fp4_status_string",
             "fp4_last_error"]
 NOALLOC_SCRATCH_BYTES = 64 << 20  # FP4_NOALLOC_SCRATCH_BYTES
 STAGES = ["permute", "x_quant", "gate_up", "h_quant", "down", "shared", "combine"]
@@ -94,6 +95,10 @@ def lib():
         L.moe_fp4_route.restype = i32
         L.moe_fp4_tile_weights.argtypes = [i32, vp, vp, i64, i64, i64, vp, vp, vp]
         L.moe_fp4_tile_weights.restype = i32
+        L.fp8_block_matmul_workspace_size.argtypes = [i32, i64, i64, i64, i64, ctypes.POINTER(sz)]
+        L.fp8_block_matmul_workspace_size.restype = i32
+        L.fp8_block_matmul.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, i64, vp, i32, vp, sz, vp]
+        L.fp8_block_matmul.restype = i32
         L.fp4_status_string.argtypes = [i32]
         L.fp4_status_string.restype = ctypes.c_char_p
         L.fp4_last_error.argtypes = []
@@ -239,6 +244,68 @@ def dequantize(q: dict, fmt: str, shape, out_dtype=torch.float32) -> torch.Tenso
     b, r, c = (int(v) for v in _dims(out))
     _check(lib().fp4_dequantize(FMT[fmt], _ptr(codes), _ptr(q["scales"]), _ptr(q.get("tensor_scale")),
                                 b, r, c, _ptr(out), _dtype_code(out), _stream()))
+    return out
+
+
+def fp8_matmul_workspace_size(x_dtype: torch.dtype, batch: int, m: int, n: int, k: int) -> int:
+    """fp8_block_matmul_workspace_size for bf16 / f32 x (codes need none)."""
+    need = ctypes.c_size_t()
+    _check(lib().fp8_block_matmul_workspace_size({torch.bfloat16: DT_BF16, torch.float32: DT_F32}[x_dtype], batch, m, n,
+                                                 k, ctypes.byref(need)))
+    return need.value
+
+
+def _same_device(dev, *tensors):
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+
+
+def fp8_matmul(x, w: dict, out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """fp8_block_matmul: y = x . W^T in block FP8.
+
+    x: contiguous bf16 / f32 device tensor [M, K] or [B, M, K], quantized
+    within the call, or a record of quantize(x, "fp8_row") (codes, scales).
+    w: a record of quantize(w, "fp8_block"): codes [N, K] or [B, N, K], scales
+    [ceil(N/128), K/128] (or [B, ...]); N need not be a multiple of 128.  A
+    leading B = 1 of w may be left out or given either way.
+    Returns y [M, N] or [B, M, N] in out_dtype (bf16 or f32), in `out` if given.
+    workspace: a uint8 device tensor of fp8_matmul_workspace_size bytes for
+    bf16 / f32 x; allocated here when not given."""
+    if isinstance(x, dict):
+        xv, xs, code = x["codes"], x["scales"], DT_E4M3
+        if xv.dtype != torch.uint8 or xs.dtype != torch.float32:
+            raise TypeError(f"x record of {xv.dtype} codes and {xs.dtype} scales, uint8 and float32 expected")
+    else:
+        xv, xs, code = x, None, _dtype_code(x)
+    wc, ws = w["codes"], w["scales"]
+    b, m, k = (int(v) for v in _dims(xv))
+    if wc.dtype != torch.uint8 or ws.dtype != torch.float32:
+        raise TypeError(f"w record of {wc.dtype} codes and {ws.dtype} scales, uint8 and float32 expected")
+    wb, n, wk = (int(v) for v in _dims(wc))
+    if wb != b or wk != k:
+        raise ValueError(f"x {tuple(xv.shape)} and W {tuple(wc.shape)} do not match")
+    if ws.numel() != b * ((n + 127) // 128) * (k // 128) or (xs is not None and xs.numel() != b * m * (k // 128)):
+        raise ValueError("scales do not match their codes")
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported dtype {out_dtype}")
+    dev = xv.device
+    shape = (*xv.shape[:-1], n)
+    _same_device(dev, xs, wc, ws, out, workspace)
+    for t in (xv, xs, wc, ws, out, workspace):
+        if t is not None and not (t.is_cuda and t.is_contiguous()):
+            raise ValueError("contiguous device tensors expected")
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=dev)
+    elif out.dtype != out_dtype or tuple(out.shape) != shape:
+        raise ValueError(f"out {out.dtype} {tuple(out.shape)}, {out_dtype} {shape} expected")
+    if workspace is None and code != DT_E4M3:
+        workspace = torch.empty(max(fp8_matmul_workspace_size(xv.dtype, b, m, n, k), 1), dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib().fp8_block_matmul(_ptr(xv), code, _ptr(xs), _ptr(wc), _ptr(ws), b, m, n, k, _ptr(out),
+                                      DT_BF16 if out_dtype == torch.bfloat16 else DT_F32, _ptr(workspace),
+                                      0 if workspace is None else workspace.numel() * workspace.element_size(), _stream()))
     return out
 
 

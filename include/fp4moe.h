@@ -79,7 +79,11 @@ typedef enum {
                           equals FP4_RULE_4OVER6)                                          */
 } fp4_rule;
 
-typedef enum { FP4_DT_BF16 = 0, FP4_DT_F32 = 1 } fp4_dtype;
+typedef enum {
+  FP4_DT_BF16 = 0,
+  FP4_DT_F32 = 1,
+  FP4_DT_E4M3 = 2 /* codes of FP4_FMT_FP8_ROW with their scales (fp8_block_matmul only) */
+} fp4_dtype;
 
 typedef enum {
   FP4_TS_DYNAMIC = 0, /* NVFP4: compute S = fp32(amax / 2688) per tensor, write it */
@@ -361,6 +365,37 @@ int moe_fp4_forward_profiled(const moe_fp4_layer* layer, const uint16_t* x, int6
 #define FP4_NOALLOC_SCRATCH_BYTES ((size_t)64 << 20)
 int moe_fp4_forward_noalloc(const moe_fp4_layer* layer, const uint16_t* x, int64_t tokens,
                             const int32_t* topk_ids, const float* topk_weights, float* y, void* stream);
+
+/*
+ * fp8_block_matmul - y[b] = x[b] . W[b]^T for `batch` independent products in
+ * block FP8, the dense layer beside a block-FP8 routed-expert layer
+ * ("MXFP4-FP8-R12", runtime contract table: block-FP8 weights on a dynamic-FP8
+ * path):
+ *   y[m][n] = sum_kb sx[m][kb] sw[n/128][kb] sum_{k in block kb} cx[m][k] cw[n][k]
+ *  x            [batch, m, k], `x_dtype`: FP4_DT_E4M3 codes with x_scales f32
+ *               [batch, m, k/128], as fp4_quantize writes FP4_FMT_FP8_ROW; or
+ *               bf16 / f32 values (finite), which the call quantizes the same
+ *               way, to the same bits (x_scales ignored).
+ *  w, w_scales  E4M3 codes [batch, n, k] and f32 scales [batch, ceil(n/128),
+ *               k/128], as fp4_quantize writes FP4_FMT_FP8_BLOCK.  n need not be
+ *               a multiple of 128: the last scale row covers the rows left.
+ *  y            [batch, m, n] bf16 or f32 (`y_dtype`), rounded once from f32 sums
+ *               of the blocks.  bf16: the sum inside a 128-block is the E4M3
+ *               MFMA's (about 1.6e-5 relative, far below bf16's rounding);
+ *               f32: the codes go through the fp16 MFMA, exactly, with f32 sums.
+ *  workspace    bf16 / f32 x: fp8_block_matmul_workspace_size bytes of device
+ *               memory, 16-byte aligned (may be NULL where that is 0).  Calls in
+ *               flight at once, captured graphs among them, need one each.
+ * Any m >= 0 and n >= 0; every buffer is contiguous.  The result does not
+ * depend on other rows of x or on earlier calls, and repeats bit for bit.
+ * Errors: k % 128, k == 0 -> FP4_ERR_SHAPE; unknown dtype, null or misaligned
+ * pointer (x, w: 16 bytes) -> FP4_ERR_INVALID_ARG; a dimension beyond the grid's
+ * or 2^31 -> FP4_ERR_UNSUPPORTED; FP4_ERR_WORKSPACE.  Stream-ordered, asynchronous.
+ */
+int fp8_block_matmul_workspace_size(int x_dtype, int64_t batch, int64_t m, int64_t n, int64_t k, size_t* bytes);
+int fp8_block_matmul(const void* x, int x_dtype, const float* x_scales, const uint8_t* w, const float* w_scales,
+                     int64_t batch, int64_t m, int64_t n, int64_t k, void* y, int y_dtype, void* workspace,
+                     size_t workspace_bytes, void* stream);
 
 const char* fp4_status_string(int status);
 const char* fp4_last_error(void);
