@@ -25,7 +25,7 @@ STATUS = {0: "FP4_OK", -1: "FP4_ERR_INVALID_ARG", -2: "FP4_ERR_SHAPE",
 EXPORTED = ["fp4_quantize", "fp4_quantize_hessian", "fp4_dequantize", "fp4_block_error", "moe_fp4_workspace_layout",
             "moe_fp4_workspace_size", "moe_fp4_forward", "moe_fp4_forward_profiled",
             "moe_fp4_route", "moe_fp4_tile_weights", "moe_fp4_forward_noalloc",
-            "fp8_block_matmul_workspace_size", "fp8_block_matmul", "fp4_status_string",
+            "moe_fp4_few_workspace_size", "moe_fp4_forward_few", "fp8_block_matmul_workspace_size", "fp8_block_matmul", "fp4_status_string",
             "fp4_last_error"]
 NOALLOC_SCRATCH_BYTES = 64 << 20  # FP4_NOALLOC_SCRATCH_BYTES
 STAGES = ["permute", "x_quant", "gate_up", "h_quant", "down", "shared", "combine"]
@@ -95,6 +95,10 @@ def lib():
         L.moe_fp4_route.restype = i32
         L.moe_fp4_tile_weights.argtypes = [i32, vp, vp, i64, i64, i64, vp, vp, vp]
         L.moe_fp4_tile_weights.restype = i32
+        L.moe_fp4_few_workspace_size.argtypes = [ctypes.POINTER(LayerStruct), i64, ctypes.POINTER(sz)]
+        L.moe_fp4_few_workspace_size.restype = i32
+        L.moe_fp4_forward_few.argtypes = [ctypes.POINTER(LayerStruct), vp, i64, vp, vp, vp, i32, vp, vp, vp, sz, vp]
+        L.moe_fp4_forward_few.restype = i32
         L.fp8_block_matmul_workspace_size.argtypes = [i32, i64, i64, i64, i64, ctypes.POINTER(sz)]
         L.fp8_block_matmul_workspace_size.restype = i32
         L.fp8_block_matmul.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, i64, vp, i32, vp, sz, vp]
@@ -389,6 +393,60 @@ def moe_forward_noalloc(layer: MoELayer, x: torch.Tensor, topk_ids: torch.Tensor
     _check(lib().moe_fp4_forward_noalloc(ctypes.byref(s), _ptr(x), T, _ptr(topk_ids), _ptr(topk_weights),
                                          _ptr(y), _stream()))
     return y
+
+
+class FewTokenLayer:
+    """A whole routed-expert layer for a few tokens (moe_fp4_forward_few): a
+    layer, its argument record and a workspace for up to max_tokens tokens
+    (1 to 16), kept between calls.
+
+    Calling it with x bf16 [T, H], router logits f32 [T, E] and an optional
+    bias f32 [E] returns (y [T, H] in out_dtype, topk_ids int32 [T, k],
+    topk_weights f32 [T, k]), in the given tensors where they are given.
+    Masked experts have logit -inf; slots left over get id -1, weight 0.
+
+    The workspace serves one call at a time: calls on several streams, or
+    captured graphs that may replay at once, need a FewTokenLayer each.  The
+    layer's tensors are those at construction."""
+
+    def __init__(self, layer: MoELayer, max_tokens: int, out_dtype: torch.dtype = torch.float32):
+        if out_dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"unsupported dtype {out_dtype}")
+        self.layer, self.max_tokens, self.out_dtype = layer, max_tokens, out_dtype
+        self.device = layer.w13.device
+        self._struct = layer.struct()
+        need = ctypes.c_size_t()
+        _check(lib().moe_fp4_few_workspace_size(ctypes.byref(self._struct), max_tokens, ctypes.byref(need)))
+        self.workspace = torch.empty(max(need.value, 1), dtype=torch.uint8, device=self.device)
+
+    def _arg(self, name, t, dtype, shape):
+        if t.dtype != dtype or tuple(t.shape) != shape or t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous {dtype} {shape} on {self.device} expected, "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+        return t.data_ptr()
+
+    def __call__(self, x: torch.Tensor, logits: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                 y: Optional[torch.Tensor] = None, topk_ids: Optional[torch.Tensor] = None,
+                 topk_weights: Optional[torch.Tensor] = None):
+        L, dev = self.layer, self.device
+        T, E, k, H = int(x.shape[0]), L.num_experts, L.top_k, L.hidden
+        if T > self.max_tokens:
+            raise ValueError(f"{T} tokens, at most {self.max_tokens}")
+        if y is None:
+            y = torch.empty(T, H, dtype=self.out_dtype, device=dev)
+        if topk_ids is None:
+            topk_ids = torch.empty(T, k, dtype=torch.int32, device=dev)
+        if topk_weights is None:
+            topk_weights = torch.empty(T, k, dtype=torch.float32, device=dev)
+        ptrs = (self._arg("x", x, torch.bfloat16, (T, H)), self._arg("logits", logits, torch.float32, (T, E)),
+                None if bias is None else self._arg("bias", bias, torch.float32, (E,)),
+                self._arg("y", y, self.out_dtype, (T, H)), self._arg("topk_ids", topk_ids, torch.int32, (T, k)),
+                self._arg("topk_weights", topk_weights, torch.float32, (T, k)))
+        with torch.cuda.device(dev):
+            _check(lib().moe_fp4_forward_few(ctypes.byref(self._struct), ptrs[0], T, ptrs[1], ptrs[2], ptrs[3],
+                                             DT_F32 if self.out_dtype == torch.float32 else DT_BF16, ptrs[4], ptrs[5],
+                                             self.workspace.data_ptr(), self.workspace.numel(), _stream()))
+        return y, topk_ids, topk_weights
 
 
 _HIP_EVENT_DISABLE_SYSTEM_FENCE = 0x20000000

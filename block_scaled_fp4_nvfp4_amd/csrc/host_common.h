@@ -6,6 +6,8 @@
 #include <stdint.h>
 #include <stdio.h>
 
+#include <atomic>
+
 #include "../../include/fp4moe.h"
 
 namespace fp4 {
@@ -43,6 +45,21 @@ struct RelaxedCapture {
     if (ok) (void)hipThreadExchangeStreamCaptureMode(&mode);
   }
 };
+
+// Raises a kernel's dynamic-LDS limit on the current device the first time
+// it launches there; `raised` holds one bit per device, so concurrent callers
+// at worst set the attribute twice.
+inline int raise_dyn_lds(const void* kernel, int bytes, std::atomic<uint64_t>& raised) {
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return fail(FP4_ERR_HIP, "hipGetDevice failed");
+  const uint64_t bit = 1ull << (dev & 63);
+  if (raised.load(std::memory_order_acquire) & bit) return FP4_OK;
+  RelaxedCapture relaxed;
+  if (hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+    return fail(FP4_ERR_HIP, "hipFuncSetAttribute failed");
+  raised.fetch_or(bit, std::memory_order_acq_rel);
+  return FP4_OK;
+}
 
 inline unsigned grid_1d(int64_t n, int threads) {
   return (unsigned)((n + threads - 1) / threads);

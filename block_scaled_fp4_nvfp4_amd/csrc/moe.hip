@@ -971,7 +971,7 @@ WsPtrs ws_pointers(const WsPlan& p, void* base) {
   return w;
 }
 
-static int validate_layer(const moe_fp4_layer* L, int64_t T) {
+int validate_layer(const moe_fp4_layer* L, int64_t T) {
   if (!L) return fail(FP4_ERR_INVALID_ARG, "null layer");
   if (T < 0) return fail(FP4_ERR_SHAPE, "negative token count");
   if (L->num_experts < 1 || L->hidden < 1 || L->inter < 1)
@@ -1003,6 +1003,16 @@ static int validate_layer(const moe_fp4_layer* L, int64_t T) {
     return fail(FP4_ERR_INVALID_ARG, "tiled FP4 codes need tiled scales; tiled block-FP8 codes take none");
   if ((L->w13_tiled && L->hidden % 128) || (L->w2_tiled && L->inter % 128))
     return fail(FP4_ERR_SHAPE, "tiled weights need a reduction size that is a multiple of 128");
+  return FP4_OK;
+}
+
+int validate_layer_pointers(const moe_fp4_layer* L) {
+  if (!L->w13 || !L->w13_scale || !L->w2 || !L->w2_scale)
+    return fail(FP4_ERR_INVALID_ARG, "null weight pointer");
+  if (L->w_fmt == FP4_FMT_NVFP4 && (!L->w13_scale_2 || !L->w2_scale_2))
+    return fail(FP4_ERR_INVALID_ARG, "NVFP4 weights need weight_scale_2");
+  if (L->shared_inter > 0 && (!L->ws13 || !L->ws13_scale || !L->ws2 || !L->ws2_scale || !L->shared_gate))
+    return fail(FP4_ERR_INVALID_ARG, "null shared-expert pointer");
   return FP4_OK;
 }
 
@@ -1093,12 +1103,7 @@ static int forward_impl(const moe_fp4_layer* L, const uint16_t* x, int64_t T, co
   FP4_CHECK(validate_layer(L, T));
   if (T == 0) return FP4_OK;
   if (!x || !topk_ids || !topk_weights || !y) return fail(FP4_ERR_INVALID_ARG, "null tensor pointer");
-  if (!L->w13 || !L->w13_scale || !L->w2 || !L->w2_scale)
-    return fail(FP4_ERR_INVALID_ARG, "null weight pointer");
-  if (L->w_fmt == FP4_FMT_NVFP4 && (!L->w13_scale_2 || !L->w2_scale_2))
-    return fail(FP4_ERR_INVALID_ARG, "NVFP4 weights need weight_scale_2");
-  if (L->shared_inter > 0 && (!L->ws13 || !L->ws13_scale || !L->ws2 || !L->ws2_scale || !L->shared_gate))
-    return fail(FP4_ERR_INVALID_ARG, "null shared-expert pointer");
+  FP4_CHECK(validate_layer_pointers(L));
   WsPlan p;
   FP4_CHECK(plan_workspace(L, T, &p));
   if (!workspace || workspace_bytes < p.total)

@@ -1613,21 +1613,6 @@ static int64_t gemm_grid(int64_t tiles_m_bound, int N, int BN) {
   return (tiles_m_bound * (N / BN) + 7) / 8 * 8;
 }
 
-// Raises a kernel's dynamic-LDS limit on the current device the first time
-// it launches there; `raised` holds one bit per device, so concurrent callers
-// at worst set the attribute twice.
-static int raise_dyn_lds(const void* kernel, int bytes, std::atomic<uint64_t>& raised) {
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return fail(FP4_ERR_HIP, "hipGetDevice failed");
-  const uint64_t bit = 1ull << (dev & 63);
-  if (raised.load(std::memory_order_acquire) & bit) return FP4_OK;
-  RelaxedCapture relaxed;
-  if (hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
-    return fail(FP4_ERR_HIP, "hipFuncSetAttribute failed");
-  raised.fetch_or(bit, std::memory_order_acq_rel);
-  return FP4_OK;
-}
-
 template <int EPI, int NSUB, int KS, bool WT, int NTW = 1>
 static int launch_gemm_nv2_t(const GemmArgs& a, int64_t tiles_m_bound, hipStream_t st) {
   using C = Nv2Cfg<EPI, NSUB, KS>;

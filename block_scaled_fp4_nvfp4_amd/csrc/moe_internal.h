@@ -50,6 +50,8 @@ struct Marker {
   }
 };
 
+int validate_layer(const moe_fp4_layer* L, int64_t T);
+int validate_layer_pointers(const moe_fp4_layer* L);
 int plan_workspace(const moe_fp4_layer* L, int64_t T, WsPlan* w);
 bool w4a8_gemv(const moe_fp4_layer* L, int64_t T);
 WsPtrs ws_pointers(const WsPlan& p, void* base);

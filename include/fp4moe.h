@@ -367,6 +367,37 @@ int moe_fp4_forward_noalloc(const moe_fp4_layer* layer, const uint16_t* x, int64
                             const int32_t* topk_ids, const float* topk_weights, float* y, void* stream);
 
 /*
+ * moe_fp4_forward_few - the whole layer for a few tokens (1 to 16), from the
+ * router's logits to y: moe_fp4_route and moe_fp4_forward in two launches
+ * (three with quantized activations or a shared expert), for every format pair
+ * and the shared expert; the decode step of one or a few sequences.
+ *  x            bf16 [tokens, H], finite.
+ *  logits, bias f32 [tokens, E] and [E] (bias may be NULL), selected from as by
+ *               moe_fp4_route.  An expert whose logit + bias is -inf (or NaN)
+ *               is never selected: slots left over get id -1 and weight 0, and
+ *               a token with every expert masked (an empty slot of a batch)
+ *               gets only the shared expert's part, or zeros.
+ *  y            [tokens, H] f32 or bf16 (`y_dtype`), rounded once from f32 sums.
+ *  topk_ids, topk_weights  optional out (may be NULL): int32 / f32 [tokens, k].
+ *  workspace    moe_fp4_few_workspace_size bytes of device memory, 16-byte
+ *               aligned, written before it is read in every call; calls in
+ *               flight at once, captured graphs among them, need one each.
+ * Quantized activations follow moe_fp4_forward, NVFP4's dynamic tensor scales
+ * included: S_x over all of x, masked tokens among it, and S_h over the
+ * selected pairs' h.  The layer's tiled weight copies are not read.  Results
+ * repeat bit for bit.
+ * Errors: as moe_fp4_forward for the layer; more than 16 tokens or 1024
+ * experts, or tokens whose x (2 bytes each, with the routing's tables) exceeds
+ * the LDS (16 tokens: hidden up to about 4000) -> FP4_ERR_UNSUPPORTED;
+ * misaligned pointer (x, codes, gate: 16 bytes) -> FP4_ERR_INVALID_ARG.
+ * tokens == 0 is a no-op.  Stream-ordered, asynchronous.
+ */
+int moe_fp4_few_workspace_size(const moe_fp4_layer* layer, int64_t tokens, size_t* bytes);
+int moe_fp4_forward_few(const moe_fp4_layer* layer, const uint16_t* x, int64_t tokens, const float* logits,
+                        const float* bias, void* y, int y_dtype, int32_t* topk_ids, float* topk_weights,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * fp8_block_matmul - y[b] = x[b] . W[b]^T for `batch` independent products in
  * block FP8, the dense layer beside a block-FP8 routed-expert layer
  * ("MXFP4-FP8-R12", runtime contract table: block-FP8 weights on a dynamic-FP8
