@@ -259,10 +259,25 @@ def fp8_matmul_workspace_size(x_dtype: torch.dtype, batch: int, m: int, n: int, 
     return need.value
 
 
-def _same_device(dev, *tensors):
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
+def _raw_stream(index: int) -> int:
+    """The current stream of device `index` as an integer (torch.cuda.current_stream builds an object
+    first, which costs as much as a kernel launch)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _on_device(index: int, fn, *args):
+    """fn(*args) with `index` the current device; the library launches on the current device."""
+    if torch.cuda.current_device() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
+
+
+def _device_tensor(t: torch.Tensor, dev: torch.device, name: str) -> int:
+    if t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous tensor on {dev} expected, got {'' if t.is_contiguous() else 'non-contiguous '}"
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
 def fp8_matmul(x, w: dict, out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
@@ -284,32 +299,37 @@ def fp8_matmul(x, w: dict, out_dtype: torch.dtype = torch.bfloat16, out: Optiona
     else:
         xv, xs, code = x, None, _dtype_code(x)
     wc, ws = w["codes"], w["scales"]
-    b, m, k = (int(v) for v in _dims(xv))
     if wc.dtype != torch.uint8 or ws.dtype != torch.float32:
         raise TypeError(f"w record of {wc.dtype} codes and {ws.dtype} scales, uint8 and float32 expected")
-    wb, n, wk = (int(v) for v in _dims(wc))
+    b, m, k = _dims(xv)
+    wb, n, wk = _dims(wc)
     if wb != b or wk != k:
         raise ValueError(f"x {tuple(xv.shape)} and W {tuple(wc.shape)} do not match")
     if ws.numel() != b * ((n + 127) // 128) * (k // 128) or (xs is not None and xs.numel() != b * m * (k // 128)):
         raise ValueError("scales do not match their codes")
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    out_code = DT_BF16 if out_dtype == torch.bfloat16 else DT_F32
+    if out_code == DT_F32 and out_dtype != torch.float32:
         raise TypeError(f"unsupported dtype {out_dtype}")
     dev = xv.device
-    shape = (*xv.shape[:-1], n)
-    _same_device(dev, xs, wc, ws, out, workspace)
-    for t in (xv, xs, wc, ws, out, workspace):
-        if t is not None and not (t.is_cuda and t.is_contiguous()):
-            raise ValueError("contiguous device tensors expected")
+    if dev.type != "cuda":
+        raise ValueError(f"device tensors expected, got {dev}")
+    shape = (m, n) if xv.dim() == 2 else (b, m, n)
     if out is None:
         out = torch.empty(shape, dtype=out_dtype, device=dev)
     elif out.dtype != out_dtype or tuple(out.shape) != shape:
         raise ValueError(f"out {out.dtype} {tuple(out.shape)}, {out_dtype} {shape} expected")
-    if workspace is None and code != DT_E4M3:
-        workspace = torch.empty(max(fp8_matmul_workspace_size(xv.dtype, b, m, n, k), 1), dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib().fp8_block_matmul(_ptr(xv), code, _ptr(xs), _ptr(wc), _ptr(ws), b, m, n, k, _ptr(out),
-                                      DT_BF16 if out_dtype == torch.bfloat16 else DT_F32, _ptr(workspace),
-                                      0 if workspace is None else workspace.numel() * workspace.element_size(), _stream()))
+    ws_bytes = 0
+    if workspace is not None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    elif code != DT_E4M3:
+        ws_bytes = fp8_matmul_workspace_size(xv.dtype, b, m, n, k)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    _check(_on_device(dev.index, lib().fp8_block_matmul, _device_tensor(xv, dev, "x"), code,
+                      None if xs is None else _device_tensor(xs, dev, "x scales"), _device_tensor(wc, dev, "W"),
+                      _device_tensor(ws, dev, "W scales"), b, m, n, k, _device_tensor(out, dev, "out"), out_code,
+                      None if workspace is None else _device_tensor(workspace, dev, "workspace"), ws_bytes,
+                      _raw_stream(dev.index)))
     return out
 
 
@@ -414,38 +434,41 @@ class FewTokenLayer:
             raise TypeError(f"unsupported dtype {out_dtype}")
         self.layer, self.max_tokens, self.out_dtype = layer, max_tokens, out_dtype
         self.device = layer.w13.device
+        self._experts, self._top_k, self._hidden = layer.num_experts, layer.top_k, layer.hidden
+        self._out_code = DT_F32 if out_dtype == torch.float32 else DT_BF16
         self._struct = layer.struct()
+        self._layer_ref = ctypes.byref(self._struct)
         need = ctypes.c_size_t()
-        _check(lib().moe_fp4_few_workspace_size(ctypes.byref(self._struct), max_tokens, ctypes.byref(need)))
+        _check(lib().moe_fp4_few_workspace_size(self._layer_ref, max_tokens, ctypes.byref(need)))
         self.workspace = torch.empty(max(need.value, 1), dtype=torch.uint8, device=self.device)
 
-    def _arg(self, name, t, dtype, shape):
-        if t.dtype != dtype or tuple(t.shape) != shape or t.device != self.device or not t.is_contiguous():
-            raise ValueError(f"{name}: contiguous {dtype} {shape} on {self.device} expected, "
+    def _arg(self, name, t, dtype, rows, cols):
+        if t.dtype != dtype or t.shape != (rows, cols) or t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous {dtype} {(rows, cols)} on {self.device} expected, "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
         return t.data_ptr()
 
     def __call__(self, x: torch.Tensor, logits: torch.Tensor, bias: Optional[torch.Tensor] = None,
                  y: Optional[torch.Tensor] = None, topk_ids: Optional[torch.Tensor] = None,
                  topk_weights: Optional[torch.Tensor] = None):
-        L, dev = self.layer, self.device
-        T, E, k, H = int(x.shape[0]), L.num_experts, L.top_k, L.hidden
+        dev, T, E, k, H = self.device, x.shape[0], self._experts, self._top_k, self._hidden
         if T > self.max_tokens:
             raise ValueError(f"{T} tokens, at most {self.max_tokens}")
         if y is None:
-            y = torch.empty(T, H, dtype=self.out_dtype, device=dev)
+            y = torch.empty((T, H), dtype=self.out_dtype, device=dev)
         if topk_ids is None:
-            topk_ids = torch.empty(T, k, dtype=torch.int32, device=dev)
+            topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev)
         if topk_weights is None:
-            topk_weights = torch.empty(T, k, dtype=torch.float32, device=dev)
-        ptrs = (self._arg("x", x, torch.bfloat16, (T, H)), self._arg("logits", logits, torch.float32, (T, E)),
-                None if bias is None else self._arg("bias", bias, torch.float32, (E,)),
-                self._arg("y", y, self.out_dtype, (T, H)), self._arg("topk_ids", topk_ids, torch.int32, (T, k)),
-                self._arg("topk_weights", topk_weights, torch.float32, (T, k)))
-        with torch.cuda.device(dev):
-            _check(lib().moe_fp4_forward_few(ctypes.byref(self._struct), ptrs[0], T, ptrs[1], ptrs[2], ptrs[3],
-                                             DT_F32 if self.out_dtype == torch.float32 else DT_BF16, ptrs[4], ptrs[5],
-                                             self.workspace.data_ptr(), self.workspace.numel(), _stream()))
+            topk_weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        if bias is not None and bias.shape != (E,):
+            raise ValueError(f"bias: ({E},) expected, got {tuple(bias.shape)}")
+        _check(_on_device(dev.index, lib().moe_fp4_forward_few, self._layer_ref, self._arg("x", x, torch.bfloat16, T, H), T,
+                          self._arg("logits", logits, torch.float32, T, E),
+                          None if bias is None else self._arg("bias", bias[None], torch.float32, 1, E),
+                          self._arg("y", y, self.out_dtype, T, H), self._out_code,
+                          self._arg("topk_ids", topk_ids, torch.int32, T, k),
+                          self._arg("topk_weights", topk_weights, torch.float32, T, k),
+                          self.workspace.data_ptr(), self.workspace.numel(), _raw_stream(dev.index)))
         return y, topk_ids, topk_weights
 
 

@@ -17,6 +17,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "fp4_device.h"
 #include "host_common.h"
@@ -79,92 +80,486 @@ __device__ __forceinline__ uint16_t out_of<uint16_t>(float v) {
   return __builtin_bit_cast(uint16_t, (__bf16)v);  // to nearest even, NaN kept
 }
 
+// 16-byte DMA from a buffer (its descriptor, the lane's and the wave's byte
+// offsets) to lds + 16 lane.  The buffer form rather than the global one: the
+// compiler counts a global load to LDS as an access to both memories and makes
+// every later LDS read wait for all that were issued before it.
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t src, uint32_t lane_off, uint32_t wave_off, void* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)lds, 16, (int)lane_off, (int)wave_off, 0, 0);
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, (int)bytes, 0x00027000);  // raw dwords, bounds-checked
+}
+
 // ------------------------------------------------------------ few rows
 
-constexpr int kSkinnyWaves = 8;
-constexpr int kSkinnyAhead = 2;  // K steps whose loads are issued together
+// x as the few-rows kernel reads it: codes with their scales, or bf16 / f32
+// values that each wave quantizes for its own K steps.
+enum XKind { X_CODES = 0, X_BF16 = 1, X_F32 = 2 };
 
-// 16 outputs x 16 MT rows of y per workgroup; its waves take every
-// kSkinnyWaves-th 128-block of K straight from memory into registers and add
-// their partial sums up in LDS.
-template <int MT, typename OutT>
-__global__ void __launch_bounds__(64 * kSkinnyWaves) fp8_skinny_kernel(MatmulArgs a) {
-  constexpr bool F32SUM = sizeof(OutT) == 4;
-  __shared__ float part[kSkinnyWaves][MT][16][17];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, r = lane & 15;
-  const int64_t b = blockIdx.z, n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * 16 * MT;
-  const int KB = a.K >> 7;
-  const int64_t NB = (a.N + 127) >> 7;
-  const uint8_t* wrow = a.w + (b * a.N + min(n0 + r, a.N - 1)) * a.K + 16 * g;  // rows past the end: the last one, unused
-  const float* wsc = a.ws + (b * NB + (n0 >> 7)) * KB;
-  const uint8_t* xrow[MT];
-  const float* xsc[MT];
+template <int XK>
+struct XRaw {
+  u32x4 v[XK == X_CODES ? 2 : XK == X_BF16 ? 4 : 8];  // chunks g, then 4 + g, of 16 values each
+  float s;
+};
+
+template <int XK>
+__device__ __forceinline__ void load_xraw(XRaw<XK>& x, const uint8_t* row, const float* srow, int kb, int g) {
+  if constexpr (XK == X_CODES) {
+    x.v[0] = ld16(row + 128 * kb + 16 * g);
+    x.v[1] = ld16(row + 128 * kb + 16 * g + 64);
+    x.s = srow[kb];
+  } else {
+    constexpr int B = XK == X_BF16 ? 2 : 4;
+    const uint8_t* p = row + (int64_t)(128 * kb + 16 * g) * B;
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t m = min(m0 + 16 * i + r, a.M - 1);
-    xrow[i] = a.x + (b * a.M + m) * a.K + 16 * g;
-    xsc[i] = a.xs + (b * a.M + m) * KB;
-  }
-  floatx4 acc[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
-  for (int kb0 = wave; kb0 < KB; kb0 += kSkinnyWaves * kSkinnyAhead) {
-    u32x4 wv[kSkinnyAhead][2], xv[kSkinnyAhead][MT][2];
-    float sw[kSkinnyAhead], sx[kSkinnyAhead][MT];
-#pragma unroll
-    for (int u = 0; u < kSkinnyAhead; ++u) {
-      const int kb = min(kb0 + u * kSkinnyWaves, KB - 1);
-      wv[u][0] = ld16(wrow + 128 * kb);
-      wv[u][1] = ld16(wrow + 128 * kb + 64);
-      sw[u] = wsc[kb];
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        xv[u][i][0] = ld16(xrow[i] + 128 * kb);
-        xv[u][i][1] = ld16(xrow[i] + 128 * kb + 64);
-        sx[u][i] = xsc[i][kb];
-      }
+    for (int i = 0; i < B; ++i) {
+      x.v[i] = ld16(p + 16 * i);
+      x.v[B + i] = ld16(p + 64 * B + 16 * i);
     }
-#pragma unroll
-    for (int u = 0; u < kSkinnyAhead; ++u) {
-      if (kb0 + u * kSkinnyWaves < KB) {
-        const intx8 wf = frag_of(wv[u][0], wv[u][1]);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const floatx4 p = block_product<F32SUM>(wf, frag_of(xv[u][i][0], xv[u][i][1]));
-          const float s = sx[u][i] * sw[u];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) acc[i][q] = fmaf(p[q], s, acc[i][q]);
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) part[wave][i][r][4 * g + q] = acc[i][q];
-  __syncthreads();
-  for (int t = threadIdx.x; t < MT * 256; t += 64 * kSkinnyWaves) {
-    const int m = t >> 4, n = t & 15;
-    float s = 0.f;
-#pragma unroll
-    for (int w = 0; w < kSkinnyWaves; ++w) s += part[w][m >> 4][m & 15][n];
-    if (m0 + m < a.M && n0 + n < a.N)
-      static_cast<OutT*>(a.y)[(b * a.M + m0 + m) * a.N + n0 + n] = out_of<OutT>(s);
   }
 }
 
-template <typename OutT>
-static int launch_matmul(const MatmulArgs& a, int64_t batch, hipStream_t st) {
-  const int64_t nx = (a.N + 15) / 16;
-  const int mt = a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
-  const int64_t ny = (a.M + 16 * mt - 1) / (16 * mt);
-  if (nx > INT32_MAX || ny > 65535 || batch > 65535)
-    return fail(FP4_ERR_UNSUPPORTED, "matmul: too many rows, outputs or matrices");
-  const dim3 grid((unsigned)nx, (unsigned)ny, (unsigned)batch), block(64 * kSkinnyWaves);
-  if (mt == 1) hipLaunchKernelGGL((fp8_skinny_kernel<1, OutT>), grid, block, 0, st, a);
-  else if (mt == 2) hipLaunchKernelGGL((fp8_skinny_kernel<2, OutT>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((fp8_skinny_kernel<4, OutT>), grid, block, 0, st, a);
+// The E4M3 fragment of a lane's 32 values of one 128-block, whose four lanes
+// are r, r + 16, r + 32, r + 48, to the codes of fp4_quantize: sigma =
+// fp32(amax / 448), code = E4M3 nearest to v / sigma.  q = v * fp32(1 / sigma)
+// is within 1.5 ulp of the quotient and rounds to the same code unless an
+// E4M3 midpoint (f32 pattern ..80000h in the low 20 bits) lies within 2 ulp
+// of it; those, and the subnormal range, take the exact path, per wave.
+template <int XK>
+__device__ __forceinline__ intx8 quantized_frag(const XRaw<XK>& x, float& sigma) {
+  if constexpr (XK == X_CODES) {
+    sigma = x.s;
+    return frag_of(x.v[0], x.v[1]);
+  } else {
+    float v[32];
+    if constexpr (XK == X_BF16) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        v[2 * i] = __uint_as_float(x.v[i >> 2][i & 3] << 16);
+        v[2 * i + 1] = __uint_as_float(x.v[i >> 2][i & 3] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(x.v[i >> 2][i & 3]);
+    }
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(v[i]));
+    amax = fmaxf(amax, __shfl_xor(amax, 16));
+    amax = fmaxf(amax, __shfl_xor(amax, 32));
+    sigma = (float)((double)amax / 448.0);
+    const float inv = sigma > 0.0f ? 1.0f / sigma : 0.0f;
+    uint32_t near_mid = 0xFFFFFFFFu, small = 0xFFFFFFFFu;
+    int d[8];
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      float q[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        q[j] = v[4 * w + j] * inv;
+        const uint32_t bits = __float_as_uint(q[j]);
+        near_mid = min(near_mid, (bits << 12) + 0x80002000u);  // 0 .. 4 ulp (of 4096) around a midpoint
+        small = min(small, (bits & 0x7FFFFFFFu) - 1u);         // zero wraps to the largest
+      }
+      d[w] = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+      d[w] = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], d[w], true);
+    }
+    // 1 / sigma that is not a normal number (rows below 2^-117 or above 2^126) is no use either
+    const bool odd = near_mid <= 0x4000u || small < 0x3C800000u - 1u || !(inv > 0x1p-125f && inv < 0x1p125f);
+    if (odd) {
+      const float sg = sigma > 0.0f ? sigma : 1.0f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        uint32_t t = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // e4m3_exact_quotient without its branches
+          const float e = v[4 * w + j], m = fabsf(e), q = fminf(m / sg, kE4M3Max);
+          uint32_t c = e4m3_hw(q);
+          const double A = (double)m, M = (double)q * (double)sg;
+          const float vc = __builtin_amdgcn_cvt_f32_fp8((int)c, 0);
+          const bool mid = e4m3_is_midpoint(q);
+          c += (uint32_t)(mid & (A > M) & (vc < q)) - (uint32_t)(mid & (A < M) & (vc > q));
+          t |= ((sigma > 0.0f ? c : 0u) | ((__float_as_uint(e) >> 24) & 0x80u)) << (8 * j);
+        }
+        d[w] = (int)t;
+      }
+    }
+    return intx8{d[0], d[1], d[2], d[3], d[4], d[5], d[6], d[7]};
+  }
+}
+
+
+// At most 16 rows of x: a workgroup of NW waves walks over strips of 16
+// outputs; wave w takes the 128-blocks w, w + NW, ... of K (U at most) of every
+// strip.  Its share of x is loaded (and quantized) once and stays in
+// registers as MFMA fragments; its share of the weights streams through a
+// ring of D steps in LDS that belongs to the wave alone (16 rows x 128 bytes
+// a step, by DMA, several strips ahead and without barriers: loading fragments
+// straight into registers touches four rows in every four lanes, which
+// measured 10.4 us against HERE us at 16 x 10240 x 2560).  A strip's partial sums meet in
+// LDS, one barrier a strip.  Bound by the weights' bytes, or by latency where
+// they are few.
+template <int U, int NW, int D, int XK, typename OutT>
+__global__ void __launch_bounds__(64 * NW) fp8_skinny_kernel(MatmulArgs a) {
+  constexpr bool F32SUM = sizeof(OutT) == 4;
+  constexpr int XB = XK == X_CODES ? 1 : XK == X_BF16 ? 2 : 4;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[NW * D * 2048 + 2 * NW * 1024];
+  float* part = reinterpret_cast<float*>(lds + NW * D * 2048);  // [2][NW][16 rows][16 outputs]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, r = lane & 15;
+  const int64_t b = blockIdx.z;
+  const int KB = a.K >> 7, strips = (int)((a.N + 15) >> 4), first = blockIdx.x, step = gridDim.x;
+  const int nu = max(0, (KB - wave + NW - 1) / NW);  // this wave's K steps of a strip
+  const int mine = (strips - first + step - 1) / step;
+  const uint8_t* wbase = a.w + b * a.N * a.K;
+  const float* ws = a.ws + b * ((a.N + 127) >> 7) * KB;
+  uint8_t* ring = lds + wave * (D * 2048);
+  // item (strip i, step u) into ring slot `slot`: row j of the strip at 128 j, its chunks swizzled as in the tile kernel
+  auto load = [&](int i, int u, int slot) __attribute__((always_inline)) {
+    const int64_t n0 = (int64_t)(first + i * step) * 16;
+    const int last = (int)min((int64_t)15, a.N - 1 - n0);  // rows past the end repeat the last one; their results are not stored
+    const auto buf = buffer_of(wbase + n0 * a.K, (uint32_t)(last + 1) * (uint32_t)a.K);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = 8 * j + (lane >> 3);
+      dma16(buf, (uint32_t)min(row, last) * (uint32_t)a.K + 16 * ((lane & 7) ^ (row >> 1)), 128 * (wave + NW * u), ring + 2048 * slot + 1024 * j);
+    }
+  };
+  const int items = mine * nu;
+  int li = 0, lu = 0;  // the next item to load
+  auto load_next = [&](int slot) __attribute__((always_inline)) {
+    // past the end the last item is loaded again, so that every step issues two instructions
+    load(min(li, mine - 1), lu, slot);
+    if (++lu == nu) { lu = 0; ++li; }
+  };
+  intx8 xf[U];
+  float sx[U];
+  if (nu > 0) {
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) load_next(d);
+    const int64_t m = b * a.M + min((int64_t)r, a.M - 1);
+    const uint8_t* xrow = a.x + m * a.K * XB;
+    const float* xsc = a.xs + m * KB;
+    XRaw<XK> xv[2];
+    load_xraw<XK>(xv[0], xrow, xsc, wave, g);
+    if (U > 1) load_xraw<XK>(xv[1], xrow, xsc, min(wave + NW, KB - 1), g);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      xf[u] = quantized_frag<XK>(xv[u & 1], sx[u]);
+      if (u + 2 < U) load_xraw<XK>(xv[u & 1], xrow, xsc, min(wave + NW * (u + 2), KB - 1), g);
+    }
+  }
+  const int frag0 = r * 128 + 16 * (g ^ (r >> 1));
+  int slot = 0;
+  for (int i = 0; i < mine; ++i) {
+    const int64_t n0 = (int64_t)(first + i * step) * 16;
+    floatx4 acc{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (u < nu) {
+        // a scalar load: a vector load would be waited for with all the DMA issued before it
+        const float f = sx[u] * *reinterpret_cast<const __attribute__((address_space(4))) float*>(
+                                    reinterpret_cast<uintptr_t>(ws + ((n0 >> 7) * KB + wave + NW * u)));
+        load_next(slot == 0 ? D - 1 : slot - 1);
+        __builtin_amdgcn_s_waitcnt(vmcnt_only(2 * (D - 1)));  // this item has arrived; the D - 1 later ones may be on their way
+        asm volatile("" ::: "memory");
+        const uint8_t* w = ring + 2048 * slot;
+        const floatx4 p = block_product<F32SUM>(frag_of(ld16(w + frag0), ld16(w + (frag0 ^ 64))), xf[u]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[q] = fmaf(p[q], f, acc[q]);
+        slot = slot == D - 1 ? 0 : slot + 1;
+      }
+    }
+    float* pt = part + (i & 1) * (NW * 256);
+    *reinterpret_cast<floatx4*>(pt + wave * 256 + r * 16 + 4 * (g ^ ((r >> 1) & 3))) = acc;
+    __builtin_amdgcn_s_waitcnt(lgkmcnt0());
+    // one barrier a strip: a wave writes this half of `part` again after the
+    // next strip's barrier, which the readers below reach after reading
+    asm volatile("s_barrier" ::: "memory");
+    if (threadIdx.x < 256) {
+      const int m = threadIdx.x >> 4, n = threadIdx.x & 15;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) v += pt[w * 256 + m * 16 + 4 * ((n >> 2) ^ ((m >> 1) & 3)) + (n & 3)];
+      if (m < a.M && n0 + n < a.N) static_cast<OutT*>(a.y)[(b * a.M + m) * a.N + n0 + n] = out_of<OutT>(v);
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(vmcnt_only(0));  // no DMA outlives the workgroup
+}
+
+// ------------------------------------------------------------ many rows
+
+// Tile of BM rows of x by BN outputs per workgroup of WM x WN waves, each
+// owning 16 MS rows and 16 NS outputs.  Both operands' tiles go through a ring
+// of RING K steps in LDS by 16-byte DMA: eight consecutive lanes copy one
+// row's 128 bytes, where loading MFMA fragments straight into registers would
+// touch four rows in every four lanes (it measured 1.5 to 2 times slower, the
+// more the larger the weights' share).  Chunks are XOR-swizzled by the row so
+// that the 16 rows a fragment read touches hit all banks once.  One barrier a
+// K step.
+constexpr int kTileTab = 24;  // K steps of scales held in LDS at once (even)
+
+template <int WM, int WN, int MS, int NS, int RING>
+struct TileCfg {
+  static constexpr int WAVES = WM * WN, BM = 16 * MS * WM, BN = 16 * NS * WN;
+  static constexpr int STAGE = (BM + BN) * 128;
+  static constexpr int XTAB = RING * STAGE;                    // f32 [kTileTab][BM]
+  static constexpr int WTAB = XTAB + kTileTab * BM * 4;        // f32 [kTileTab][BN / 16]
+  static constexpr int LDS = WTAB + kTileTab * (BN / 16) * 4;
+  static constexpr int ND = (BM + BN) / 8 / WAVES;             // DMA instructions of a wave per K step
+  static_assert((BM / 8) % WAVES == 0 && (BN / 8) % WAVES == 0, "whole DMA instructions per wave");
+  static_assert(LDS <= 160 * 1024, "LDS");
+};
+
+template <int WM, int WN, int MS, int NS, int RING, typename OutT>
+__global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(MatmulArgs a, int mt, int nt) {
+  using C = TileCfg<WM, WN, MS, NS, RING>;
+  constexpr bool F32SUM = sizeof(OutT) == 4;
+  constexpr int TH = 64 * C::WAVES, XD = C::BM / 8 / C::WAVES, WD = C::BN / 8 / C::WAVES;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[C::LDS];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, r = lane & 15;
+  const int wm = wave / WN, wn = wave % WN;
+  // workgroups b, b + 8, ... run on one XCD: give it consecutive tiles (they
+  // share x and W tiles in its L2), in groups of 8 rows of tiles
+  const int tiles = mt * nt, per = (tiles + 7) / 8;
+  const int t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (t >= tiles) return;
+  const int grp = t / (8 * nt), in = t - grp * 8 * nt, rows = min(8, mt - grp * 8);
+  const int64_t m0 = (int64_t)(grp * 8 + in % rows) * C::BM, n0 = (int64_t)(in / rows) * C::BN, b = blockIdx.z;
+  const int K = a.K, KB = K >> 7;
+  const int64_t NB = (a.N + 127) >> 7;
+  const float* xs = a.xs + (b * a.M + m0) * KB;
+  const float* ws = a.ws + b * NB * KB;
+  // rows past the end of an operand repeat its last one; their results are not stored
+  const int mlast = (int)min((int64_t)C::BM - 1, a.M - 1 - m0), nlast = (int)min((int64_t)C::BN - 1, a.N - 1 - n0);
+  const auto xb = buffer_of(a.x + (b * a.M + m0) * K, (uint32_t)(mlast + 1) * (uint32_t)K);
+  const auto wb = buffer_of(a.w + (b * a.N + n0) * K, (uint32_t)(nlast + 1) * (uint32_t)K);
+  uint32_t xoff[XD], woff[WD];
+#pragma unroll
+  for (int j = 0; j < XD; ++j) {
+    const int row = wave * 8 * XD + 8 * j + (lane >> 3);
+    xoff[j] = (uint32_t)min(row, mlast) * (uint32_t)K + 16 * ((lane & 7) ^ ((row >> 1) & 7));
+  }
+#pragma unroll
+  for (int j = 0; j < WD; ++j) {
+    const int row = wave * 8 * WD + 8 * j + (lane >> 3);
+    woff[j] = (uint32_t)min(row, nlast) * (uint32_t)K + 16 * ((lane & 7) ^ ((row >> 1) & 7));
+  }
+  auto load = [&](int kb, int stage) __attribute__((always_inline)) {
+    uint8_t* st = lds + stage * C::STAGE;
+#pragma unroll
+    for (int j = 0; j < XD; ++j) dma16(xb, xoff[j], 128 * kb, st + (wave * XD + j) * 1024);
+#pragma unroll
+    for (int j = 0; j < WD; ++j) dma16(wb, woff[j], 128 * kb, st + C::BM * 128 + (wave * WD + j) * 1024);
+  };
+  float* xtab = reinterpret_cast<float*>(lds + C::XTAB);
+  float* wtab = reinterpret_cast<float*>(lds + C::WTAB);
+  // Scales of the K steps [kb0, kb0 + kTileTab): every thread's loads are
+  // issued together, consecutive threads along a row's K steps.
+  auto fill_tables = [&](int kb0) __attribute__((always_inline)) {
+    const uint32_t n = min(kTileTab, KB - kb0), inv = ((1u << 20) + n - 1) / n;  // i / n = i inv >> 20 for i < 2^13
+    constexpr int XI = (C::BM * kTileTab + TH - 1) / TH, WI = (C::BN / 16 * kTileTab + TH - 1) / TH;
+    float xv[XI], wv[WI];
+#pragma unroll
+    for (int j = 0; j < XI; ++j) {
+      const uint32_t i = min(tid + (uint32_t)TH * j, C::BM * n - 1), m = (i * inv) >> 20, q = i - m * n;
+      xv[j] = xs[(int64_t)min((int)m, mlast) * KB + kb0 + q];
+    }
+#pragma unroll
+    for (int j = 0; j < WI; ++j) {
+      const uint32_t i = min(tid + (uint32_t)TH * j, C::BN / 16 * n - 1), s = (i * inv) >> 20, q = i - s * n;
+      wv[j] = ws[min((n0 + 16 * s) >> 7, NB - 1) * KB + kb0 + q];
+    }
+#pragma unroll
+    for (int j = 0; j < XI; ++j) {  // threads past the end repeat the last entry
+      const uint32_t i = min(tid + (uint32_t)TH * j, C::BM * n - 1), m = (i * inv) >> 20, q = i - m * n;
+      xtab[q * C::BM + m] = xv[j];
+    }
+#pragma unroll
+    for (int j = 0; j < WI; ++j) {
+      const uint32_t i = min(tid + (uint32_t)TH * j, C::BN / 16 * n - 1), s = (i * inv) >> 20, q = i - s * n;
+      wtab[q * (C::BN / 16) + s] = wv[j];
+    }
+  };
+  floatx4 acc[MS][NS];
+#pragma unroll
+  for (int i = 0; i < MS; ++i)
+#pragma unroll
+    for (int s = 0; s < NS; ++s) acc[i][s] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int v = 0; v < RING - 1; ++v) load(min(v, KB - 1), v);
+  // row 16 i + r of a tile: chunks g and 4 + g
+  const int frag0 = r * 128 + 16 * (g ^ (r >> 1));
+  int stage = 0;
+  auto step = [&](int kb, int q) __attribute__((always_inline)) {
+    // this wave's part of step kb has arrived; the RING - 2 later ones may still be on their way
+    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0(C::ND * (RING - 2)));
+    asm volatile("s_barrier" ::: "memory");
+    const uint8_t* xr = lds + stage * C::STAGE + wm * (16 * MS * 128) + frag0;
+    const uint8_t* wr = lds + stage * C::STAGE + C::BM * 128 + wn * (16 * NS * 128);
+    load(min(kb + RING - 1, KB - 1), stage == 0 ? RING - 1 : stage - 1);
+    stage = stage == RING - 1 ? 0 : stage + 1;
+    float sw[NS];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) sw[s] = wtab[q * (C::BN / 16) + wn * NS + s];
+    intx8 wf[NS];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) wf[s] = frag_of(ld16(wr + frag0 + 2048 * s), ld16(wr + (frag0 ^ 64) + 2048 * s));
+    // Software pipeline over the row groups i: while the MFMAs of group i run,
+    // the scaled sums of group i - 1 are added up and group i + 2 is read.
+    intx8 xf[3];
+    float sx[2];
+    floatx4 p[2][NS];
+    auto read_x = [&](int i) __attribute__((always_inline)) {
+      xf[i % 3] = frag_of(ld16(xr + 2048 * i), ld16(xr - frag0 + (frag0 ^ 64) + 2048 * i));
+    };
+    auto add = [&](int i, int s) __attribute__((always_inline)) {
+      const float f = sx[i & 1] * sw[s];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[i][s][c] = fmaf(p[i & 1][s][c], f, acc[i][s][c]);
+    };
+    read_x(0);
+    read_x(1);
+    sx[0] = xtab[q * C::BM + wm * 16 * MS + r];
+    // the order is pinned: left to itself the scheduler moves the reads next
+    // to their uses and the sums next to their MFMAs, and waits for both
+#pragma unroll
+    for (int i = 0; i <= MS; ++i) {
+      if (i + 2 < MS) read_x(i + 2);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (i < MS) p[i & 1][s] = block_product<F32SUM>(wf[s], xf[i % 3]);
+        if (i > 0) add(i - 1, s);
+      }
+      if (i + 1 < MS) sx[(i + 1) & 1] = xtab[q * C::BM + wm * 16 * MS + 16 * (i + 1) + r];
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < MS; ++i)
+#pragma unroll
+      for (int s = 0; s < NS; ++s) asm volatile("" ::"v"(acc[i][s]));
+  };
+  for (int kb0 = 0; kb0 < KB; kb0 += kTileTab) {
+    if (kb0 > 0) asm volatile("s_barrier" ::: "memory");  // every wave is past the tables' last use
+    fill_tables(kb0);
+    const int n = min(kTileTab, KB - kb0);
+    for (int q = 0; q < n; ++q) step(kb0 + q, q);  // the step's barrier follows the table stores
+  }
+  __builtin_amdgcn_s_waitcnt(vmcnt_only(0));  // the last steps' DMA repeats step KB - 1: none outlives the workgroup
+  // The tile is turned in LDS: straight from the accumulators every four lanes
+  // of a store would touch four rows of y (7 of the 22 us of a lone tile's
+  // fixed cost); from LDS consecutive lanes store consecutive 16 bytes.
+  __syncthreads();
+  constexpr int ROW = C::BN * (int)sizeof(OutT) + 16, PV = 16 / (int)sizeof(OutT), PIECES = C::BN / PV;
+  static_assert(C::BM * ROW <= C::LDS, "the output tile fits the ring");
+#pragma unroll
+  for (int i = 0; i < MS; ++i)
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      struct alignas(4 * sizeof(OutT)) V4 { OutT v[4]; } v;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v.v[c] = out_of<OutT>(acc[i][s][c]);
+      *reinterpret_cast<V4*>(lds + (wm * 16 * MS + 16 * i + r) * ROW + (wn * 16 * NS + 16 * s + 4 * g) * (int)sizeof(OutT)) = v;
+    }
+  __syncthreads();
+  OutT* y = static_cast<OutT*>(a.y) + (b * a.M + m0) * a.N + n0;
+  const bool vec = a.N % PV == 0 && (uintptr_t)a.y % 16 == 0;  // rows of y in whole 16-byte pieces
+#pragma unroll 4
+  for (int q = tid; q < C::BM * PIECES; q += TH) {
+    const int m = q / PIECES, n = (q % PIECES) * PV;
+    if (m > mlast || n > nlast) continue;
+    const u32x4 v = ld16(lds + m * ROW + n * (int)sizeof(OutT));
+    if (vec) {
+      st16(y + (int64_t)m * a.N + n, v);
+    } else {
+#pragma unroll
+      for (int c = 0; c < PV; ++c) {
+        OutT o;
+        if constexpr (sizeof(OutT) == 2) o = (OutT)(v[c >> 1] >> (16 * (c & 1)));
+        else o = __uint_as_float(v[c]);
+        if (n + c <= nlast) y[(int64_t)m * a.N + n + c] = o;
+      }
+    }
+  }
+}
+
+template <int WM, int WN, int MS, int NS, int RING, typename OutT>
+static int launch_tile(const MatmulArgs& a, int64_t batch, hipStream_t st) {
+  using C = TileCfg<WM, WN, MS, NS, RING>;
+  const int64_t mt = (a.M + C::BM - 1) / C::BM, nt = (a.N + C::BN - 1) / C::BN;
+  const int64_t grid = (mt * nt + 7) / 8 * 8;
+  if (grid > INT32_MAX / 8 || batch > 65535) return fail(FP4_ERR_UNSUPPORTED, "matmul: too many rows, outputs or matrices");
+  hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, MS, NS, RING, OutT>), dim3((unsigned)grid, 1, (unsigned)batch), dim3(64 * C::WAVES), 0, st,
+                     a, (int)mt, (int)nt);
   return check_launch("fp8_block_matmul");
+}
+
+template <int U, int NW, int D, int XK, typename OutT>
+static int launch_skinny(const MatmulArgs& a, int64_t batch, hipStream_t st) {
+  const int64_t strips = (a.N + 15) / 16, wgs = std::max<int64_t>(1, 2 * device_cu_count() / batch);
+  if (batch > 65535) return fail(FP4_ERR_UNSUPPORTED, "matmul: too many matrices");
+  hipLaunchKernelGGL((fp8_skinny_kernel<U, NW, D, XK, OutT>), dim3((unsigned)std::min(strips, wgs), 1, (unsigned)batch), dim3(64 * NW), 0, st, a);
+  return check_launch("fp8_block_matmul");
+}
+
+constexpr int kSkinnyMaxK = 8 * 8 * 128;  // 8 K steps for each of 8 waves
+template <int XK, typename OutT>
+static int launch_skinny_k(const MatmulArgs& a, int64_t batch, hipStream_t st) {
+  const int kb = a.K / 128;
+  if (kb <= 8) return launch_skinny<1, 8, 4, XK, OutT>(a, batch, st);
+  if (kb <= 16) return launch_skinny<2, 8, 4, XK, OutT>(a, batch, st);
+  if (kb <= 24) return launch_skinny<3, 8, 4, XK, OutT>(a, batch, st);
+  if (kb <= 40) return launch_skinny<5, 8, 4, XK, OutT>(a, batch, st);
+  return launch_skinny<8, 8, 4, XK, OutT>(a, batch, st);
+}
+
+// One variant's modelled time: rounds of `slots` tiles at full load, and a last
+// partial round between a lone tile's time and a full round's (microseconds).
+struct TileModel {
+  int bm, bn, slots_per_cu;
+  double fixed, lone, loaded;  // per K step
+  double time(const MatmulArgs& a, int64_t batch) const {
+    const double tiles = (double)((a.M + bm - 1) / bm) * (double)((a.N + bn - 1) / bn) * (double)batch, slots = (double)slots_per_cu * device_cu_count();
+    const double kb = a.K / 128, full = fixed + loaded * kb, one = fixed + lone * kb;
+    const double rounds = std::floor(tiles / slots), rest = tiles - rounds * slots;
+    return rounds * full + (rest > 0 ? one + (full - one) * rest / slots : 0.0);
+  }
+};
+
+// The tile whose modelled time is the least.  The constants are this card's,
+// fitted at K = 2560: a tile alone / a full round (us) 8.8 / 19.8 (64 x 64),
+// 16 / 28 (128 x 128), 27 / 36 (192 x 256), 34 / 46 (256 x 256).  Measured (us),
+// in that order: 1024 x 2560 15.4, 17.6, 28.8, 35.7; 8192 x 2560 98.8, 73.9, 68.4,
+// 78.6; 8192 x 10240 (128 up) 268, 247, 230.  f32 results take the fp16 MFMA, whose
+// converted operands leave registers for 64 x 64 and 128 x 128 only.
+constexpr TileModel kTile64{64, 64, 4, 2.0, 0.34, 0.89}, kTile128{128, 128, 2, 4.0, 0.60, 1.20}, kTile192{192, 256, 1, 4.4, 1.15, 1.58},
+    kTile256{256, 256, 1, 5.0, 1.45, 2.05};
+
+template <typename OutT>
+static int launch_tiles(const MatmulArgs& a, int64_t batch, hipStream_t st) {
+  const double t64 = kTile64.time(a, batch), t128 = kTile128.time(a, batch);
+  if constexpr (sizeof(OutT) == 2) {
+    const double t192 = kTile192.time(a, batch), t256 = kTile256.time(a, batch);
+    if (t256 <= std::min(t192, std::min(t64, t128))) return launch_tile<2, 4, 8, 4, 2, OutT>(a, batch, st);
+    if (t192 <= std::min(t64, t128)) return launch_tile<2, 4, 6, 4, 2, OutT>(a, batch, st);
+  }
+  return t64 <= t128 ? launch_tile<2, 2, 2, 2, 2, OutT>(a, batch, st) : launch_tile<2, 2, 4, 4, 2, OutT>(a, batch, st);
+}
+
+constexpr int64_t kFewRows = 16;
+
+// bf16 / f32 x that the few-rows kernel quantizes by itself (one launch, no workspace)
+static bool quantized_inside(int x_dtype, int64_t m, int64_t k) {
+  return x_dtype != FP4_DT_E4M3 && m <= kFewRows && k <= kSkinnyMaxK;
+}
+
+template <typename OutT>
+static int launch_matmul(const MatmulArgs& a, int xk, int64_t batch, hipStream_t st) {
+  if (xk == X_BF16) return launch_skinny_k<X_BF16, OutT>(a, batch, st);
+  if (xk == X_F32) return launch_skinny_k<X_F32, OutT>(a, batch, st);
+  if (a.M <= kFewRows && a.K <= kSkinnyMaxK) return launch_skinny_k<X_CODES, OutT>(a, batch, st);
+  return launch_tiles<OutT>(a, batch, st);
 }
 
 static size_t codes_bytes(int64_t batch, int64_t m, int64_t k) { return ((size_t)(batch * m * k) + 255) / 256 * 256; }
@@ -177,6 +572,7 @@ static int validate_matmul(int x_dtype, int64_t batch, int64_t m, int64_t n, int
   const int64_t most = (int64_t)1 << 31;
   if (batch >= most || m >= most || n >= most || k >= most)
     return fail(FP4_ERR_UNSUPPORTED, "matmul: a dimension of 2^31 or more");
+  if (k > (int64_t)1 << 22) return fail(FP4_ERR_UNSUPPORTED, "matmul: k beyond 2^22");  // 32-bit offsets inside a tile of 256 rows
   const double elems = 0x1p48;  // byte offsets stay far inside 64 bits
   if ((double)batch * m * k > elems || (double)batch * n * k > elems || (double)batch * m * n > elems)
     return fail(FP4_ERR_UNSUPPORTED, "matmul: an operand of more than 2^48 values");
@@ -192,7 +588,7 @@ extern "C" {
 int fp8_block_matmul_workspace_size(int x_dtype, int64_t batch, int64_t m, int64_t n, int64_t k, size_t* bytes) {
   if (!bytes) return fail(FP4_ERR_INVALID_ARG, "null size pointer");
   FP4_CHECK(validate_matmul(x_dtype, batch, m, n, k));
-  *bytes = x_dtype == FP4_DT_E4M3 ? 0 : codes_bytes(batch, m, k) + sizeof(float) * (size_t)(batch * m * (k / 128));
+  *bytes = x_dtype == FP4_DT_E4M3 || quantized_inside(x_dtype, m, k) ? 0 : codes_bytes(batch, m, k) + sizeof(float) * (size_t)(batch * m * (k / 128));
   return FP4_OK;
 }
 
@@ -211,7 +607,10 @@ int fp8_block_matmul(const void* x, int x_dtype, const float* x_scales, const ui
     return fail(FP4_ERR_INVALID_ARG, "matmul: misaligned pointer");
   hipStream_t st = as_stream(stream);
   MatmulArgs a{static_cast<const uint8_t*>(x), x_scales, w, w_scales, y, m, n, (int)k};
-  if (x_dtype != FP4_DT_E4M3) {
+  int xk = X_CODES;
+  if (quantized_inside(x_dtype, m, k)) {
+    xk = x_dtype == FP4_DT_BF16 ? X_BF16 : X_F32;
+  } else if (x_dtype != FP4_DT_E4M3) {
     if (!workspace || workspace_bytes < need)
       return fail(FP4_ERR_WORKSPACE, "matmul: workspace of %zu bytes, %zu needed", workspace_bytes, need);
     if ((uintptr_t)workspace % 16) return fail(FP4_ERR_INVALID_ARG, "matmul: misaligned workspace");
@@ -221,7 +620,7 @@ int fp8_block_matmul(const void* x, int x_dtype, const float* x_scales, const ui
     a.x = codes;
     a.xs = scales;
   }
-  return y_dtype == FP4_DT_BF16 ? launch_matmul<uint16_t>(a, batch, st) : launch_matmul<float>(a, batch, st);
+  return y_dtype == FP4_DT_BF16 ? launch_matmul<uint16_t>(a, xk, batch, st) : launch_matmul<float>(a, xk, batch, st);
 }
 
 }  // extern "C"

@@ -49,6 +49,7 @@ __device__ __forceinline__ float dot2_bf16(uint32_t a, uint32_t b, float c) {
 // 6:4, lgkmcnt 11:8): vmcnt <= n only, and vmcnt <= n with lgkmcnt = 0.
 constexpr int vmcnt_only(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
 constexpr int vmcnt_lgkm0(int n) { return (n & 15) | (7 << 4) | ((n >> 4) << 14); }
+constexpr int lgkmcnt0() { return 15 | (7 << 4) | (3 << 14); }  // lgkmcnt = 0 only
 
 // SiLU(g) = g / (1 + e^-g), as g times the hardware reciprocal (about 1 ulp)
 // of 1 + e^-g: two VALU instructions where the IEEE divide takes about ten,

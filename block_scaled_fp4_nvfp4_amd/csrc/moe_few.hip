@@ -417,7 +417,7 @@ __device__ __forceinline__ void gu_reduce(floatx4& a, floatx4& b, float* red, in
 }
 
 template <int MODE>
-__global__ void __launch_bounds__(64 * kGuWaves) few_gateup_kernel(FewArgs a) {
+__global__ void __launch_bounds__(64 * kGuWaves, 4) few_gateup_kernel(FewArgs a) {
   constexpr int WF = weight_fmt(MODE), AF = act_fmt(MODE);
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ float tmp[kGuWaves];

@@ -39,15 +39,14 @@ def test_workspace(L):
     sz = ctypes.c_size_t()
     size = L.fp8_block_matmul_workspace_size
     assert size(2, 1, 4, 128, 256, ctypes.byref(sz)) == 0 and sz.value == 0
-    assert size(0, 3, 5, 128, 256, ctypes.byref(sz)) == 0 and sz.value >= 3 * 5 * (256 + 4 * 2)
-    need = sz.value
+    assert size(0, 3, 70, 128, 256, ctypes.byref(sz)) == 0 and sz.value >= 3 * 70 * (256 + 4 * 2)
+    assert size(0, 3, 5, 128, 256, ctypes.byref(sz)) == 0 and sz.value == 0  # few rows are quantized inside the product
     assert size(0, 1, 4, 128, 256, None) == -1
     # a workspace that is missing, too small or misaligned is refused before any launch; 33 rows take one
     assert size(0, 1, 33, 128, 256, ctypes.byref(sz)) == 0
     assert _call(L, xd=0, m=33) == -4
     assert _call(L, xd=1, m=33, wk=FAKE, wb=sz.value - 1) == -4
     assert _call(L, xd=0, m=33, wk=ODD, wb=1 << 20) == -1
-    assert need > 0
 
 
 def test_empty_is_a_no_op(L):
