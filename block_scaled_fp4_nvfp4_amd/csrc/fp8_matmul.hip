@@ -97,98 +97,112 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* p, ui
 // values that each wave quantizes for its own K steps.
 enum XKind { X_CODES = 0, X_BF16 = 1, X_F32 = 2 };
 
-template <int XK>
-struct XRaw {
-  u32x4 v[XK == X_CODES ? 2 : XK == X_BF16 ? 4 : 8];  // chunks g, then 4 + g, of 16 values each
-  float s;
-};
-
-template <int XK>
-__device__ __forceinline__ void load_xraw(XRaw<XK>& x, const uint8_t* row, const float* srow, int kb, int g) {
-  if constexpr (XK == X_CODES) {
-    x.v[0] = ld16(row + 128 * kb + 16 * g);
-    x.v[1] = ld16(row + 128 * kb + 16 * g + 64);
-    x.s = srow[kb];
-  } else {
-    constexpr int B = XK == X_BF16 ? 2 : 4;
-    const uint8_t* p = row + (int64_t)(128 * kb + 16 * g) * B;
+// N values (a multiple of 2) to E4M3 codes of v / sigma in d, bit for bit
+// those of fp4_quantize.  With q2 = fp32 within an ulp of the quotient and the
+// exact sign of its remainder, the quotient rounded to odd (the last bit set
+// where the remainder is not zero) rounds on to E4M3 as the exact quotient
+// does: ties, which bf16 values hit all the time, need no branch.  Both are
+// scaled by the power of two that brings sigma into [0.5, 1), so that the
+// remainder of every quotient above E4M3's smallest midpoint is exact.
+template <int N>
+__device__ __forceinline__ void e4m3_codes(const float (&v)[N], float sigma, uint32_t (&d)[(N + 3) / 4]) {
+  const int e = -__builtin_amdgcn_frexp_expf(sigma);
+  const float s = ldexpf(sigma, e), inv = sigma > 0.0f ? 1.0f / s : 0.0f;
 #pragma unroll
-    for (int i = 0; i < B; ++i) {
-      x.v[i] = ld16(p + 16 * i);
-      x.v[B + i] = ld16(p + 64 * B + 16 * i);
+  for (int w = 0; w < (N + 3) / 4; ++w) d[w] = 0;
+#pragma unroll
+  for (int w = 0; w < N / 2; ++w) {
+    float q[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float a = ldexpf(fabsf(v[2 * w + j]), e), q1 = a * inv, q2 = fmaf(fmaf(-q1, s, a), inv, q1), rem = fmaf(-q2, s, a);
+      const uint32_t odd = (__float_as_uint(q2) - (uint32_t)(rem < 0.0f)) | (uint32_t)(rem != 0.0f);
+      q[j] = copysignf(__uint_as_float(odd), v[2 * w + j]);
     }
+    d[w >> 1] = (uint32_t)((w & 1) ? __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], (int)d[w >> 1], true)
+                                   : __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], (int)d[w >> 1], false));
   }
 }
 
-// The E4M3 fragment of a lane's 32 values of one 128-block, whose four lanes
-// are r, r + 16, r + 32, r + 48, to the codes of fp4_quantize: sigma =
-// fp32(amax / 448), code = E4M3 nearest to v / sigma.  q = v * fp32(1 / sigma)
-// is within 1.5 ulp of the quotient and rounds to the same code unless an
-// E4M3 midpoint (f32 pattern ..80000h in the low 20 bits) lies within 2 ulp
-// of it; those, and the subnormal range, take the exact path, per wave.
-template <int XK>
-__device__ __forceinline__ intx8 quantized_frag(const XRaw<XK>& x, float& sigma) {
-  if constexpr (XK == X_CODES) {
-    sigma = x.s;
-    return frag_of(x.v[0], x.v[1]);
+// V bf16 / f32 values from p (2 bf16 of 4 bytes upwards).
+template <int XK, int V>
+__device__ __forceinline__ void load_values(const uint8_t* p, float (&v)[V]) {
+  constexpr int W = V * (XK == X_BF16 ? 2 : 4) / 4;
+  uint32_t d[W];
+  if constexpr (W == 1) {
+    d[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (W == 2) {
+    const u32x2 t = *reinterpret_cast<const u32x2*>(p);
+    d[0] = t.x;
+    d[1] = t.y;
   } else {
-    float v[32];
-    if constexpr (XK == X_BF16) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        v[2 * i] = __uint_as_float(x.v[i >> 2][i & 3] << 16);
-        v[2 * i + 1] = __uint_as_float(x.v[i >> 2][i & 3] & 0xFFFF0000u);
-      }
-    } else {
+    for (int i = 0; i < W / 4; ++i) {
+      const u32x4 t = ld16(p + 16 * i);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(x.v[i >> 2][i & 3]);
+      for (int j = 0; j < 4; ++j) d[4 * i + j] = t[j];
     }
-    float amax = 0.0f;
+  }
 #pragma unroll
-    for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(v[i]));
-    amax = fmaxf(amax, __shfl_xor(amax, 16));
-    amax = fmaxf(amax, __shfl_xor(amax, 32));
-    sigma = (float)((double)amax / 448.0);
-    const float inv = sigma > 0.0f ? 1.0f / sigma : 0.0f;
-    uint32_t near_mid = 0xFFFFFFFFu, small = 0xFFFFFFFFu;
-    int d[8];
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      float q[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        q[j] = v[4 * w + j] * inv;
-        const uint32_t bits = __float_as_uint(q[j]);
-        near_mid = min(near_mid, (bits << 12) + 0x80002000u);  // 0 .. 4 ulp (of 4096) around a midpoint
-        small = min(small, (bits & 0x7FFFFFFFu) - 1u);         // zero wraps to the largest
-      }
-      d[w] = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-      d[w] = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], d[w], true);
-    }
-    // 1 / sigma that is not a normal number (rows below 2^-117 or above 2^126) is no use either
-    const bool odd = near_mid <= 0x4000u || small < 0x3C800000u - 1u || !(inv > 0x1p-125f && inv < 0x1p125f);
-    if (odd) {
-      const float sg = sigma > 0.0f ? sigma : 1.0f;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        uint32_t t = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {  // e4m3_exact_quotient without its branches
-          const float e = v[4 * w + j], m = fabsf(e), q = fminf(m / sg, kE4M3Max);
-          uint32_t c = e4m3_hw(q);
-          const double A = (double)m, M = (double)q * (double)sg;
-          const float vc = __builtin_amdgcn_cvt_f32_fp8((int)c, 0);
-          const bool mid = e4m3_is_midpoint(q);
-          c += (uint32_t)(mid & (A > M) & (vc < q)) - (uint32_t)(mid & (A < M) & (vc > q));
-          t |= ((sigma > 0.0f ? c : 0u) | ((__float_as_uint(e) >> 24) & 0x80u)) << (8 * j);
-        }
-        d[w] = (int)t;
-      }
-    }
-    return intx8{d[0], d[1], d[2], d[3], d[4], d[5], d[6], d[7]};
+  for (int i = 0; i < V; ++i) {
+    if constexpr (XK == X_BF16) v[i] = __uint_as_float((i & 1) ? d[i >> 1] & 0xFFFF0000u : d[i >> 1] << 16);
+    else v[i] = __uint_as_float(d[i]);
   }
 }
 
+// x [blocks, 128] to codes and one scale a block, 8 lanes of 16 values each
+// per block (fp4_quantize's row kernel, with 4 lanes and IEEE divisions, takes
+// 20 us for 8192 x 2560 bf16 and 8 us for 77 rows; this one 9 and 5).
+template <int XK>
+__global__ void __launch_bounds__(256) fp8_rows_kernel(const uint8_t* __restrict__ x, int64_t blocks, uint8_t* __restrict__ codes,
+                                                       float* __restrict__ scales) {
+  constexpr int XB = XK == X_BF16 ? 2 : 4;
+  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if ((t >> 3) >= blocks) return;  // whole groups of 8 lanes
+  float v[16];
+  load_values<XK, 16>(x + t * 16 * XB, v);
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
+  const float sigma = (float)((double)amax / 448.0);
+  uint32_t d[4];
+  e4m3_codes<16>(v, sigma, d);
+  st16(codes + t * 16, u32x4{d[0], d[1], d[2], d[3]});
+  if ((t & 7) == 0) scales[t >> 3] = sigma;
+}
+
+// One wave quantizes its 128-block kb of P rows of x: 64 / P lanes a row, 2 P
+// values a lane, so that the work follows the rows there are.  The codes pass
+// through `stage` (2 KB of LDS of the wave) into the MFMA fragment; lane (g,
+// r) gets row r mod P and its scale.
+template <int XK, int P>
+__device__ __forceinline__ intx8 quantized_frag(const uint8_t* x, int64_t row_bytes, int64_t M, int kb, uint8_t* stage, float& scale) {
+  constexpr int V = 2 * P, LPR = 64 / P, XB = XK == X_BF16 ? 2 : 4;
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15, row = lane / LPR, at = (lane % LPR) * V;
+  float v[V];
+  load_values<XK, V>(x + min((int64_t)row, M - 1) * row_bytes + (int64_t)(128 * kb + at) * XB, v);
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) amax = fmaxf(amax, fabsf(v[i]));
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
+  const float sigma = (float)((double)amax / 448.0);
+  uint32_t d[(V + 3) / 4];
+  e4m3_codes<V>(v, sigma, d);
+  uint8_t* to = stage + row * 128 + 16 * ((at >> 4) ^ (row >> 1)) + (at & 15);
+  if constexpr (V == 2) *reinterpret_cast<uint16_t*>(to) = (uint16_t)d[0];
+  else if constexpr (V == 8) *reinterpret_cast<u32x2*>(to) = u32x2{d[0], d[1]};
+  else {
+    st16(to, u32x4{d[0], d[1], d[2], d[3]});
+    st16(stage + row * 128 + 16 * (((at >> 4) + 1) ^ (row >> 1)), u32x4{d[4], d[5], d[6], d[7]});
+  }
+  const int rr = r % P;
+  scale = __shfl(sigma, rr * LPR);
+  const uint8_t* from = stage + rr * 128 + 16 * (g ^ (rr >> 1));
+  return frag_of(ld16(from), ld16(stage + rr * 128 + 16 * ((4 + g) ^ (rr >> 1))));
+}
 
 // At most 16 rows of x: a workgroup of NW waves walks over strips of 16
 // outputs; wave w takes the 128-blocks w, w + NW, ... of K (U at most) of every
@@ -197,15 +211,16 @@ __device__ __forceinline__ intx8 quantized_frag(const XRaw<XK>& x, float& sigma)
 // ring of D steps in LDS that belongs to the wave alone (16 rows x 128 bytes
 // a step, by DMA, several strips ahead and without barriers: loading fragments
 // straight into registers touches four rows in every four lanes, which
-// measured 10.4 us against HERE us at 16 x 10240 x 2560).  A strip's partial sums meet in
+// measured 10.4 us against 7.5 at 16 x 10240 x 2560).  A strip's partial sums meet in
 // LDS, one barrier a strip.  Bound by the weights' bytes, or by latency where
 // they are few.
-template <int U, int NW, int D, int XK, typename OutT>
+template <int U, int NW, int D, int XK, int P, typename OutT>
 __global__ void __launch_bounds__(64 * NW) fp8_skinny_kernel(MatmulArgs a) {
   constexpr bool F32SUM = sizeof(OutT) == 4;
   constexpr int XB = XK == X_CODES ? 1 : XK == X_BF16 ? 2 : 4;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[NW * D * 2048 + 2 * NW * 1024];
-  float* part = reinterpret_cast<float*>(lds + NW * D * 2048);  // [2][NW][16 rows][16 outputs]
+  constexpr int STAGED = XK == X_CODES ? 0 : 2048;  // a wave's staging of quantized x
+  __shared__ __attribute__((aligned(16))) uint8_t lds[NW * (D * 2048 + STAGED) + 2 * NW * 1024];
+  float* part = reinterpret_cast<float*>(lds + NW * (D * 2048 + STAGED));  // [2][NW][16 rows][16 outputs]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, r = lane & 15;
   const int64_t b = blockIdx.z;
   const int KB = a.K >> 7, strips = (int)((a.N + 15) >> 4), first = blockIdx.x, step = gridDim.x;
@@ -213,7 +228,7 @@ __global__ void __launch_bounds__(64 * NW) fp8_skinny_kernel(MatmulArgs a) {
   const int mine = (strips - first + step - 1) / step;
   const uint8_t* wbase = a.w + b * a.N * a.K;
   const float* ws = a.ws + b * ((a.N + 127) >> 7) * KB;
-  uint8_t* ring = lds + wave * (D * 2048);
+  uint8_t* ring = lds + wave * (D * 2048 + STAGED);
   // item (strip i, step u) into ring slot `slot`: row j of the strip at 128 j, its chunks swizzled as in the tile kernel
   auto load = [&](int i, int u, int slot) __attribute__((always_inline)) {
     const int64_t n0 = (int64_t)(first + i * step) * 16;
@@ -237,16 +252,20 @@ __global__ void __launch_bounds__(64 * NW) fp8_skinny_kernel(MatmulArgs a) {
   if (nu > 0) {
 #pragma unroll
     for (int d = 0; d < D - 1; ++d) load_next(d);
-    const int64_t m = b * a.M + min((int64_t)r, a.M - 1);
-    const uint8_t* xrow = a.x + m * a.K * XB;
-    const float* xsc = a.xs + m * KB;
-    XRaw<XK> xv[2];
-    load_xraw<XK>(xv[0], xrow, xsc, wave, g);
-    if (U > 1) load_xraw<XK>(xv[1], xrow, xsc, min(wave + NW, KB - 1), g);
+    if constexpr (XK == X_CODES) {
+      const int64_t m = b * a.M + min((int64_t)r, a.M - 1);
+      const uint8_t* xrow = a.x + m * a.K + 16 * g;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      xf[u] = quantized_frag<XK>(xv[u & 1], sx[u]);
-      if (u + 2 < U) load_xraw<XK>(xv[u & 1], xrow, xsc, min(wave + NW * (u + 2), KB - 1), g);
+      for (int u = 0; u < U; ++u) {
+        const int kb = min(wave + NW * u, KB - 1);
+        xf[u] = frag_of(ld16(xrow + 128 * kb), ld16(xrow + 128 * kb + 64));
+        sx[u] = a.xs[m * KB + kb];
+      }
+    } else {
+      const int64_t row_bytes = (int64_t)a.K * XB;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u < nu) xf[u] = quantized_frag<XK, P>(a.x + b * a.M * row_bytes, row_bytes, a.M, wave + NW * u, ring + D * 2048, sx[u]);
     }
   }
   const int frag0 = r * 128 + 16 * (g ^ (r >> 1));
@@ -495,23 +514,29 @@ static int launch_tile(const MatmulArgs& a, int64_t batch, hipStream_t st) {
   return check_launch("fp8_block_matmul");
 }
 
-template <int U, int NW, int D, int XK, typename OutT>
+template <int U, int NW, int D, int XK, int P, typename OutT>
 static int launch_skinny(const MatmulArgs& a, int64_t batch, hipStream_t st) {
   const int64_t strips = (a.N + 15) / 16, wgs = std::max<int64_t>(1, 2 * device_cu_count() / batch);
   if (batch > 65535) return fail(FP4_ERR_UNSUPPORTED, "matmul: too many matrices");
-  hipLaunchKernelGGL((fp8_skinny_kernel<U, NW, D, XK, OutT>), dim3((unsigned)std::min(strips, wgs), 1, (unsigned)batch), dim3(64 * NW), 0, st, a);
+  hipLaunchKernelGGL((fp8_skinny_kernel<U, NW, D, XK, P, OutT>), dim3((unsigned)std::min(strips, wgs), 1, (unsigned)batch), dim3(64 * NW), 0, st, a);
   return check_launch("fp8_block_matmul");
 }
 
 constexpr int kSkinnyMaxK = 8 * 8 * 128;  // 8 K steps for each of 8 waves
-template <int XK, typename OutT>
+template <int XK, int P, typename OutT>
 static int launch_skinny_k(const MatmulArgs& a, int64_t batch, hipStream_t st) {
+  constexpr int D = XK == X_CODES ? 4 : 3;  // with the staging of x, two workgroups share a CU's LDS either way
   const int kb = a.K / 128;
-  if (kb <= 8) return launch_skinny<1, 8, 4, XK, OutT>(a, batch, st);
-  if (kb <= 16) return launch_skinny<2, 8, 4, XK, OutT>(a, batch, st);
-  if (kb <= 24) return launch_skinny<3, 8, 4, XK, OutT>(a, batch, st);
-  if (kb <= 40) return launch_skinny<5, 8, 4, XK, OutT>(a, batch, st);
-  return launch_skinny<8, 8, 4, XK, OutT>(a, batch, st);
+  if (kb <= 8) return launch_skinny<1, 8, D, XK, P, OutT>(a, batch, st);
+  if (kb <= 24) return launch_skinny<3, 8, D, XK, P, OutT>(a, batch, st);
+  return launch_skinny<8, 8, D, XK, P, OutT>(a, batch, st);
+}
+
+template <int XK, typename OutT>
+static int launch_skinny_rows(const MatmulArgs& a, int64_t batch, hipStream_t st) {
+  if (a.M == 1) return launch_skinny_k<XK, 1, OutT>(a, batch, st);
+  if (a.M <= 4) return launch_skinny_k<XK, 4, OutT>(a, batch, st);
+  return launch_skinny_k<XK, 16, OutT>(a, batch, st);
 }
 
 // One variant's modelled time: rounds of `slots` tiles at full load, and a last
@@ -556,9 +581,9 @@ static bool quantized_inside(int x_dtype, int64_t m, int64_t k) {
 
 template <typename OutT>
 static int launch_matmul(const MatmulArgs& a, int xk, int64_t batch, hipStream_t st) {
-  if (xk == X_BF16) return launch_skinny_k<X_BF16, OutT>(a, batch, st);
-  if (xk == X_F32) return launch_skinny_k<X_F32, OutT>(a, batch, st);
-  if (a.M <= kFewRows && a.K <= kSkinnyMaxK) return launch_skinny_k<X_CODES, OutT>(a, batch, st);
+  if (xk == X_BF16) return launch_skinny_rows<X_BF16, OutT>(a, batch, st);
+  if (xk == X_F32) return launch_skinny_rows<X_F32, OutT>(a, batch, st);
+  if (a.M <= kFewRows && a.K <= kSkinnyMaxK) return launch_skinny_k<X_CODES, 16, OutT>(a, batch, st);
   return launch_tiles<OutT>(a, batch, st);
 }
 
@@ -616,7 +641,13 @@ int fp8_block_matmul(const void* x, int x_dtype, const float* x_scales, const ui
     if ((uintptr_t)workspace % 16) return fail(FP4_ERR_INVALID_ARG, "matmul: misaligned workspace");
     uint8_t* codes = static_cast<uint8_t*>(workspace);
     float* scales = reinterpret_cast<float*>(codes + codes_bytes(batch, m, k));
-    FP4_CHECK(fp4_quantize(FP4_FMT_FP8_ROW, 0, 0, x, x_dtype, 1, batch * m, k, codes, scales, nullptr, nullptr, stream));
+    const int64_t blocks = batch * m * (k / 128), wgs = (blocks * 8 + 255) / 256;
+    if (wgs > INT32_MAX) return fail(FP4_ERR_UNSUPPORTED, "matmul: too many rows");
+    if (x_dtype == FP4_DT_BF16)
+      hipLaunchKernelGGL(fp8_rows_kernel<X_BF16>, dim3((unsigned)wgs), dim3(256), 0, st, static_cast<const uint8_t*>(x), blocks, codes, scales);
+    else
+      hipLaunchKernelGGL(fp8_rows_kernel<X_F32>, dim3((unsigned)wgs), dim3(256), 0, st, static_cast<const uint8_t*>(x), blocks, codes, scales);
+    FP4_CHECK(check_launch("fp8_rows"));
     a.x = codes;
     a.xs = scales;
   }
