@@ -80,17 +80,6 @@ __device__ __forceinline__ uint16_t out_of<uint16_t>(float v) {
   return __builtin_bit_cast(uint16_t, (__bf16)v);  // to nearest even, NaN kept
 }
 
-// 16-byte DMA from a buffer (its descriptor, the lane's and the wave's byte
-// offsets) to lds + 16 lane.  The buffer form rather than the global one: the
-// compiler counts a global load to LDS as an access to both memories and makes
-// every later LDS read wait for all that were issued before it.
-__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t src, uint32_t lane_off, uint32_t wave_off, void* lds) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)lds, 16, (int)lane_off, (int)wave_off, 0, 0);
-}
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, (int)bytes, 0x00027000);  // raw dwords, bounds-checked
-}
-
 // ------------------------------------------------------------ few rows
 
 // x as the few-rows kernel reads it: codes with their scales, or bf16 / f32
@@ -237,7 +226,7 @@ __global__ void __launch_bounds__(64 * NW) fp8_skinny_kernel(MatmulArgs a) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int row = 8 * j + (lane >> 3);
-      dma16(buf, (uint32_t)min(row, last) * (uint32_t)a.K + 16 * ((lane & 7) ^ (row >> 1)), 128 * (wave + NW * u), ring + 2048 * slot + 1024 * j);
+      dma_buffer(buf, (uint32_t)min(row, last) * (uint32_t)a.K + 16 * ((lane & 7) ^ (row >> 1)), 128 * (wave + NW * u), ring + 2048 * slot + 1024 * j);
     }
   };
   const int items = mine * nu;
@@ -276,9 +265,7 @@ __global__ void __launch_bounds__(64 * NW) fp8_skinny_kernel(MatmulArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (u < nu) {
-        // a scalar load: a vector load would be waited for with all the DMA issued before it
-        const float f = sx[u] * *reinterpret_cast<const __attribute__((address_space(4))) float*>(
-                                    reinterpret_cast<uintptr_t>(ws + ((n0 >> 7) * KB + wave + NW * u)));
+        const float f = sx[u] * scalar_load(ws + ((n0 >> 7) * KB + wave + NW * u));
         load_next(slot == 0 ? D - 1 : slot - 1);
         __builtin_amdgcn_s_waitcnt(vmcnt_only(2 * (D - 1)));  // this item has arrived; the D - 1 later ones may be on their way
         asm volatile("" ::: "memory");
@@ -367,9 +354,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(MatmulArgs a,
   auto load = [&](int kb, int stage) __attribute__((always_inline)) {
     uint8_t* st = lds + stage * C::STAGE;
 #pragma unroll
-    for (int j = 0; j < XD; ++j) dma16(xb, xoff[j], 128 * kb, st + (wave * XD + j) * 1024);
+    for (int j = 0; j < XD; ++j) dma_buffer(xb, xoff[j], 128 * kb, st + (wave * XD + j) * 1024);
 #pragma unroll
-    for (int j = 0; j < WD; ++j) dma16(wb, woff[j], 128 * kb, st + C::BM * 128 + (wave * WD + j) * 1024);
+    for (int j = 0; j < WD; ++j) dma_buffer(wb, woff[j], 128 * kb, st + C::BM * 128 + (wave * WD + j) * 1024);
   };
   float* xtab = reinterpret_cast<float*>(lds + C::XTAB);
   float* wtab = reinterpret_cast<float*>(lds + C::WTAB);

@@ -51,10 +51,30 @@ constexpr int vmcnt_only(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >
 constexpr int vmcnt_lgkm0(int n) { return (n & 15) | (7 << 4) | ((n >> 4) << 14); }
 constexpr int lgkmcnt0() { return 15 | (7 << 4) | (3 << 14); }  // lgkmcnt = 0 only
 
+// DMA of 16 (4) bytes a lane from a buffer (its descriptor, the lane's and the
+// wave's byte offsets) to lds + 16 (4) lane.  The buffer form rather than the
+// global one: the compiler counts a global load to LDS as an access to both
+// memories and makes every later LDS read wait for all that were issued before.
+__device__ __forceinline__ void dma_buffer(__amdgpu_buffer_rsrc_t src, uint32_t lane_off, uint32_t wave_off, void* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)lds, 16, (int)lane_off, (int)wave_off, 0, 0);
+}
+__device__ __forceinline__ void dma_buffer4(__amdgpu_buffer_rsrc_t src, uint32_t lane_off, uint32_t wave_off, void* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)lds, 4, (int)lane_off, (int)wave_off, 0, 0);
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);  // raw dwords, bounds-checked
+}
+
 // SiLU(g) = g / (1 + e^-g), as g times the hardware reciprocal (about 1 ulp)
 // of 1 + e^-g: two VALU instructions where the IEEE divide takes about ten,
 // in epilogues that evaluate it 32 times per lane.  g very negative gives
 // 1 + e^-g = inf and a signed zero, as the divide does.
 __device__ __forceinline__ float silu_f32(float g) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+
+// A float that no lane varies and no kernel of the launch writes, by a scalar
+// load: a vector load would be waited for with all the DMA issued before it.
+__device__ __forceinline__ float scalar_load(const float* p) {
+  return *reinterpret_cast<const __attribute__((address_space(4))) float*>(reinterpret_cast<uintptr_t>(p));
+}
 
 }  // namespace fp4

@@ -7,23 +7,26 @@
 //
 // Two kernels: routing, quantization of x and the gate_up products (every
 // workgroup routes the tokens by itself); then the down products with the
-// routing-weighted sum over experts kept in registers, so that neither a
+// routing-weighted sum over experts kept on the chip, so that neither a
 // permutation nor per-pair down outputs exist.  Where h is quantized a small
 // kernel between the two does it.
 //
 // What bounds it: the touched experts' weights, read once (2.76 MB an expert
-// at hidden 2560, intermediate 640 in NVFP4).  All tokens of the call are the
-// 16 columns of one 16x16x32 bf16 MFMA tile, so an expert's weights are
-// decoded once whatever the number of its tokens, and no gather is needed:
-// gate_up computes every column and keeps those of the expert's tokens, down
-// reads zeros for the others.
+// at hidden 2560, intermediate 640 in NVFP4).  They stream through a ring of
+// blocks in LDS that belongs to one wave (16 rows x 128 bytes of codes and
+// their scales, by DMA, without barriers); loading MFMA fragments straight
+// into registers touches four rows in every four lanes and measured twice the
+// time.  All tokens of the call are the 16 columns of one 16x16x32 bf16 MFMA
+// tile, so gate_up decodes an expert's weights once whatever the number of its
+// tokens and gathers nothing: it computes every column and keeps those of the
+// expert's tokens.
 //
 // Everything the products read is exact in bf16: bf16 x, E4M3 values times
 // powers of two (MXFP8), E4M3 codes alone (FP8 rows; their scales multiply the
 // f32 sum of each 128-block), E2M1 codes times E4M3 block scales (6
-// significant bits), E2M1 codes times powers of two.  An unquantized h (f32)
-// is split into three bf16 terms whose sum is h (3 x 8 significant bits).
-// Sums are f32.
+// significant bits), E2M1 codes times powers of two.  An h held in f32 (not
+// quantized, or FP8 codes times their scales) is split into three bf16 terms
+// whose sum is h (3 x 8 significant bits).  Sums are f32.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -39,11 +42,11 @@ namespace fp4 {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 
-constexpr int kFewTokens = 16;   // columns of the MFMA tile
-constexpr int kGuWaves = 8;      // waves per workgroup of the gate_up kernel
-constexpr int kGuAhead = 5;      // K steps loaded together
-constexpr int kDnWaves = 16;     // waves per workgroup of the down kernel
-constexpr int kDnAhead = 5;
+constexpr int kFewTokens = 16;  // columns of the MFMA tile
+constexpr int kGuWaves = 8;     // most waves per workgroup of the gate_up kernel
+constexpr int kDnWaves = 8;     // waves per workgroup of the down kernel, a strip of 16 outputs each
+constexpr int kDnRing = 4;      // blocks in a wave's ring of the down kernel
+constexpr int kDnSeg = 64;      // most experts of one split
 
 // format pairs of the layer
 enum FewMode { FM_NV = 0, FM_MX = 1, FM_NVNV = 2, FM_MXMX = 3, FM_FP8 = 4 };
@@ -66,14 +69,17 @@ struct FewArgs {
   int T, E, k, H, I, S;    // S: shared width, 0 without a shared expert
   int routed_wgs;          // gate_up workgroups of the routed experts; the rest take the shared expert
   int k_split;             // waves that share one unit of the routed gate_up
+  int splits, shared_splits;  // down workgroups of a row group: of the routed experts, of the shared expert
+  int pass_pairs, shared_pairs;  // pairs of an expert, tokens of the shared expert that the down kernel takes at once
   // workspace
-  int32_t *ids, *list, *slot;  // [T k], [1 + min(E, T k)] (count first), [.., 16] pair of (listed expert, token) or -1
+  int32_t *list, *pairs;   // touched experts [1 + min(E, T k)] (count first); [.., 16] their pairs, then -1
+  int32_t* done;           // [ceil(H / 128)] arrivals of the down kernel's splits
   float *wts, *sgate, *amax_part, *h_ts;
   float* h;                // f32 [T k, I] (quantized modes)
   uint16_t* hb;            // bf16 [T k, I] quantized values, or [T k, 3, I] terms
-  float* hf;               // FP8 rows: scales [T k, I / 128]
   float* sh;               // f32 [T, S]
   uint16_t* shb;           // bf16 [T, S]
+  float* ypart;            // f32 [splits + shared_splits, T, H]
   // outputs
   int32_t* ids_out;
   float* wts_out;
@@ -90,32 +96,78 @@ __device__ __forceinline__ float ue8m0_f32(uint32_t c) {
   return c ? __uint_as_float(c << 23) : 5.877471754111438e-39f;  // 2^-127
 }
 
-// A lane's share of a weight row's 128-wide K step: 32 consecutive values
-// (chunk g of lane group g) and their block scales.
+// A block of a strip: 16 weight rows x 128 bytes of codes (K values 256 wide
+// in E2M1, 128 in E4M3) and their scale bytes, as a ring slot holds them: the
+// rows' 16-byte chunks XOR-swizzled by the row, then the scales row by row.
 template <int FMT>
-struct WStep {
-  u32x4 c[FMT == FP4_FMT_NVFP4 || FMT == FP4_FMT_MXFP4 ? 1 : 2];
-  uint32_t s;
+struct Blk {
+  static constexpr bool FP4 = FMT == FP4_FMT_NVFP4 || FMT == FP4_FMT_MXFP4;
+  static constexpr int K = FP4 ? 256 : 128, STEPS = K / 128;
+  static constexpr int SROW = FMT == FP4_FMT_NVFP4 ? 16 : FMT == FP4_FMT_MXFP4 ? 8 : FMT == FP4_FMT_MXFP8 ? 4 : 0;  // scale bytes a row
+  static constexpr int NDMA = SROW ? 3 : 2;           // DMA instructions of a strip's block
+  static constexpr int SLOT = 2048 + 16 * SROW;
 };
 
+// A strip's tensors: 16 rows of codes and of scales.
 template <int FMT>
-__device__ __forceinline__ void load_wstep(WStep<FMT>& v, const uint8_t* row, const uint8_t* srow, int kb, int g, int K) {
-  const int k0 = 128 * kb + 32 * g;
-  const int kk = k0 < K ? k0 : 0;  // past the row's end: its start, multiplied by zeros
-  if constexpr (FMT == FP4_FMT_NVFP4) {
-    v.c[0] = ld16(row + kk / 2);
-    v.s = *reinterpret_cast<const uint16_t*>(srow + kk / 16);
-  } else if constexpr (FMT == FP4_FMT_MXFP4) {
-    v.c[0] = ld16(row + kk / 2);
-    v.s = srow[kk / 32];
-  } else {
-    v.c[0] = ld16(row + kk);
-    v.c[1] = ld16(row + kk + 16);
-    v.s = FMT == FP4_FMT_MXFP8 ? srow[kk / 32] : 0;
+struct Strip {
+  __amdgpu_buffer_rsrc_t codes, scales;
+  const uint8_t* srow;  // the scales' first row
+  __device__ __forceinline__ void set(const uint8_t* c, const uint8_t* sc, int64_t rb, int64_t rs) {
+    codes = buffer_of(c, (uint32_t)(16 * rb));
+    scales = buffer_of(sc, (uint32_t)(16 * rs));
+    srow = sc;
+  }
+};
+
+// Loads block `blk` of a strip into `slot`.  Chunks and scales past a row's
+// end read the row's start (they meet zeros of x or h).  Scale rows that are no multiple of 4 bytes (K not a
+// multiple of 64 in NVFP4, of 128 in MXFP4) cannot be copied by DMA and go
+// through registers.
+template <int FMT>
+__device__ __forceinline__ void load_block(const Strip<FMT>& s, int blk, int64_t rb, int64_t rs, uint8_t* slot) {
+  using B = Blk<FMT>;
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int row = 8 * j + (lane >> 3), at = 128 * blk + 16 * ((lane & 7) ^ (row >> 1));
+    dma_buffer(s.codes, (uint32_t)(row * (int)rb) + (at < (int)rb ? at : 0), 0, slot + 1024 * j);
+  }
+  if constexpr (B::SROW > 0) {
+    uint8_t* to = slot + 2048;
+    if ((rs & 3) == 0) {
+      constexpr int W = B::SROW / 4;  // dwords of a row's scales
+      const int row = lane / W, at = B::SROW * blk + 4 * (lane % W);
+      if (lane < 16 * W) dma_buffer4(s.scales, (uint32_t)(row * (int)rs + (at < (int)rs ? at : 0)), 0, to);
+    } else {
+      for (int i = lane; i < 16 * B::SROW; i += 64) {
+        const int row = i / B::SROW, at = B::SROW * blk + i % B::SROW;
+        to[i] = at < (int)rs ? s.srow[row * rs + at] : 0;
+      }
+    }
   }
 }
 
-// Values 8j .. 8j+7 of the lane's 32 as bf16 (exact).
+// Values 8j .. 8j+7 of a lane's 32 (K values [128 step + 32 g, + 32) of the
+// block, row r) as bf16 (exact).
+template <int FMT>
+struct WStep {
+  u32x4 c[Blk<FMT>::FP4 ? 1 : 2];
+  uint32_t s;
+  __device__ __forceinline__ void read(const uint8_t* slot, int step, int g, int r) {
+    const uint8_t* row = slot + 128 * r;
+    if constexpr (Blk<FMT>::FP4) {
+      c[0] = ld16(row + 16 * ((4 * step + g) ^ (r >> 1)));
+    } else {
+      c[0] = ld16(row + 16 * ((2 * g) ^ (r >> 1)));
+      c[1] = ld16(row + 16 * ((2 * g + 1) ^ (r >> 1)));
+    }
+    if constexpr (FMT == FP4_FMT_NVFP4) s = *reinterpret_cast<const uint16_t*>(slot + 2048 + 16 * r + 8 * step + 2 * g);
+    else if constexpr (FMT == FP4_FMT_MXFP4) s = slot[2048 + 8 * r + 4 * step + g];
+    else if constexpr (FMT == FP4_FMT_MXFP8) s = slot[2048 + 4 * r + g];
+  }
+};
+
 template <int FMT>
 __device__ __forceinline__ bf16x8_t wstep_frag(const WStep<FMT>& v, int j) {
   u32x4 p;
@@ -226,6 +278,18 @@ __device__ __forceinline__ void store_bf16x32(void* p, const float (&v)[32]) {
   }
 }
 
+// The three bf16 terms of v (their sum is v): by truncation, so that a finite
+// rest never rounds up to infinity, and each rest is exact.  An infinity or
+// NaN is its first term.
+__device__ __forceinline__ void bf16_terms(float v, uint32_t (&t)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const uint32_t b = __float_as_uint(v);
+    t[i] = b >> 16;
+    v = (b & 0x7F800000u) != 0x7F800000u ? v - __uint_as_float(b & 0xFFFF0000u) : 0.0f;
+  }
+}
+
 // ---------------------------------------------------------------- routing
 
 // Order-preserving key of a router value: larger value, larger key; 0 for
@@ -291,19 +355,23 @@ __device__ __forceinline__ uint32_t select_topk(const float* logits, const float
 // ------------------------------------------------------------------ gate_up
 
 struct GuSmem {
-  int x, xf, ids, mask, list, red, total;
+  int x, xf, ids, mask, list, scale, slot, red, ring, total;
 };
-// byte offsets of the gate_up kernel's dynamic LDS
-__host__ __device__ inline GuSmem gu_smem(int T, int E, int k, int K) {
+// byte offsets of the gate_up kernel's dynamic LDS: nw waves with `ring` bytes
+// each, their partial sums if a unit is split between waves
+__host__ __device__ inline GuSmem gu_smem(int T, int E, int k, int K, int nw, int ring, bool split) {
   GuSmem s;
-  const int kp = (K + 127) / 128 * 128;
+  const int kp = (K + 127) / 128 * 128, D = E < T * k ? E : T * k;
   s.x = 0;  // rows padded by 16 bytes: 16 lanes that read one chunk of 16 rows hit different banks
   s.xf = s.x + T * (kp + 8) * 2;
   s.ids = s.xf + T * (kp / 128) * 4;
   s.mask = s.ids + T * k * 4;
   s.list = s.mask + E * 4;
-  s.red = (s.list + (T * k + 1) * 4 + 15) / 16 * 16;
-  s.total = s.red + kGuWaves * 64 * 8 * 4;
+  s.scale = s.list + (D + 1) * 4;
+  s.slot = s.scale + D * 4;
+  s.red = (s.slot + D * kFewTokens + 15) / 16 * 16;
+  s.ring = s.red + (split ? nw * 64 * 8 * 4 : 0);
+  s.total = s.ring + nw * ring;
   return s;
 }
 
@@ -318,7 +386,7 @@ __device__ float prepare_x(const FewArgs& a, uint8_t* sx, float* xf, float* tmp)
       ts = a.x_scale[0];
     } else {
       float m = 0.0f;
-      for (int c = threadIdx.x; c < T * H / 32; c += 64 * kGuWaves) {
+      for (int c = threadIdx.x; c < T * H / 32; c += (int)blockDim.x) {
         float v[32];
         load_bf16x32(a.x + 32 * (int64_t)c, v);
 #pragma unroll
@@ -330,12 +398,13 @@ __device__ float prepare_x(const FewArgs& a, uint8_t* sx, float* xf, float* tmp)
       __syncthreads();
       m = tmp[0];
 #pragma unroll
-      for (int w = 1; w < kGuWaves; ++w) m = fmaxf(m, tmp[w]);
+      for (int w = 1; w < kGuWaves; ++w)
+        if (w < (int)blockDim.x >> 6) m = fmaxf(m, tmp[w]);
       ts = (float)((double)m / kNvTensorDivisor);
     }
   }
   const int per = kp / 32;
-  for (int c = threadIdx.x; c < T * per; c += 64 * kGuWaves) {
+  for (int c = threadIdx.x; c < T * per; c += (int)blockDim.x) {
     const int t = c / per, q = c - t * per;
     float v[32];
     if (32 * q < H) {
@@ -351,62 +420,22 @@ __device__ float prepare_x(const FewArgs& a, uint8_t* sx, float* xf, float* tmp)
   return ts;
 }
 
-// 16 gate rows and the 16 up rows of one unit over the K steps [kb0, kb1) for
-// all tokens.
-template <int FMT>
-__device__ __forceinline__ void gu_unit(const uint8_t* wg, const uint8_t* wu, const uint8_t* sg, const uint8_t* su,
-                                        const float* fg, const float* fu, const uint8_t* sx, const float* xf, int K, int kb0, int kb1, int xt,
-                                        int g, floatx4& accg, floatx4& accu) {
-  const int kp = (K + 127) / 128 * 128;
-  const uint8_t* xrow = sx + (xt * (kp + 8) + 32 * g) * 2;
-  for (int kb = kb0; kb < kb1; kb += kGuAhead) {
-    WStep<FMT> vg[kGuAhead], vu[kGuAhead];
-#pragma unroll
-    for (int u = 0; u < kGuAhead; ++u) {
-      const int q = min(kb + u, kb1 - 1);
-      load_wstep<FMT>(vg[u], wg, sg, q, g, K);
-      load_wstep<FMT>(vu[u], wu, su, q, g, K);
-    }
-#pragma unroll
-    for (int u = 0; u < kGuAhead; ++u) {
-      if (kb + u < kb1) {
-        floatx4 pg = accg, pu = accu;
-        if (FMT == FP4_FMT_FP8_BLOCK) pg = pu = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bf16x8_t xv = __builtin_bit_cast(bf16x8_t, ld16(xrow + (128 * (kb + u) + 8 * j) * 2));
-          pg = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wstep_frag<FMT>(vg[u], j), xv, pg, 0, 0, 0);
-          pu = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wstep_frag<FMT>(vu[u], j), xv, pu, 0, 0, 0);
-        }
-        if (FMT == FP4_FMT_FP8_BLOCK) {
-          const float f = xf[xt * (kp / 128) + kb + u];
-          const float a = f * fg[kb + u], b = f * fu[kb + u];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            accg[q] = fmaf(pg[q], a, accg[q]);
-            accu[q] = fmaf(pu[q], b, accu[q]);
-          }
-        } else {
-          accg = pg;
-          accu = pu;
-        }
-      }
-    }
-  }
-}
-
-// Sum over the k_split waves of a unit (LDS, one barrier before and one
+// Sum over the `split` waves of a unit (in LDS, a barrier before and one
 // after); the first of them holds the result.
 __device__ __forceinline__ void gu_reduce(floatx4& a, floatx4& b, float* red, int ks, int split) {
   if (split == 1) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  __syncthreads();
+  auto sync = []() __attribute__((always_inline)) {  // LDS only: the blocks on their way stay so
+    __builtin_amdgcn_s_waitcnt(lgkmcnt0());
+    asm volatile("s_barrier" ::: "memory");
+  };
+  sync();
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     red[(wave * 8 + q) * 64 + lane] = a[q];
     red[(wave * 8 + 4 + q) * 64 + lane] = b[q];
   }
-  __syncthreads();
+  sync();
   if (ks == 0)
     for (int w = 1; w < split; ++w)
 #pragma unroll
@@ -416,25 +445,101 @@ __device__ __forceinline__ void gu_reduce(floatx4& a, floatx4& b, float* red, in
       }
 }
 
-template <int MODE>
-__global__ void __launch_bounds__(64 * kGuWaves, 4) few_gateup_kernel(FewArgs a) {
+// One wave's stream of gate_up units: in every round j < rounds it multiplies
+// the blocks [lo, hi) of a unit's 16 gate rows and 16 up rows with all
+// tokens' x~ (if j < mine) and hands the sums to finish(j, gate, up).
+// strips(j, gate, up) gives a round's weight rows, scales(j) the first block
+// scales of block FP8.  A ring of D slots; the loads of the next D - 1 blocks
+// are on their way, over the rounds' borders.
+template <int FMT, int D, typename Strips, typename Scales, typename Finish>
+__device__ __forceinline__ void gu_stream(int rounds, int mine, int lo, int hi, int K, int64_t rb, int64_t rs, const uint8_t* sx, const float* xf,
+                                          int xt, uint8_t* ring, Strips strips, Scales scales, Finish finish) {
+  using B = Blk<FMT>;
+  constexpr int SLOT = 2 * B::SLOT, ND = 2 * B::NDMA;
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15, kp = (K + 127) / 128 * 128;
+  const uint8_t* xrow = sx + (xt * (kp + 8) + 32 * g) * 2;
+  const bool any = mine > 0 && hi > lo, dma_scales = (rs & 3) == 0;
+  Strip<FMT> sg, su;
+  int lj = 0, lb = lo;
+  auto load_next = [&](int slot) __attribute__((always_inline)) {
+    if (lb == lo) strips(min(lj, mine - 1), sg, su);  // past the end the last unit again: every step issues as many loads
+    load_block<FMT>(sg, lb, rb, rs, ring + slot * SLOT);
+    load_block<FMT>(su, lb, rb, rs, ring + slot * SLOT + B::SLOT);
+    if (++lb == hi) { lb = lo; ++lj; }
+  };
+  if (any) {
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) load_next(d);
+  }
+  int slot = 0;
+  for (int j = 0; j < rounds; ++j) {
+    floatx4 ag{0.f, 0.f, 0.f, 0.f}, au = ag;
+    if (any && j < mine) {
+      const float *fg = nullptr, *fu = nullptr;
+      if (FMT == FP4_FMT_FP8_BLOCK) scales(j, fg, fu);
+      for (int blk = lo; blk < hi; ++blk) {
+        load_next(slot == 0 ? D - 1 : slot - 1);
+        if (dma_scales) __builtin_amdgcn_s_waitcnt(vmcnt_only(ND * (D - 1)));
+        else __builtin_amdgcn_s_waitcnt(0);
+        asm volatile("" ::: "memory");
+        const uint8_t* at = ring + slot * SLOT;
+        slot = slot == D - 1 ? 0 : slot + 1;
+#pragma unroll
+        for (int st = 0; st < B::STEPS; ++st) {
+          const int kb = blk * B::STEPS + st;
+          if (128 * kb < K) {
+            WStep<FMT> wg, wu;
+            wg.read(at, st, g, r);
+            wu.read(at + B::SLOT, st, g, r);
+            floatx4 pg = ag, pu = au;
+            if (FMT == FP4_FMT_FP8_BLOCK) pg = pu = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const bf16x8_t xv = __builtin_bit_cast(bf16x8_t, ld16(xrow + (128 * kb + 8 * q) * 2));
+              pg = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wstep_frag<FMT>(wg, q), xv, pg, 0, 0, 0);
+              pu = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wstep_frag<FMT>(wu, q), xv, pu, 0, 0, 0);
+            }
+            if (FMT == FP4_FMT_FP8_BLOCK) {
+              const float f = xf[xt * (kp / 128) + kb], a = f * scalar_load(fg + kb), b = f * scalar_load(fu + kb);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                ag[q] = fmaf(pg[q], a, ag[q]);
+                au[q] = fmaf(pu[q], b, au[q]);
+              }
+            } else {
+              ag = pg;
+              au = pu;
+            }
+          }
+        }
+      }
+    }
+    finish(j, ag, au);
+  }
+  __builtin_amdgcn_s_waitcnt(vmcnt_only(0));  // no DMA outlives the workgroup
+}
+
+template <int MODE, int D>
+__global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a) {
   constexpr int WF = weight_fmt(MODE), AF = act_fmt(MODE);
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ float tmp[kGuWaves];
   __shared__ uint32_t s_amax;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, r = lane & 15;
-  const int T = a.T, k = a.k, H = a.H, KB = (H + 127) / 128, P = T * k;
-  const GuSmem sm = gu_smem(T, a.E, k, H);
+  const int tid = threadIdx.x, th = blockDim.x, nw = th >> 6, lane = tid & 63, g = lane >> 4, r = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int T = a.T, k = a.k, H = a.H, P = T * k, split = a.k_split, ks = wave % split, per = nw / split;
+  constexpr int RING = D * 2 * Blk<WF>::SLOT, SRING = D * 2 * Blk<FP4_FMT_MXFP8>::SLOT;
+  const GuSmem sm = gu_smem(T, a.E, k, H, nw, RING > SRING ? RING : SRING, split > 1);
   float* xf = reinterpret_cast<float*>(smem + sm.xf);
   float* red = reinterpret_cast<float*>(smem + sm.red);
+  uint8_t* ring = smem + sm.ring + wave * (RING > SRING ? RING : SRING);
   const int xt = min(r, T - 1);  // columns past the last token repeat it and are not kept
-  const floatx4 zero{0.f, 0.f, 0.f, 0.f};
 
   if ((int)blockIdx.x >= a.routed_wgs) {  // shared expert
-    const int S = a.S, units = S / 16, first = blockIdx.x - a.routed_wgs, step = gridDim.x - a.routed_wgs;
+    const int S = a.S, units = S / 16, wgs = gridDim.x - a.routed_wgs, first = (blockIdx.x - a.routed_wgs) * per + wave / split;
     prepare_x<FP4_FMT_MXFP8>(a, smem + sm.x, xf, tmp);
-    if (first == 0) {  // sigmoid(x_t . g) on unquantized x
-      for (int t = wave; t < T; t += kGuWaves) {
+    if ((int)blockIdx.x == a.routed_wgs) {  // sigmoid(x_t . g) on unquantized x
+      for (int t = wave; t < T; t += nw) {
         float acc = 0.0f;
         for (int c = lane * 8; c < H; c += 512) {
           const u32x4 p = ld16(a.x + (int64_t)t * H + c), q = ld16(a.gate + c);
@@ -447,30 +552,38 @@ __global__ void __launch_bounds__(64 * kGuWaves, 4) few_gateup_kernel(FewArgs a)
       }
     }
     __syncthreads();
-    const int lo = wave * KB / kGuWaves, hi = (wave + 1) * KB / kGuWaves;
-    for (int u = first; u < units; u += step) {
-      const int64_t row = 16 * u + r;
-      floatx4 ag = zero, au = zero;
-      const uint8_t *wg = a.ws13 + row * H, *sg = a.ws13s + row * (H / 32);
-      gu_unit<FP4_FMT_MXFP8>(wg, wg + (int64_t)S * H, sg, sg + (int64_t)S * (H / 32), nullptr, nullptr, smem + sm.x, xf, H,
-                             lo, hi, xt, g, ag, au);
-      gu_reduce(ag, au, red, wave, kGuWaves);
-      if (wave == 0 && r < T) {
-        floatx4 h;
+    const int NB = H / 128, lo = ks * NB / split, hi = (ks + 1) * NB / split;
+    const int base = (blockIdx.x - a.routed_wgs) * per, rounds = (units - base + wgs * per - 1) / (wgs * per);
+    const int mine = max(0, (units - first + wgs * per - 1) / (wgs * per));
+    gu_stream<FP4_FMT_MXFP8, D>(
+        rounds, mine, lo, hi, H, H, H / 32, smem + sm.x, xf, xt, ring,
+        [&](int j, Strip<FP4_FMT_MXFP8>& sg, Strip<FP4_FMT_MXFP8>& su) __attribute__((always_inline)) {
+          const int64_t row = 16 * (int64_t)(first + j * wgs * per);
+          sg.set(a.ws13 + row * H, a.ws13s + row * (H / 32), H, H / 32);
+          su.set(a.ws13 + (S + row) * H, a.ws13s + (S + row) * (H / 32), H, H / 32);
+        },
+        [](int, const float*&, const float*&) {},
+        [&](int j, floatx4& ag, floatx4& au) __attribute__((always_inline)) {
+          gu_reduce(ag, au, red, ks, split);
+          if (j < mine && ks == 0 && r < T) {
+            floatx4 h;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) h[q] = silu_f32(ag[q]) * au[q];
-        *reinterpret_cast<floatx4*>(a.sh + (int64_t)r * S + 16 * u + 4 * g) = h;
-      }
-    }
+            for (int q = 0; q < 4; ++q) h[q] = silu_f32(ag[q]) * au[q];
+            *reinterpret_cast<floatx4*>(a.sh + (int64_t)r * S + 16 * (first + j * wgs * per) + 4 * g) = h;
+          }
+        });
     return;
   }
 
   int* ids = reinterpret_cast<int*>(smem + sm.ids);
-  uint32_t* mask = reinterpret_cast<uint32_t*>(smem + sm.mask);
+  uint32_t* mask = reinterpret_cast<uint32_t*>(smem + sm.mask);  // tokens of an expert; then its place in the list above them
   int* list = reinterpret_cast<int*>(smem + sm.list);
-  for (int e = tid; e < a.E; e += 64 * kGuWaves) mask[e] = 0;
+  float* scale = reinterpret_cast<float*>(smem + sm.scale);
+  uint8_t* slots = smem + sm.slot;  // [listed expert][token]: the token's slot + 1
+  for (int e = tid; e < a.E; e += th) mask[e] = 0;
+  for (int i = tid; i < min(a.E, P) * kFewTokens / 4; i += th) reinterpret_cast<uint32_t*>(slots)[i] = 0;
   if (tid == 0) s_amax = 0;
-  for (int t = wave; t < T; t += kGuWaves) {
+  for (int t = wave; t < T; t += nw) {
     const float* lg = a.logits + (int64_t)t * a.E;
     uint32_t key;
     if (a.E <= 128) key = select_topk<2>(lg, a.bias, a.E, k, ids + t * k);
@@ -493,89 +606,84 @@ __global__ void __launch_bounds__(64 * kGuWaves, 4) few_gateup_kernel(FewArgs a)
   }
   const float xs = prepare_x<AF>(a, smem + sm.x, xf, tmp);
   __syncthreads();
-  for (int p = tid; p < P; p += 64 * kGuWaves)
+  for (int p = tid; p < P; p += th)
     if (ids[p] >= 0) atomicOr(&mask[ids[p]], 1u << (p / k));
   __syncthreads();
   if (wave == 0) {  // the touched experts, by id
     int n = 0;
     for (int e0 = 0; e0 < a.E; e0 += 64) {
-      const bool on = e0 + lane < a.E && mask[e0 + lane] != 0;
-      const uint64_t m = __ballot(on);
-      if (on) list[1 + n + __popcll(m & ((1ull << lane) - 1))] = e0 + lane;
-      n += __popcll(m);
+      const uint32_t m = e0 + lane < a.E ? mask[e0 + lane] : 0u;
+      const uint64_t on = __ballot(m != 0);
+      if (m) {
+        const int at = n + __popcll(on & ((1ull << lane) - 1));
+        list[1 + at] = e0 + lane;
+        mask[e0 + lane] = m | (uint32_t)at << 16;
+        scale[at] = WF == FP4_FMT_NVFP4 ? a.w13s2[e0 + lane] * xs : 1.0f;
+      }
+      n += __popcll(on);
     }
     if (lane == 0) list[0] = n;
   }
   __syncthreads();
+  for (int p = tid; p < P; p += th)
+    if (ids[p] >= 0) slots[(mask[ids[p]] >> 16) * kFewTokens + p / k] = (uint8_t)(p % k + 1);
+  __syncthreads();
   const int nd = list[0];
-  if (blockIdx.x == 0) {
-    for (int p = tid; p < P; p += 64 * kGuWaves) {
-      a.ids[p] = ids[p];
-      if (a.ids_out) a.ids_out[p] = ids[p];
-    }
-    for (int i = tid; i <= nd; i += 64 * kGuWaves) a.list[i] = list[i];
-    for (int i = tid; i < nd * kFewTokens; i += 64 * kGuWaves) {
-      const int e = list[1 + (i >> 4)], t = i & 15;
-      int p = -1;
-      if (t < T && (mask[e] >> t & 1u))
-        for (int j = 0; j < k; ++j)
-          if (ids[t * k + j] == e) p = t * k + j;
-      a.slot[i] = p;
+  if (blockIdx.x == 0) {  // for the down kernel
+    for (int i = tid; i < (H + 127) / 128; i += th) a.done[i] = 0;
+    if (a.ids_out)
+      for (int p = tid; p < P; p += th) a.ids_out[p] = ids[p];
+    for (int i = tid; i <= nd; i += th) a.list[i] = list[i];
+    for (int i = tid; i < nd; i += th) {
+      int n = 0;
+      for (int t = 0; t < T; ++t)
+        if (const int j = slots[i * kFewTokens + t]) a.pairs[i * kFewTokens + n++] = t * k + j - 1;
+      for (; n < kFewTokens; ++n) a.pairs[i * kFewTokens + n] = -1;
     }
   }
 
-  const int I = a.I, strips = I / 16, units = nd * strips;
-  const int split = a.k_split, per = kGuWaves / split, ks = wave % split;
-  const int lo = ks * KB / split, hi = (ks + 1) * KB / split;
+  const int I = a.I, strips = I / 16, units = nd * strips, base = blockIdx.x * per, first = base + wave / split, step = a.routed_wgs * per;
   const int64_t rb = code_row_bytes<WF>(H), rs = scale_row_bytes<WF>(H);
+  const int NB = (H + Blk<WF>::K - 1) / Blk<WF>::K, lo = ks * NB / split, hi = (ks + 1) * NB / split;
   float hmax = 0.0f;
-  for (int u0 = blockIdx.x * per; u0 < units; u0 += a.routed_wgs * per) {
-    const int u = u0 + wave / split;
-    const bool on = u < units;
-    const int e = list[1 + (on ? u / strips : 0)], i0 = (on ? u % strips : 0) * 16;
-    floatx4 ag = zero, au = zero;
-    if (on) {
-      const int64_t row = (int64_t)e * 2 * I + i0 + r;
-      const uint8_t *wg = a.w13 + row * rb, *sg = static_cast<const uint8_t*>(a.w13s) + row * rs;
-      const float *fg = nullptr, *fu = nullptr;
-      if (WF == FP4_FMT_FP8_BLOCK) {
-        fg = static_cast<const float*>(a.w13s) + ((int64_t)e * (2 * I / 128) + i0 / 128) * KB;
+  gu_stream<WF, D>(
+      max(0, (units - base + step - 1) / step), max(0, (units - first + step - 1) / step), lo, hi, H, rb, rs, smem + sm.x, xf, xt, ring,
+      [&](int j, Strip<WF>& sg, Strip<WF>& su) __attribute__((always_inline)) {
+        const int u = first + j * step, e = __builtin_amdgcn_readfirstlane(list[1 + u / strips]);
+        const int64_t row = (int64_t)e * 2 * I + (u % strips) * 16;
+        const uint8_t* ss = static_cast<const uint8_t*>(a.w13s);
+        sg.set(a.w13 + row * rb, ss + row * rs, rb, rs);
+        su.set(a.w13 + (row + I) * rb, ss + (row + I) * rs, rb, rs);
+      },
+      [&](int j, const float*& fg, const float*& fu) __attribute__((always_inline)) {
+        const int u = first + j * step, e = __builtin_amdgcn_readfirstlane(list[1 + u / strips]), KB = H / 128;
+        fg = static_cast<const float*>(a.w13s) + ((int64_t)e * (2 * I / 128) + (u % strips) / 8) * KB;
         fu = fg + (int64_t)(I / 128) * KB;
-      }
-      gu_unit<WF>(wg, wg + I * rb, sg, sg + I * rs, fg, fu, smem + sm.x, xf, H, lo, hi, xt, g, ag, au);
-    }
-    gu_reduce(ag, au, red, ks, split);
-    if (on && ks == 0 && r < T && (mask[e] >> r & 1u)) {
-      int p = 0;
-      for (int j = 0; j < k; ++j)
-        if (ids[r * k + j] == e) p = r * k + j;
-      const float s = WF == FP4_FMT_NVFP4 ? a.w13s2[e] * xs : 1.0f;
-      floatx4 h;
+      },
+      [&](int j, floatx4& ag, floatx4& au) __attribute__((always_inline)) {
+        gu_reduce(ag, au, red, ks, split);
+        const int u = first + j * step;
+        if (u >= units || ks != 0) return;
+        const int ai = u / strips, i0 = (u % strips) * 16, slot = slots[ai * kFewTokens + r];
+        if (slot == 0) return;  // not a token of this expert
+        const int64_t p = (int64_t)r * k + slot - 1;
+        const float s = scale[ai];
+        floatx4 h;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) h[q] = silu_f32(ag[q] * s) * (au[q] * s);
-      if constexpr (AF == FP4_FMT_NONE) {
-        uint16_t* d = a.hb + (int64_t)p * 3 * I + i0 + 4 * g;
-        float rest[4] = {h[0], h[1], h[2], h[3]};
+        for (int q = 0; q < 4; ++q) h[q] = silu_f32(ag[q] * s) * (au[q] * s);
+        if constexpr (AF == FP4_FMT_NONE) {
+          uint32_t t[4][3];
 #pragma unroll
-        for (int term = 0; term < 3; ++term) {
-          uint32_t w[2] = {0, 0};
+          for (int q = 0; q < 4; ++q) bf16_terms(h[q], t[q]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            // truncation, so that a finite rest never rounds up to infinity; what is left is exact
-            const uint32_t b = __float_as_uint(rest[q]);
-            w[q >> 1] |= (b >> 16) << (16 * (q & 1));
-            const bool fin = (b & 0x7F800000u) != 0x7F800000u;
-            rest[q] = fin ? rest[q] - __uint_as_float(b & 0xFFFF0000u) : 0.0f;
-          }
-          *reinterpret_cast<u32x2*>(d + (int64_t)term * I) = u32x2{w[0], w[1]};
+          for (int i = 0; i < 3; ++i)
+            *reinterpret_cast<u32x2*>(a.hb + (p * 3 + i) * I + i0 + 4 * g) = u32x2{t[0][i] | t[1][i] << 16, t[2][i] | t[3][i] << 16};
+        } else {
+          *reinterpret_cast<floatx4*>(a.h + p * I + i0 + 4 * g) = h;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) hmax = fmaxf(hmax, fabsf(h[q]));
         }
-      } else {
-        *reinterpret_cast<floatx4*>(a.h + (int64_t)p * I + i0 + 4 * g) = h;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) hmax = fmaxf(hmax, fabsf(h[q]));
-      }
-    }
-  }
+      });
   if constexpr (AF == FP4_FMT_NVFP4) {  // the largest |h| of this workgroup (non-negative floats order as integers)
     if (hmax > 0.0f) atomicMax(&s_amax, __float_as_uint(hmax));
     __syncthreads();
@@ -617,8 +725,25 @@ __global__ void __launch_bounds__(256) few_hquant_kernel(FewArgs a) {
   if (c < routed) {
     load(a.h + 32 * (int64_t)c);
     const float f = quantize32<AF>(v, ts);
-    store_bf16x32(a.hb + 32 * (int64_t)c, v);
-    if (AF == FP4_FMT_FP8_ROW && (c & 3) == 0) a.hf[c >> 2] = f;
+    if constexpr (AF == FP4_FMT_FP8_ROW) {  // code times scale, as three terms
+      const int p = c / (a.I / 32), i0 = 32 * (c - p * (a.I / 32));
+#pragma unroll
+      for (int i = 0; i < 32; i += 8) {
+        u32x4 w[3];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t lo[3], hi[3];
+          bf16_terms(v[i + 2 * q] * f, lo);
+          bf16_terms(v[i + 2 * q + 1] * f, hi);
+#pragma unroll
+          for (int t = 0; t < 3; ++t) w[t][q] = lo[t] | hi[t] << 16;
+        }
+#pragma unroll
+        for (int t = 0; t < 3; ++t) st16(a.hb + ((int64_t)p * 3 + t) * a.I + i0 + i, w[t]);
+      }
+    } else {
+      store_bf16x32(a.hb + 32 * (int64_t)c, v);
+    }
   } else if (c < routed + shared) {
     load(a.sh + 32 * (int64_t)(c - routed));
     quantize32<FP4_FMT_MXFP8>(v, ts);
@@ -628,176 +753,341 @@ __global__ void __launch_bounds__(256) few_hquant_kernel(FewArgs a) {
 
 // --------------------------------------------------------------------- down
 
-// K steps [kb0, kb0 + kDnAhead) of 16 rows of one expert's down matrix times
-// the expert's h: acc += f * product (FP8 blocks: f times the block's scales).
-// hrow: the lane's pair's h (its first term), or null (a column of zeros).
-template <int FMT, int NT>
-__device__ __forceinline__ void dn_item(const uint8_t* row, const uint8_t* srow, const float* fw, const uint16_t* hrow, const float* hf,
-                                        int K, int kb0, int g, float f, floatx4& acc) {
-  const int KB = (K + 127) / 128;
-  WStep<FMT> v[kDnAhead];
+// LDS of the down kernel: the waves' rings, then h of two passes, then the
+// waves' outputs (f32 [16 tokens][16]).
+template <int FMT>
+constexpr int dn_ring() { return kDnRing * Blk<FMT>::SLOT; }
+
+// One workgroup's share of the down products: a row group (128 outputs, a
+// strip of 16 a wave) times the passes of the experts [a0, a1) of a list; a
+// pass is up to PP pairs of one expert, whose h rows (NT terms each) are
+// copied into LDS one pass ahead and are the columns of the MFMA tile: row
+// term * PP + pair.  expert(i) gives the expert's number and pair count,
+// pair(i, q) its q-th pair, factor(p) what multiplies a pair's product, token(p)
+// its row of y; blocks [lo, hi) of K.
+template <int FMT, int NT, typename Expert, typename Pair, typename Factor, typename Token>
+__device__ __forceinline__ void dn_stream(const uint8_t* w, const uint8_t* ws, const float* wf, int H, int K, int n0, int lo, int hi, int a0, int a1,
+                                          const uint16_t* h, uint32_t h_bytes, int PP, uint8_t* smem, Expert expert, Pair pair, Factor factor, Token token) {
+  using B = Blk<FMT>;
+  constexpr int D = kDnRing, ND = B::NDMA;
+  static_assert(D == 4, "the waits below count 3 blocks");
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t rb = code_row_bytes<FMT>(K), rs = scale_row_bytes<FMT>(K);
+  uint8_t* ring = smem + wave * dn_ring<FMT>();
+  uint8_t* hbuf = smem + kDnWaves * dn_ring<FMT>();
+  const int RC = K / 8, rows = PP * NT, hbytes = rows * RC * 16;  // 16-byte chunks of a row of h
+  float* yl = reinterpret_cast<float*>(hbuf + 2 * hbytes) + wave * 256;
 #pragma unroll
-  for (int u = 0; u < kDnAhead; ++u) load_wstep<FMT>(v[u], row, srow, min(kb0 + u, KB - 1), g, K);
-  floatx4 p[NT];
+  for (int q = 0; q < 4; ++q) yl[q * 64 + lane] = 0.0f;
+  const bool strip_on = n0 < H, dma_scales = (rs & 3) == 0;  // H is a multiple of 32, not of 128: a wave may have no strip
+  // load cursor of the weights: (expert, pass, block)
+  Strip<FMT> st;
+  int li = a0, lp = 0, lb = lo;
+  auto set_strip = [&](int i) __attribute__((always_inline)) {
+    const int64_t row = (int64_t)expert(i).x * H + n0;
+    st.set(w + row * rb, ws + row * rs, rb, rs);
+  };
+  auto load_next = [&](int slot) __attribute__((always_inline)) {
+    if (lb == lo) set_strip(min(li, a1 - 1));
+    load_block<FMT>(st, lb, rb, rs, ring + slot * B::SLOT);
+    if (++lb == hi) {
+      lb = lo;
+      lp += PP;
+      if (li < a1 && lp >= expert(li).y) { lp = 0; ++li; }
+    }
+  };
+  // h of the pass (expert i, pairs from p0) into buffer `buf`: chunk c of row q at place c + q (mod RC), so that the
+  // 16 lanes that read one chunk of 16 rows hit different banks
+  const uint32_t inv = 0xFFFFFFFFu / (uint32_t)RC + 1;  // s / RC = (s inv) >> 32 for s < 2^16
+  const auto hb = buffer_of(h, h_bytes);
+  auto load_h = [&](int i, int p0, int buf) __attribute__((always_inline)) {
+    const int n = expert(i).y - p0;
+    for (int s0 = wave * 64; s0 < rows * RC; s0 += kDnWaves * 64) {
+      const uint32_t s = (uint32_t)min(s0 + lane, rows * RC - 1), row = __umulhi(s, inv), at = s - row * RC;
+      const int rot = RC >= 16 ? (int)row : 0, c = (int)at - rot + ((int)at < rot ? RC : 0);
+      const int t = (int)row / PP, q = (int)row - t * PP;
+      const int p = pair(i, p0 + (q < n ? q : 0));  // rows past the pairs repeat the first; their columns are not kept
+      if (s0 + lane < rows * RC) dma_buffer(hb, (uint32_t)(2 * ((p * NT + t) * K + 8 * c)), 0, hbuf + buf * hbytes + 16 * s0);
+    }
+  };
+  if (a0 < a1) {
+    load_h(a0, 0, 0);
+    if (strip_on) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t) p[t] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int u = 0; u < kDnAhead; ++u) {
-    if (kb0 + u < KB) {
-      const int k0 = 128 * (kb0 + u) + 32 * g;
-      u32x4 hv[NT][4];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) hv[t][j] = u32x4{0, 0, 0, 0};
-      if (hrow && k0 < K) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) hv[t][j] = ld16(hrow + (int64_t)t * K + k0 + 8 * j);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bf16x8_t w = wstep_frag<FMT>(v[u], j);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          p[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8_t, hv[t][j]), p[t], 0, 0, 0);
-      }
-      if (FMT == FP4_FMT_FP8_BLOCK) {
-        const float s = hrow ? hf[kb0 + u] * fw[kb0 + u] * f : 0.0f;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[q] = fmaf(p[0][q], s, acc[q]);
-        p[0] = floatx4{0.f, 0.f, 0.f, 0.f};
-      }
+      for (int d = 0; d < D - 1; ++d) load_next(d);
     }
   }
-  if (FMT != FP4_FMT_FP8_BLOCK) {
+  int slot = 0, buf = 0;
+  const int hr = r < rows ? r : 0, rot = RC >= 16 ? hr : 0;
+  for (int i = a0, p0 = 0; i < a1;) {
+    const int n = expert(i).y;
+    int ni = i, np = p0 + PP;
+    if (np >= n) { np = 0; ++ni; }
+    // h of this pass was issued a pass ago (the first before the ring's first D - 1 blocks): only the weight blocks
+    // issued since may still be on their way
+    if (!strip_on || !dma_scales) __builtin_amdgcn_s_waitcnt(0);
+    else if (hi - lo >= 3) __builtin_amdgcn_s_waitcnt(vmcnt_only(3 * ND));
+    else if (hi - lo == 2) __builtin_amdgcn_s_waitcnt(vmcnt_only(2 * ND));
+    else __builtin_amdgcn_s_waitcnt(vmcnt_only(ND));
+    asm volatile("s_barrier" ::: "memory");  // h of this pass is there for every wave, and every wave is past the last one's
+    if (ni < a1) load_h(ni, np, buf ^ 1);
+    const uint8_t* hrow = hbuf + buf * hbytes + hr * RC * 16;
+    floatx4 acc{0.f, 0.f, 0.f, 0.f};
+    if (strip_on) {
+      const float* fw = FMT == FP4_FMT_FP8_BLOCK ? wf + ((int64_t)expert(i).x * (H / 128) + n0 / 128) * (K / 128) : nullptr;
+      for (int blk = lo; blk < hi; ++blk) {
+        load_next(slot == 0 ? D - 1 : slot - 1);
+        if (dma_scales) __builtin_amdgcn_s_waitcnt(vmcnt_only(ND * (D - 1)));
+        else __builtin_amdgcn_s_waitcnt(0);
+        asm volatile("" ::: "memory");
+        const uint8_t* at = ring + slot * B::SLOT;
+        slot = slot == D - 1 ? 0 : slot + 1;
 #pragma unroll
-    for (int t = 1; t < NT; ++t) p[0] += p[t];
+        for (int s = 0; s < B::STEPS; ++s) {
+          const int kb = blk * B::STEPS + s;
+          if (128 * kb < K) {
+            WStep<FMT> v;
+            v.read(at, s, g, r);
+            floatx4 pr = FMT == FP4_FMT_FP8_BLOCK ? floatx4{0.f, 0.f, 0.f, 0.f} : acc;
+            const bool in = 128 * kb + 32 * g < K;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) acc[q] = fmaf(p[0][q], f, acc[q]);
+            for (int q = 0; q < 4; ++q) {
+              int c = 16 * kb + 4 * g + q + rot;
+              c -= c >= RC ? RC : 0;
+              u32x4 hv = ld16(hrow + 16 * (in ? c : 0));
+              if (!in) hv = u32x4{0, 0, 0, 0};
+              pr = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wstep_frag<FMT>(v, q), __builtin_bit_cast(bf16x8_t, hv), pr, 0, 0, 0);
+            }
+            if (FMT == FP4_FMT_FP8_BLOCK) {
+              const float f = scalar_load(fw + kb);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) acc[q] = fmaf(pr[q], f, acc[q]);
+            } else {
+              acc = pr;
+            }
+          }
+        }
+      }
+      // the terms' columns of a pair add up, then go to its token's outputs (a token is in an expert's list once)
+      floatx4 v = acc;
+      if constexpr (NT == 3) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] += __shfl(acc[q], lane + PP) + __shfl(acc[q], lane + 2 * PP);
+      }
+      if (r < PP && p0 + r < n) {
+        const float f = factor(i, p0 + r);
+        floatx4* y = reinterpret_cast<floatx4*>(yl + token(pair(i, p0 + r)) * 16 + 4 * g);
+        floatx4 o = *y;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q] = fmaf(v[q], f, o[q]);
+        *y = o;
+      }
+    }
+    buf ^= 1;
+    i = ni;
+    p0 = np;
   }
+  __builtin_amdgcn_s_waitcnt(vmcnt_only(0));  // no DMA outlives the workgroup
 }
 
-// 16 outputs of y for all tokens per workgroup; its waves share the touched
-// experts (in chunks of kDnAhead K steps) and the shared expert.
+// Grid: (row groups of 128 outputs, splits).  A split takes a run of the
+// touched experts, or (the last shared_splits) a run of K of the shared
+// expert, and leaves its sums in ypart; the last of a row group to arrive adds
+// all splits up, in their order, and writes y.  Partial sums are stored and
+// read at device scope, past the XCDs' L2s; no workgroup waits for another.
 template <int MODE, typename OutT>
-__global__ void __launch_bounds__(64 * kDnWaves) few_down_kernel(FewArgs a) {
-  constexpr int WF = weight_fmt(MODE), AF = act_fmt(MODE), NT = AF == FP4_FMT_NONE ? 3 : 1;
-  __shared__ float part[kDnWaves][kFewTokens][17];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, r = lane & 15;
-  const int T = a.T, I = a.I, H = a.H, KB = (I + 127) / 128, chunks = (KB + kDnAhead - 1) / kDnAhead;
-  const int n0 = blockIdx.x * 16;
-  const int nd = a.list[0], items = nd * chunks;
-  const int schunks = (a.S / 128 + kDnAhead - 1) / kDnAhead;
-  const int64_t rb = code_row_bytes<WF>(I), rs = scale_row_bytes<WF>(I);
-  floatx4 acc{0.f, 0.f, 0.f, 0.f};
-  for (int it = wave; it < items + schunks; it += kDnWaves) {
-    if (it < items) {
-      const int ai = it / chunks, kb0 = (it - ai * chunks) * kDnAhead;
-      const int e = a.list[1 + ai], p = a.slot[ai * kFewTokens + r];
-      float f = p >= 0 ? a.wts[p] : 0.0f;
+__global__ void __launch_bounds__(64 * kDnWaves, 2) few_down_kernel(FewArgs a) {
+  constexpr int WF = weight_fmt(MODE), AF = act_fmt(MODE), NT = AF == FP4_FMT_NONE || AF == FP4_FMT_FP8_ROW ? 3 : 1;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ int2 s_expert[kDnSeg];                 // this split's experts: number, pairs
+  __shared__ int16_t s_pair[kDnSeg][kFewTokens];
+  __shared__ float s_factor[kDnSeg][kFewTokens];    // routing weight times the tensor scales
+  __shared__ int s_last;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int T = a.T, H = a.H, k = a.k, split = blockIdx.y, total = gridDim.y;
+  const int n0 = blockIdx.x * 128 + wave * 16;
+  const float* yl;
+  if (split < a.splits) {
+    const int nd = a.list[0], a0 = split * nd / a.splits, a1 = (split + 1) * nd / a.splits;
+    for (int i = tid; i < (a1 - a0) * kFewTokens; i += 64 * kDnWaves) {
+      const int e = a.list[1 + a0 + (i >> 4)], p = a.pairs[a0 * kFewTokens + i];
+      float f = a.wts[max(p, 0)];
       if (WF == FP4_FMT_NVFP4) f *= a.w2s2[e];
       if (AF == FP4_FMT_NVFP4) f *= a.h_ts[0];
-      const int64_t row = (int64_t)e * H + n0 + r;
-      const float* fw = WF == FP4_FMT_FP8_BLOCK ? static_cast<const float*>(a.w2s) + ((int64_t)e * (H / 128) + n0 / 128) * KB : nullptr;
-      dn_item<WF, NT>(a.w2 + row * rb, static_cast<const uint8_t*>(a.w2s) + row * rs, fw,
-                      p >= 0 ? a.hb + (int64_t)p * NT * I : nullptr, a.hf + (int64_t)max(p, 0) * KB, I, kb0, g, f, acc);
-    } else {
-      const int S = a.S;
-      const int64_t row = n0 + r;
-      dn_item<FP4_FMT_MXFP8, 1>(a.ws2 + row * S, a.ws2s + row * (S / 32), nullptr, r < T ? a.shb + (int64_t)r * S : nullptr,
-                                nullptr, S, (it - items) * kDnAhead, g, r < T ? a.sgate[r] : 0.0f, acc);
+      s_pair[i >> 4][i & 15] = (int16_t)p;
+      s_factor[i >> 4][i & 15] = f;
+      const uint64_t on = __ballot(p >= 0) >> (threadIdx.x & 48) & 0xFFFFull;  // 16 lanes hold one expert's pairs
+      if ((i & 15) == 0) s_expert[i >> 4] = int2{e, __popcll(on)};
     }
+    __syncthreads();
+    dn_stream<WF, NT>(
+        a.w2, static_cast<const uint8_t*>(a.w2s), static_cast<const float*>(a.w2s), H, a.I, n0, 0, (a.I + Blk<WF>::K - 1) / Blk<WF>::K, 0, a1 - a0,
+        a.hb, (uint32_t)(T * k) * NT * a.I * 2, a.pass_pairs, smem,
+        [&](int i) __attribute__((always_inline)) {
+          return int2{__builtin_amdgcn_readfirstlane(s_expert[i].x), __builtin_amdgcn_readfirstlane(s_expert[i].y)};
+        },
+        [&](int i, int q) __attribute__((always_inline)) { return (int)s_pair[i][q]; },
+        [&](int i, int q) __attribute__((always_inline)) { return s_factor[i][q]; },
+        [&](int p) __attribute__((always_inline)) { return p / k; });
+    yl = reinterpret_cast<const float*>(smem + kDnWaves * dn_ring<WF>() + 2 * a.pass_pairs * NT * a.I * 2);
+  } else {
+    const int S = a.S, NB = S / 128, sp = split - a.splits, PP = min(a.shared_pairs, T);
+    if (tid < T) s_factor[0][tid] = a.sgate[tid];
+    __syncthreads();
+    dn_stream<FP4_FMT_MXFP8, 1>(
+        a.ws2, a.ws2s, nullptr, H, S, n0, sp * NB / a.shared_splits, (sp + 1) * NB / a.shared_splits, 0, 1, a.shb, (uint32_t)(T * S * 2), PP, smem,
+        [&](int) __attribute__((always_inline)) { return int2{0, T}; }, [](int, int q) __attribute__((always_inline)) { return q; },
+        [&](int, int q) __attribute__((always_inline)) { return s_factor[0][q]; }, [](int p) __attribute__((always_inline)) { return p; });
+    yl = reinterpret_cast<const float*>(smem + kDnWaves * dn_ring<FP4_FMT_MXFP8>() + 2 * PP * S * 2);
   }
-#pragma unroll
-  for (int q = 0; q < 4; ++q) part[wave][r][4 * g + q] = acc[q];
   __syncthreads();
-  if (tid < 256 && (tid >> 4) < T) {
-    const int t = tid >> 4, n = tid & 15;
-    float s = 0.0f;
+  // element q of this row group: token q / 128, output q % 128
+  const int cols = min(128, H - (int)blockIdx.x * 128);
+  auto own = [&](int q) __attribute__((always_inline)) { return yl[((q & 127) >> 4) * 256 + (q >> 7) * 16 + (q & 15)]; };
+  auto store = [&](int q, float v) __attribute__((always_inline)) {
+    OutT* y = static_cast<OutT*>(a.y) + (int64_t)(q >> 7) * H + blockIdx.x * 128 + (q & 127);
+    if constexpr (sizeof(OutT) == 4) *y = v;
+    else *y = __builtin_bit_cast(uint16_t, (__bf16)v);
+  };
+  if (total == 1) {
+    for (int q = tid; q < T * 128; q += 64 * kDnWaves)
+      if ((q & 127) < cols) store(q, own(q));
+    return;
+  }
+  auto part = [&](int s, int q) __attribute__((always_inline)) { return a.ypart + ((int64_t)s * T + (q >> 7)) * H + blockIdx.x * 128 + (q & 127); };
+  for (int q = tid; q < T * 128; q += 64 * kDnWaves)
+    if ((q & 127) < cols) __hip_atomic_store(part(split, q), own(q), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __builtin_amdgcn_s_waitcnt(0);  // this thread's stores acknowledged
+  __syncthreads();
+  if (tid == 0) s_last = __hip_atomic_fetch_add(a.done + blockIdx.x, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == total - 1;
+  __syncthreads();
+  if (!s_last) return;
+  for (int q = tid; q < T * 128; q += 64 * kDnWaves) {
+    if ((q & 127) >= cols) continue;
+    float v = 0.0f;
+    for (int s0 = 0; s0 < total; s0 += 8) {
+      float t[8];
 #pragma unroll
-    for (int w = 0; w < kDnWaves; ++w) s += part[w][t][n];
-    OutT* y = static_cast<OutT*>(a.y) + (int64_t)t * H + n0 + n;
-    if constexpr (sizeof(OutT) == 4) *y = s;
-    else *y = __builtin_bit_cast(uint16_t, (__bf16)s);
+      for (int s = 0; s < 8; ++s) t[s] = __hip_atomic_load(part(min(s0 + s, total - 1), q), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+      for (int s = 0; s < 8; ++s) v += s0 + s < total ? t[s] : 0.0f;
+    }
+    store(q, v);
   }
 }
 
 // --------------------------------------------------------------------- host
 
 struct FewPlan {
-  int mode;
-  size_t ids, wts, list, slot, sgate, amax_part, h_ts, h, hb, hf, sh, shb, total;
+  int mode, splits, shared_splits, pass_pairs, shared_pairs;
+  int nw, deep;  // gate_up: waves of a workgroup, ring of 4 blocks instead of 2
+  size_t wts, list, pairs, done, sgate, amax_part, h_ts, h, hb, sh, shb, ypart, total;
 };
 
-constexpr int kFewMaxWgs = 2048;
+constexpr int kFewCus = 256;        // workgroups that a launch aims at: the card's compute units
+constexpr int kLds = 160 * 1024;
+constexpr int kGuLds = kLds - 64;   // dynamic LDS beside the gate_up kernel's static bytes
+constexpr int kDnHBytes = 48 * 1024;  // LDS for h of two passes
+
+static int ring_slot(int w_fmt) {  // gate and up block
+  const int slot = w_fmt == FP4_FMT_NVFP4 ? Blk<FP4_FMT_NVFP4>::SLOT : w_fmt == FP4_FMT_MXFP4 ? Blk<FP4_FMT_MXFP4>::SLOT : Blk<FP4_FMT_FP8_BLOCK>::SLOT;
+  return 2 * std::max(slot, Blk<FP4_FMT_MXFP8>::SLOT);
+}
 
 static int few_plan(const moe_fp4_layer* L, int64_t T, FewPlan* out) {
   FP4_CHECK(validate_layer(L, T));
   if (T > kFewTokens) return fail(FP4_ERR_UNSUPPORTED, "few-token forward: %lld tokens, at most %d", (long long)T, kFewTokens);
   if (L->num_experts > 1024) return fail(FP4_ERR_UNSUPPORTED, "few-token forward: more than 1024 experts");
-  if (gu_smem((int)T, L->num_experts, L->top_k, L->hidden).total > 159 * 1024)
-    return fail(FP4_ERR_UNSUPPORTED, "few-token forward: %lld tokens of width %d do not fit the LDS", (long long)T, L->hidden);
+  if (L->hidden > 1 << 16 || L->inter > 1 << 16 || L->shared_inter > 1 << 16)
+    return fail(FP4_ERR_UNSUPPORTED, "few-token forward: a width above 65536");
   const bool nv = L->w_fmt == FP4_FMT_NVFP4;
   FewPlan p{};
   p.mode = L->w_fmt == FP4_FMT_FP8_BLOCK ? FM_FP8 : L->a_fmt == FP4_FMT_NONE ? (nv ? FM_NV : FM_MX) : (nv ? FM_NVNV : FM_MXMX);
-  const size_t P = (size_t)T * L->top_k, D = std::min<size_t>(P, L->num_experts), I = L->inter, S = L->shared_inter;
+  const int nt = L->a_fmt == FP4_FMT_NONE || L->a_fmt == FP4_FMT_FP8_ROW ? 3 : 1;
+  const size_t P = (size_t)T * L->top_k, D = std::min<size_t>(P, L->num_experts), I = L->inter, S = L->shared_inter, H = L->hidden;
+  // gate_up: the most waves whose rings fit beside x, with deep rings if they fit
+  const int rings[][2] = {{8, 4}, {8, 2}, {4, 2}, {2, 2}, {1, 2}};
+  for (auto& r : rings)
+    if (p.nw == 0 && gu_smem((int)T, L->num_experts, L->top_k, L->hidden, r[0], r[1] * ring_slot(L->w_fmt), true).total <= kGuLds) {
+      p.nw = r[0];
+      p.deep = r[1] == 4;
+    }
+  if (p.nw == 0 && T > 0)
+    return fail(FP4_ERR_UNSUPPORTED, "few-token forward: %lld tokens of width %d do not fit the LDS", (long long)T, L->hidden);
+  p.pass_pairs = (int)std::min<size_t>(std::min<size_t>(16 / nt, std::max<int64_t>(T, 1)), kDnHBytes / (4 * nt * I));
+  p.shared_pairs = S ? (int)std::min<size_t>(8, kDnHBytes / (4 * S)) : 1;
+  if (p.pass_pairs < 1 || p.shared_pairs < 1) return fail(FP4_ERR_UNSUPPORTED, "few-token forward: intermediate width too large for the LDS");
+  // down: splits of a row group, so that the launch has about a workgroup per compute unit
+  const int64_t groups = (H + 127) / 128;
+  p.shared_splits = S ? (int)std::max<size_t>(1, std::min<size_t>(S / 128, (S + 319) / 320)) : 0;
+  p.splits = (int)std::max<int64_t>((D + kDnSeg - 1) / kDnSeg, std::min<int64_t>(D, std::max<int64_t>(1, kFewCus / groups - p.shared_splits)));
+  p.splits = std::max(p.splits, 1);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
     off += (bytes + 255) / 256 * 256;
     return at;
   };
-  p.ids = take(4 * P);
   p.wts = take(4 * P);
   p.list = take(4 * (1 + D));
-  p.slot = take(4 * D * kFewTokens);
+  p.pairs = take(4 * D * kFewTokens);
+  p.done = take(4 * groups);
   p.sgate = take(4 * T);
-  p.amax_part = take(4 * kFewMaxWgs);
+  p.amax_part = take(4 * 2 * kFewCus);
   p.h_ts = take(4);
   p.h = take(L->a_fmt == FP4_FMT_NONE ? 0 : 4 * P * I);
-  p.hb = take((L->a_fmt == FP4_FMT_NONE ? 6 : 2) * P * I);
-  p.hf = take(L->a_fmt == FP4_FMT_FP8_ROW ? 4 * P * (I / 128) : 0);
+  p.hb = take(2 * nt * P * I);
   p.sh = take(4 * T * S);
   p.shb = take(2 * T * S);
+  p.ypart = take(4 * (size_t)(p.splits + p.shared_splits) * T * H);
   p.total = off;
   *out = p;
   return FP4_OK;
 }
 
-template <int MODE>
-static int launch_few(FewArgs a, int y_dtype, hipStream_t st) {
-  constexpr int AF = act_fmt(MODE);
-  static std::atomic<uint64_t> lds_raised{0};
-  FP4_CHECK(raise_dyn_lds(reinterpret_cast<const void*>(&few_gateup_kernel<MODE>), 159 * 1024, lds_raised));
-  const int cus = device_cu_count();
-  const GuSmem sm = gu_smem(a.T, a.E, a.k, a.H);
-  // workgroups that fit the chip at once, shared between the routed and the shared expert by bytes
-  const int fit = cus * std::max(1, std::min(2, (160 * 1024) / (sm.total + 1024)));
-  const int strips = a.I / 16;
-  const int max_units = std::min(a.E, a.T * a.k) * strips;
-  int shared = 0;
+template <int MODE, int D>
+static int launch_few(FewArgs a, const FewPlan& p, int y_dtype, hipStream_t st) {
+  constexpr int AF = act_fmt(MODE), WF = weight_fmt(MODE), NT = AF == FP4_FMT_NONE || AF == FP4_FMT_FP8_ROW ? 3 : 1;
+  static std::atomic<uint64_t> gu_raised{0}, dn32_raised{0}, dn16_raised{0};
+  FP4_CHECK(raise_dyn_lds(reinterpret_cast<const void*>(&few_gateup_kernel<MODE, D>), kGuLds, gu_raised));
+  const int ring = D * ring_slot(WF), strips = a.I / 16, max_units = std::min(a.E, a.T * a.k) * strips;
+  // a unit is split between waves (each a run of K) until the units there may be fill the chip's waves
+  a.k_split = 1;
+  while (a.k_split < p.nw && max_units * a.k_split < kFewCus * p.nw) a.k_split *= 2;
+  const int lds = gu_smem(a.T, a.E, a.k, a.H, p.nw, ring, a.k_split > 1).total;
+  const int per = p.nw / a.k_split, fit = kFewCus * std::max(1, std::min(2, kLds / (lds + 64)));
+  int shared = 0;  // workgroups of the shared expert, by its share of the bytes
   if (a.S > 0) {
     const double sb = 2.0 * a.S, rb = (double)std::min(a.E, a.T * a.k) * 2 * a.I * (MODE == FM_FP8 ? 1.0 : 0.55);
-    shared = std::max(1, std::min(a.S / 16, (int)(fit * sb / (sb + rb))));
+    shared = std::max(1, std::min((a.S / 16 + per - 1) / per, (int)(fit * sb / (sb + rb))));
   }
-  // waves per unit: as many as leave every workgroup of the chip a unit
-  a.k_split = 1;
-  while (a.k_split < kGuWaves && max_units * a.k_split < fit * kGuWaves) a.k_split *= 2;
-  const int per = kGuWaves / a.k_split;
-  a.routed_wgs = std::max(1, std::min(std::min(fit - shared, kFewMaxWgs), (max_units + per - 1) / per));
-  hipLaunchKernelGGL(few_gateup_kernel<MODE>, dim3((unsigned)(a.routed_wgs + shared)), dim3(64 * kGuWaves), (size_t)sm.total, st, a);
+  a.routed_wgs = std::max(1, std::min(fit - shared, (max_units + per - 1) / per));
+  hipLaunchKernelGGL((few_gateup_kernel<MODE, D>), dim3((unsigned)(a.routed_wgs + shared)), dim3(64 * p.nw), (size_t)lds, st, a);
   FP4_CHECK(check_launch("few_gateup"));
   const int64_t lanes = (AF == FP4_FMT_NONE ? 0 : (int64_t)a.T * a.k * (a.I / 32)) + (int64_t)a.T * (a.S / 32);
   if (lanes > 0) {
     hipLaunchKernelGGL(few_hquant_kernel<AF>, dim3(grid_1d(lanes, 256)), dim3(256), 0, st, a);
     FP4_CHECK(check_launch("few_hquant"));
   }
-  const dim3 grid((unsigned)(a.H / 16)), block(64 * kDnWaves);
-  if (y_dtype == FP4_DT_F32) hipLaunchKernelGGL((few_down_kernel<MODE, float>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((few_down_kernel<MODE, uint16_t>), grid, block, 0, st, a);
+  const size_t routed_lds = kDnWaves * (dn_ring<WF>() + 1024) + 4 * (size_t)a.pass_pairs * NT * a.I;
+  const size_t shared_lds = a.S ? kDnWaves * (dn_ring<FP4_FMT_MXFP8>() + 1024) + 4 * (size_t)std::min(a.shared_pairs, a.T) * a.S : 0;
+  constexpr int dn_static = kDnSeg * (8 + kFewTokens * 6) + 64;
+  const size_t dn_lds = std::max(routed_lds, shared_lds);
+  if (dn_lds + dn_static > kLds) return fail(FP4_ERR_UNSUPPORTED, "few-token forward: down kernel needs %zu bytes of LDS", dn_lds);
+  const dim3 grid((unsigned)((a.H + 127) / 128), (unsigned)(a.splits + a.shared_splits)), block(64 * kDnWaves);
+  if (y_dtype == FP4_DT_F32) {
+    FP4_CHECK(raise_dyn_lds(reinterpret_cast<const void*>(&few_down_kernel<MODE, float>), kLds - dn_static, dn32_raised));
+    hipLaunchKernelGGL((few_down_kernel<MODE, float>), grid, block, dn_lds, st, a);
+  } else {
+    FP4_CHECK(raise_dyn_lds(reinterpret_cast<const void*>(&few_down_kernel<MODE, uint16_t>), kLds - dn_static, dn16_raised));
+    hipLaunchKernelGGL((few_down_kernel<MODE, uint16_t>), grid, block, dn_lds, st, a);
+  }
   return check_launch("few_down");
+}
+
+template <int MODE>
+static int launch_few(const FewArgs& a, const FewPlan& p, int y_dtype, hipStream_t st) {
+  return p.deep ? launch_few<MODE, 4>(a, p, y_dtype, st) : launch_few<MODE, 2>(a, p, y_dtype, st);
 }
 
 }  // namespace fp4
@@ -841,26 +1131,27 @@ int moe_fp4_forward_few(const moe_fp4_layer* L, const uint16_t* x, int64_t token
   a.x_scale = L->input_scale; a.h_scale = L->inter_scale;
   a.ws13 = L->ws13; a.ws13s = L->ws13_scale; a.ws2 = L->ws2; a.ws2s = L->ws2_scale; a.gate = L->shared_gate;
   a.T = (int)tokens; a.E = L->num_experts; a.k = L->top_k; a.H = L->hidden; a.I = L->inter; a.S = L->shared_inter;
-  a.ids = reinterpret_cast<int32_t*>(b + p.ids);
+  a.splits = p.splits; a.shared_splits = p.shared_splits; a.pass_pairs = p.pass_pairs; a.shared_pairs = p.shared_pairs;
   a.list = reinterpret_cast<int32_t*>(b + p.list);
-  a.slot = reinterpret_cast<int32_t*>(b + p.slot);
+  a.pairs = reinterpret_cast<int32_t*>(b + p.pairs);
+  a.done = reinterpret_cast<int32_t*>(b + p.done);
   a.wts = reinterpret_cast<float*>(b + p.wts);
   a.sgate = reinterpret_cast<float*>(b + p.sgate);
   a.amax_part = reinterpret_cast<float*>(b + p.amax_part);
   a.h_ts = reinterpret_cast<float*>(b + p.h_ts);
   a.h = reinterpret_cast<float*>(b + p.h);
   a.hb = reinterpret_cast<uint16_t*>(b + p.hb);
-  a.hf = reinterpret_cast<float*>(b + p.hf);
   a.sh = reinterpret_cast<float*>(b + p.sh);
   a.shb = reinterpret_cast<uint16_t*>(b + p.shb);
+  a.ypart = reinterpret_cast<float*>(b + p.ypart);
   a.ids_out = topk_ids; a.wts_out = topk_weights; a.y = y;
   hipStream_t st = as_stream(stream);
   switch (p.mode) {
-    case FM_NV: return launch_few<FM_NV>(a, y_dtype, st);
-    case FM_MX: return launch_few<FM_MX>(a, y_dtype, st);
-    case FM_NVNV: return launch_few<FM_NVNV>(a, y_dtype, st);
-    case FM_MXMX: return launch_few<FM_MXMX>(a, y_dtype, st);
-    default: return launch_few<FM_FP8>(a, y_dtype, st);
+    case FM_NV: return launch_few<FM_NV>(a, p, y_dtype, st);
+    case FM_MX: return launch_few<FM_MX>(a, p, y_dtype, st);
+    case FM_NVNV: return launch_few<FM_NVNV>(a, p, y_dtype, st);
+    case FM_MXMX: return launch_few<FM_MXMX>(a, p, y_dtype, st);
+    default: return launch_few<FM_FP8>(a, p, y_dtype, st);
   }
 }
 
