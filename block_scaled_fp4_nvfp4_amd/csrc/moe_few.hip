@@ -45,7 +45,6 @@ typedef float floatx4 __attribute__((ext_vector_type(4)));
 constexpr int kFewTokens = 16;  // columns of the MFMA tile
 constexpr int kGuWaves = 8;     // most waves per workgroup of the gate_up kernel
 constexpr int kDnWaves = 8;     // waves per workgroup of the down kernel, a strip of 16 outputs each
-constexpr int kDnRing = 4;      // blocks in a wave's ring of the down kernel
 constexpr int kDnSeg = 64;      // most experts of one split
 
 // format pairs of the layer
@@ -96,78 +95,90 @@ __device__ __forceinline__ float ue8m0_f32(uint32_t c) {
   return c ? __uint_as_float(c << 23) : 5.877471754111438e-39f;  // 2^-127
 }
 
-// A block of a strip: 16 weight rows x 128 bytes of codes (K values 256 wide
-// in E2M1, 128 in E4M3) and their scale bytes, as a ring slot holds them: the
-// rows' 16-byte chunks XOR-swizzled by the row, then the scales row by row.
+// A block: 16 weight rows (one strip) x one 128-wide K step, as a ring slot
+// holds it: the rows' 16-byte chunks of codes XOR-swizzled by the row, then
+// their block scales row by row.  gate_up's slots hold a gate and an up block:
+// codes, codes, scales, scales.
 template <int FMT>
 struct Blk {
   static constexpr bool FP4 = FMT == FP4_FMT_NVFP4 || FMT == FP4_FMT_MXFP4;
-  static constexpr int K = FP4 ? 256 : 128, STEPS = K / 128;
-  static constexpr int SROW = FMT == FP4_FMT_NVFP4 ? 16 : FMT == FP4_FMT_MXFP4 ? 8 : FMT == FP4_FMT_MXFP8 ? 4 : 0;  // scale bytes a row
-  static constexpr int NDMA = SROW ? 3 : 2;           // DMA instructions of a strip's block
-  static constexpr int SLOT = 2048 + 16 * SROW;
+  static constexpr int ROW = FP4 ? 64 : 128, CODES = 16 * ROW;  // code bytes of a row, of a block
+  static constexpr int SROW = FMT == FP4_FMT_NVFP4 ? 8 : FMT == FP4_FMT_FP8_BLOCK ? 0 : 4;  // scale bytes of a row
+  static constexpr int NC = CODES / 1024;  // DMA instructions of a block's codes
+  static __device__ __forceinline__ int chunk(int c, int row) { return FP4 ? c ^ ((row >> 2) & 3) : c ^ (row >> 1); }
 };
+// bytes of a slot of `strips` blocks, and its DMA instructions
+template <int FMT>
+constexpr int slot_bytes(int strips) { return strips * (Blk<FMT>::CODES + 16 * Blk<FMT>::SROW); }
+template <int FMT>
+constexpr int slot_dmas(int strips) { return strips * Blk<FMT>::NC + (Blk<FMT>::SROW ? 1 : 0); }
 
-// A strip's tensors: 16 rows of codes and of scales.
+// One or two strips' tensors (gate rows and the up rows `up` bytes behind).
 template <int FMT>
 struct Strip {
   __amdgpu_buffer_rsrc_t codes, scales;
-  const uint8_t* srow;  // the scales' first row
-  __device__ __forceinline__ void set(const uint8_t* c, const uint8_t* sc, int64_t rb, int64_t rs) {
-    codes = buffer_of(c, (uint32_t)(16 * rb));
-    scales = buffer_of(sc, (uint32_t)(16 * rs));
+  const uint8_t* srow;
+  __device__ __forceinline__ void set(const uint8_t* c, const uint8_t* sc, uint32_t bytes, uint32_t sbytes) {
+    codes = buffer_of(c, bytes);
+    scales = buffer_of(sc, sbytes);
     srow = sc;
   }
 };
 
-// Loads block `blk` of a strip into `slot`.  Chunks and scales past a row's
-// end read the row's start (they meet zeros of x or h).  Scale rows that are no multiple of 4 bytes (K not a
+// Loads K step kb of NS strips (the second cup / sup bytes behind the first)
+// into `slot`.  Chunks and scales past a row's end read the row's start (they
+// meet zeros of x or h).  Scale rows that are no multiple of 4 bytes (K not a
 // multiple of 64 in NVFP4, of 128 in MXFP4) cannot be copied by DMA and go
 // through registers.
-template <int FMT>
-__device__ __forceinline__ void load_block(const Strip<FMT>& s, int blk, int64_t rb, int64_t rs, uint8_t* slot) {
+template <int FMT, int NS>
+__device__ __forceinline__ void load_slot(const Strip<FMT>& s, int kb, int rb, int rs, uint32_t cup, uint32_t sup, uint8_t* slot) {
   using B = Blk<FMT>;
+  constexpr int CPR = B::ROW / 16, RPI = 64 / CPR;  // 16-byte chunks of a row, rows of an instruction
   const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int row = 8 * j + (lane >> 3), at = 128 * blk + 16 * ((lane & 7) ^ (row >> 1));
-    dma_buffer(s.codes, (uint32_t)(row * (int)rb) + (at < (int)rb ? at : 0), 0, slot + 1024 * j);
-  }
+  for (int u = 0; u < NS; ++u)
+#pragma unroll
+    for (int j = 0; j < B::NC; ++j) {
+      const int row = RPI * j + lane / CPR, at = B::ROW * kb + 16 * B::chunk(lane % CPR, row);
+      dma_buffer(s.codes, (uint32_t)(row * rb + (at < rb ? at : 0)), u * cup, slot + u * B::CODES + 1024 * j);
+    }
   if constexpr (B::SROW > 0) {
-    uint8_t* to = slot + 2048;
+    uint8_t* to = slot + NS * B::CODES;
     if ((rs & 3) == 0) {
       constexpr int W = B::SROW / 4;  // dwords of a row's scales
-      const int row = lane / W, at = B::SROW * blk + 4 * (lane % W);
-      if (lane < 16 * W) dma_buffer4(s.scales, (uint32_t)(row * (int)rs + (at < (int)rs ? at : 0)), 0, to);
+      const int row = (lane / W) & 15, u = lane / (16 * W), at = B::SROW * kb + 4 * (lane % W);
+      if (lane < NS * 16 * W) dma_buffer4(s.scales, (uint32_t)(row * rs + (at < rs ? at : 0)) + (uint32_t)u * sup, 0, to);
     } else {
-      for (int i = lane; i < 16 * B::SROW; i += 64) {
-        const int row = i / B::SROW, at = B::SROW * blk + i % B::SROW;
-        to[i] = at < (int)rs ? s.srow[row * rs + at] : 0;
+      for (int i = lane; i < NS * 16 * B::SROW; i += 64) {
+        const int row = (i / B::SROW) & 15, u = i / (16 * B::SROW), at = B::SROW * kb + i % B::SROW;
+        to[i] = at < rs ? s.srow[(int64_t)u * sup + row * rs + at] : 0;
       }
     }
   }
 }
 
-// Values 8j .. 8j+7 of a lane's 32 (K values [128 step + 32 g, + 32) of the
-// block, row r) as bf16 (exact).
+// A lane's 32 values (K values [32 g, + 32) of the step, row r) of strip u.
 template <int FMT>
 struct WStep {
   u32x4 c[Blk<FMT>::FP4 ? 1 : 2];
   uint32_t s;
-  __device__ __forceinline__ void read(const uint8_t* slot, int step, int g, int r) {
-    const uint8_t* row = slot + 128 * r;
-    if constexpr (Blk<FMT>::FP4) {
-      c[0] = ld16(row + 16 * ((4 * step + g) ^ (r >> 1)));
+  template <int NS>
+  __device__ __forceinline__ void read(const uint8_t* slot, int u, int g, int r) {
+    using B = Blk<FMT>;
+    const uint8_t* row = slot + u * B::CODES + B::ROW * r;
+    if constexpr (B::FP4) {
+      c[0] = ld16(row + 16 * B::chunk(g, r));
     } else {
-      c[0] = ld16(row + 16 * ((2 * g) ^ (r >> 1)));
-      c[1] = ld16(row + 16 * ((2 * g + 1) ^ (r >> 1)));
+      c[0] = ld16(row + 16 * B::chunk(2 * g, r));
+      c[1] = ld16(row + 16 * B::chunk(2 * g + 1, r));
     }
-    if constexpr (FMT == FP4_FMT_NVFP4) s = *reinterpret_cast<const uint16_t*>(slot + 2048 + 16 * r + 8 * step + 2 * g);
-    else if constexpr (FMT == FP4_FMT_MXFP4) s = slot[2048 + 8 * r + 4 * step + g];
-    else if constexpr (FMT == FP4_FMT_MXFP8) s = slot[2048 + 4 * r + g];
+    const uint8_t* sr = slot + NS * B::CODES + (16 * u + r) * B::SROW;
+    if constexpr (FMT == FP4_FMT_NVFP4) s = *reinterpret_cast<const uint16_t*>(sr + 2 * g);
+    else if constexpr (B::SROW > 0) s = sr[g];
   }
 };
 
+// Values 8j .. 8j+7 of them as bf16 (exact).
 template <int FMT>
 __device__ __forceinline__ bf16x8_t wstep_frag(const WStep<FMT>& v, int j) {
   u32x4 p;
@@ -232,12 +243,10 @@ __device__ __forceinline__ float quantize32(float (&v)[32], float ts) {
     amax = fmaxf(amax, __shfl_xor(amax, 1));
     amax = fmaxf(amax, __shfl_xor(amax, 2));
     const float sigma = (float)((double)amax / 448.0);
-    const float sg = sigma > 0.0f ? sigma : 1.0f;
+    uint32_t d[8];
+    e4m3_codes<32>(v, sigma, d);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float q = __builtin_amdgcn_cvt_f32_fp8((int)e4m3_exact_quotient(fabsf(v[i]), sg), 0);
-      v[i] = copysignf(sigma > 0.0f ? q : 0.0f, v[i]);
-    }
+    for (int i = 0; i < 32; ++i) v[i] = __builtin_amdgcn_cvt_f32_fp8((int)(d[i >> 2] >> (8 * (i & 3))), 0);
     return sigma;
   } else if constexpr (FMT == FP4_FMT_NVFP4) {
 #pragma unroll
@@ -245,7 +254,9 @@ __device__ __forceinline__ float quantize32(float (&v)[32], float ts) {
       float amax = 0.0f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[16 * b + i]));
-      const uint32_t sc = ts > 0.0f ? e4m3_rne_sat_f64((double)amax / (6.0 * (double)ts)) : 0u;
+      uint32_t sc = 0xFFu;
+      if (ts > 0x1p-100f && ts < 0x1p100f) sc = e4m3_of_quotient(amax, amax / (6.0f * ts), 6.0f, ts);
+      if (sc == 0xFFu) sc = ts > 0.0f ? e4m3_rne_sat_f64((double)amax / (6.0 * (double)ts)) : 0u;  // subnormal scales
       const float s = __builtin_amdgcn_cvt_f32_fp8((int)sc, 0);
       const E2M1Thresholds th = e2m1_thresholds((double)s * (double)ts);
 #pragma unroll
@@ -318,55 +329,70 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
 }
 
 // One wave selects the k experts of one token: ids to LDS in order, and the
-// j-th selected value's key in lane j.  PL: experts per lane.
+// j-th selected value's key in lane j.  Lane l holds experts l + 64 i, sorted
+// once by key (stably: the lower id first); then each of the k rounds takes the
+// largest of the lanes' heads and pops it.
 template <int PL>
 __device__ __forceinline__ uint32_t select_topk(const float* logits, const float* bias, int E, int k, int* s_ids) {
   const int lane = threadIdx.x & 63;
   uint32_t key[PL];
+  int id[PL];
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
-    const int e = lane + 64 * i;
-    key[i] = e < E ? route_key(logits[e] + (bias ? bias[e] : 0.0f)) : 0u;
+    id[i] = lane + 64 * i;
+    key[i] = id[i] < E ? route_key(logits[id[i]] + (bias ? bias[id[i]] : 0.0f)) : 0u;
   }
-  uint32_t mine = 0;
-  for (int j = 0; j < k; ++j) {
-    uint32_t best = key[0];
 #pragma unroll
-    for (int i = 1; i < PL; ++i) best = max(best, key[i]);
-    const uint32_t top = wave_umax(best);
-    int id = -1;
-    if (top) {
-      // lowest id among the equal: experts lane + 64 i, so the lowest i, then the lowest lane
+  for (int pass = 0; pass < PL; ++pass)
 #pragma unroll
-      for (int i = PL - 1; i >= 0; --i) {
-        const uint64_t m = __ballot(key[i] == top);
-        if (m) id = 64 * i + __builtin_ctzll(m);
-      }
-#pragma unroll
-      for (int i = 0; i < PL; ++i)
-        if (id == lane + 64 * i) key[i] = 0u;
+    for (int i = pass & 1; i + 1 < PL; i += 2) {
+      const bool swap = key[i + 1] > key[i];
+      const uint32_t ka = key[i], kb = key[i + 1];
+      const int ia = id[i], ib = id[i + 1];
+      key[i] = swap ? kb : ka;
+      key[i + 1] = swap ? ka : kb;
+      id[i] = swap ? ib : ia;
+      id[i + 1] = swap ? ia : ib;
     }
-    if (lane == j) mine = top;
-    if (lane == 0) s_ids[j] = id;
+  uint32_t mine = 0;
+  int my_id = -1;
+  for (int j = 0; j < k; ++j) {
+    const uint32_t top = wave_umax(key[0]);
+    if (top == 0) break;  // nothing selectable is left: ids -1
+    uint64_t at = __ballot(key[0] == top);
+    int win = __builtin_ctzll(at), e = __builtin_amdgcn_readlane(id[0], win);
+    for (at &= at - 1; at; at &= at - 1) {  // equal values: the lowest id
+      const int l = __builtin_ctzll(at), o = __builtin_amdgcn_readlane(id[0], l);
+      if (o < e) { e = o; win = l; }
+    }
+    if (lane == j) { mine = top; my_id = e; }
+    if (lane == win) {
+#pragma unroll
+      for (int i = 0; i + 1 < PL; ++i) { key[i] = key[i + 1]; id[i] = id[i + 1]; }
+      key[PL - 1] = 0u;
+    }
   }
+  if (lane < k) s_ids[lane] = my_id;
   return mine;
 }
 
 // ------------------------------------------------------------------ gate_up
 
 struct GuSmem {
-  int x, xf, ids, mask, list, scale, slot, red, ring, total;
+  int x, xf, ids, mask, place, list, scale, slot, red, ring, total;
 };
-// byte offsets of the gate_up kernel's dynamic LDS: nw waves with `ring` bytes
-// each, their partial sums if a unit is split between waves
-__host__ __device__ inline GuSmem gu_smem(int T, int E, int k, int K, int nw, int ring, bool split) {
+// byte offsets of the gate_up kernel's dynamic LDS: x~ (with `factors` one per
+// token and K step), the routing's tables, nw waves with `ring` bytes each, their
+// partial sums if a unit is split between waves
+__host__ __device__ inline GuSmem gu_smem(int T, int E, int k, int K, bool factors, int nw, int ring, bool split) {
   GuSmem s;
   const int kp = (K + 127) / 128 * 128, D = E < T * k ? E : T * k;
   s.x = 0;  // rows padded by 16 bytes: 16 lanes that read one chunk of 16 rows hit different banks
   s.xf = s.x + T * (kp + 8) * 2;
-  s.ids = s.xf + T * (kp / 128) * 4;
+  s.ids = s.xf + (factors ? T * (kp / 128) * 4 : 0);
   s.mask = s.ids + T * k * 4;
-  s.list = s.mask + E * 4;
+  s.place = s.mask + E * 4;
+  s.list = s.place + (E + 1) / 2 * 4;
   s.scale = s.list + (D + 1) * 4;
   s.slot = s.scale + D * 4;
   s.red = (s.slot + D * kFewTokens + 15) / 16 * 16;
@@ -403,16 +429,21 @@ __device__ float prepare_x(const FewArgs& a, uint8_t* sx, float* xf, float* tmp)
       ts = (float)((double)m / kNvTensorDivisor);
     }
   }
+  if constexpr (AF == FP4_FMT_NONE) {  // as it is, by DMA; the caller's barrier waits for it
+    const auto xb = buffer_of(a.x, (uint32_t)(T * H * 2));
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    for (int t = wave; t < T; t += (int)blockDim.x >> 6) {
+      for (int c = 0; c < H / 8; c += 64)
+        if (c + lane < H / 8) dma_buffer(xb, (uint32_t)(t * H * 2 + 16 * (c + lane)), 0, sx + t * (kp + 8) * 2 + 16 * c);
+      if (H / 8 + lane < kp / 8) st16(sx + t * (kp + 8) * 2 + 16 * (H / 8 + lane), u32x4{0, 0, 0, 0});
+    }
+    return 1.0f;
+  }
   const int per = kp / 32;
   for (int c = threadIdx.x; c < T * per; c += (int)blockDim.x) {
     const int t = c / per, q = c - t * per;
     float v[32];
-    if (32 * q < H) {
-      load_bf16x32(a.x + (int64_t)t * H + 32 * q, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-    }
+    load_bf16x32(a.x + (int64_t)t * H + 32 * q, v);  // H is a multiple of 128 where x is quantized
     const float f = quantize32<AF>(v, ts);
     store_bf16x32(sx + (t * (kp + 8) + 32 * q) * 2, v);
     if (AF == FP4_FMT_FP8_ROW && (q & 3) == 0) xf[t * (kp / 128) + (q >> 2)] = f;
@@ -446,71 +477,66 @@ __device__ __forceinline__ void gu_reduce(floatx4& a, floatx4& b, float* red, in
 }
 
 // One wave's stream of gate_up units: in every round j < rounds it multiplies
-// the blocks [lo, hi) of a unit's 16 gate rows and 16 up rows with all
+// the K steps [lo, hi) of a unit's 16 gate rows and 16 up rows with all
 // tokens' x~ (if j < mine) and hands the sums to finish(j, gate, up).
-// strips(j, gate, up) gives a round's weight rows, scales(j) the first block
-// scales of block FP8.  A ring of D slots; the loads of the next D - 1 blocks
-// are on their way, over the rounds' borders.
-template <int FMT, int D, typename Strips, typename Scales, typename Finish>
-__device__ __forceinline__ void gu_stream(int rounds, int mine, int lo, int hi, int K, int64_t rb, int64_t rs, const uint8_t* sx, const float* xf,
-                                          int xt, uint8_t* ring, Strips strips, Scales scales, Finish finish) {
-  using B = Blk<FMT>;
-  constexpr int SLOT = 2 * B::SLOT, ND = 2 * B::NDMA;
+// strip(j, s) gives a round's weight rows, scales(j, ..) the first block scales
+// of block FP8, started() runs once the first loads are on their way.  A ring
+// of D slots; the next D - 1 are being loaded, over the rounds' borders.
+template <int FMT, int D, typename SetStrip, typename Scales, typename Started, typename Finish>
+__device__ __forceinline__ void gu_stream(int rounds, int mine, int lo, int hi, int K, int I, const uint8_t* sx, const float* xf, int xt, uint8_t* ring,
+                                          SetStrip strip, Scales scales, Started started, Finish finish) {
+  constexpr int SLOT = slot_bytes<FMT>(2), ND = slot_dmas<FMT>(2);
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15, kp = (K + 127) / 128 * 128;
+  const int rb = (int)code_row_bytes<FMT>(K), rs = (int)scale_row_bytes<FMT>(K);
+  const uint32_t cup = (uint32_t)I * (uint32_t)rb, sup = (uint32_t)I * (uint32_t)rs;
   const uint8_t* xrow = sx + (xt * (kp + 8) + 32 * g) * 2;
   const bool any = mine > 0 && hi > lo, dma_scales = (rs & 3) == 0;
-  Strip<FMT> sg, su;
+  Strip<FMT> st;
   int lj = 0, lb = lo;
   auto load_next = [&](int slot) __attribute__((always_inline)) {
-    if (lb == lo) strips(min(lj, mine - 1), sg, su);  // past the end the last unit again: every step issues as many loads
-    load_block<FMT>(sg, lb, rb, rs, ring + slot * SLOT);
-    load_block<FMT>(su, lb, rb, rs, ring + slot * SLOT + B::SLOT);
+    if (lb == lo) strip(min(lj, mine - 1), st);  // past the end the last unit again: every step issues as many loads
+    load_slot<FMT, 2>(st, lb, rb, rs, cup, sup, ring + slot * SLOT);
     if (++lb == hi) { lb = lo; ++lj; }
   };
   if (any) {
 #pragma unroll
     for (int d = 0; d < D - 1; ++d) load_next(d);
   }
+  started();
   int slot = 0;
   for (int j = 0; j < rounds; ++j) {
     floatx4 ag{0.f, 0.f, 0.f, 0.f}, au = ag;
     if (any && j < mine) {
       const float *fg = nullptr, *fu = nullptr;
       if (FMT == FP4_FMT_FP8_BLOCK) scales(j, fg, fu);
-      for (int blk = lo; blk < hi; ++blk) {
+      for (int kb = lo; kb < hi; ++kb) {
         load_next(slot == 0 ? D - 1 : slot - 1);
         if (dma_scales) __builtin_amdgcn_s_waitcnt(vmcnt_only(ND * (D - 1)));
         else __builtin_amdgcn_s_waitcnt(0);
         asm volatile("" ::: "memory");
         const uint8_t* at = ring + slot * SLOT;
         slot = slot == D - 1 ? 0 : slot + 1;
+        WStep<FMT> wg, wu;
+        wg.template read<2>(at, 0, g, r);
+        wu.template read<2>(at, 1, g, r);
+        floatx4 pg = ag, pu = au;
+        if (FMT == FP4_FMT_FP8_BLOCK) pg = pu = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int st = 0; st < B::STEPS; ++st) {
-          const int kb = blk * B::STEPS + st;
-          if (128 * kb < K) {
-            WStep<FMT> wg, wu;
-            wg.read(at, st, g, r);
-            wu.read(at + B::SLOT, st, g, r);
-            floatx4 pg = ag, pu = au;
-            if (FMT == FP4_FMT_FP8_BLOCK) pg = pu = floatx4{0.f, 0.f, 0.f, 0.f};
+        for (int q = 0; q < 4; ++q) {
+          const bf16x8_t xv = __builtin_bit_cast(bf16x8_t, ld16(xrow + (128 * kb + 8 * q) * 2));
+          pg = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wstep_frag<FMT>(wg, q), xv, pg, 0, 0, 0);
+          pu = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wstep_frag<FMT>(wu, q), xv, pu, 0, 0, 0);
+        }
+        if (FMT == FP4_FMT_FP8_BLOCK) {
+          const float f = xf[xt * (kp / 128) + kb], a = f * scalar_load(fg + kb), b = f * scalar_load(fu + kb);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const bf16x8_t xv = __builtin_bit_cast(bf16x8_t, ld16(xrow + (128 * kb + 8 * q) * 2));
-              pg = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wstep_frag<FMT>(wg, q), xv, pg, 0, 0, 0);
-              pu = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wstep_frag<FMT>(wu, q), xv, pu, 0, 0, 0);
-            }
-            if (FMT == FP4_FMT_FP8_BLOCK) {
-              const float f = xf[xt * (kp / 128) + kb], a = f * scalar_load(fg + kb), b = f * scalar_load(fu + kb);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                ag[q] = fmaf(pg[q], a, ag[q]);
-                au[q] = fmaf(pu[q], b, au[q]);
-              }
-            } else {
-              ag = pg;
-              au = pu;
-            }
+          for (int q = 0; q < 4; ++q) {
+            ag[q] = fmaf(pg[q], a, ag[q]);
+            au[q] = fmaf(pu[q], b, au[q]);
           }
+        } else {
+          ag = pg;
+          au = pu;
         }
       }
     }
@@ -518,6 +544,15 @@ __device__ __forceinline__ void gu_stream(int rounds, int mine, int lo, int hi, 
   }
   __builtin_amdgcn_s_waitcnt(vmcnt_only(0));  // no DMA outlives the workgroup
 }
+
+// a wave's ring of D slots; the shared expert's larger MXFP8 slots share its bytes (two at least)
+template <int MODE, int D>
+__host__ __device__ constexpr int gu_ring(bool shared) {
+  constexpr int own = D * slot_bytes<weight_fmt(MODE)>(2), sh = 2 * slot_bytes<FP4_FMT_MXFP8>(2);
+  return shared && sh > own ? sh : own;
+}
+template <int MODE, int D>
+constexpr int shared_depth() { return gu_ring<MODE, D>(true) / slot_bytes<FP4_FMT_MXFP8>(2); }
 
 template <int MODE, int D>
 __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a) {
@@ -528,11 +563,10 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
   const int tid = threadIdx.x, th = blockDim.x, nw = th >> 6, lane = tid & 63, g = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int T = a.T, k = a.k, H = a.H, P = T * k, split = a.k_split, ks = wave % split, per = nw / split;
-  constexpr int RING = D * 2 * Blk<WF>::SLOT, SRING = D * 2 * Blk<FP4_FMT_MXFP8>::SLOT;
-  const GuSmem sm = gu_smem(T, a.E, k, H, nw, RING > SRING ? RING : SRING, split > 1);
+  const GuSmem sm = gu_smem(T, a.E, k, H, AF == FP4_FMT_FP8_ROW, nw, gu_ring<MODE, D>(a.S > 0), split > 1);
   float* xf = reinterpret_cast<float*>(smem + sm.xf);
   float* red = reinterpret_cast<float*>(smem + sm.red);
-  uint8_t* ring = smem + sm.ring + wave * (RING > SRING ? RING : SRING);
+  uint8_t* ring = smem + sm.ring + wave * gu_ring<MODE, D>(a.S > 0);
   const int xt = min(r, T - 1);  // columns past the last token repeat it and are not kept
 
   if ((int)blockIdx.x >= a.routed_wgs) {  // shared expert
@@ -555,14 +589,13 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
     const int NB = H / 128, lo = ks * NB / split, hi = (ks + 1) * NB / split;
     const int base = (blockIdx.x - a.routed_wgs) * per, rounds = (units - base + wgs * per - 1) / (wgs * per);
     const int mine = max(0, (units - first + wgs * per - 1) / (wgs * per));
-    gu_stream<FP4_FMT_MXFP8, D>(
-        rounds, mine, lo, hi, H, H, H / 32, smem + sm.x, xf, xt, ring,
-        [&](int j, Strip<FP4_FMT_MXFP8>& sg, Strip<FP4_FMT_MXFP8>& su) __attribute__((always_inline)) {
+    gu_stream<FP4_FMT_MXFP8, shared_depth<MODE, D>()>(
+        rounds, mine, lo, hi, H, S, smem + sm.x, xf, xt, ring,
+        [&](int j, Strip<FP4_FMT_MXFP8>& st) __attribute__((always_inline)) {
           const int64_t row = 16 * (int64_t)(first + j * wgs * per);
-          sg.set(a.ws13 + row * H, a.ws13s + row * (H / 32), H, H / 32);
-          su.set(a.ws13 + (S + row) * H, a.ws13s + (S + row) * (H / 32), H, H / 32);
+          st.set(a.ws13 + row * H, a.ws13s + row * (H / 32), (uint32_t)(S + 16) * H, (uint32_t)(S + 16) * (H / 32));
         },
-        [](int, const float*&, const float*&) {},
+        [](int, const float*&, const float*&) {}, []() {},
         [&](int j, floatx4& ag, floatx4& au) __attribute__((always_inline)) {
           gu_reduce(ag, au, red, ks, split);
           if (j < mine && ks == 0 && r < T) {
@@ -576,10 +609,12 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
   }
 
   int* ids = reinterpret_cast<int*>(smem + sm.ids);
-  uint32_t* mask = reinterpret_cast<uint32_t*>(smem + sm.mask);  // tokens of an expert; then its place in the list above them
+  uint32_t* mask = reinterpret_cast<uint32_t*>(smem + sm.mask);    // tokens of an expert
+  uint16_t* place = reinterpret_cast<uint16_t*>(smem + sm.place);  // of a touched expert in the list
   int* list = reinterpret_cast<int*>(smem + sm.list);
   float* scale = reinterpret_cast<float*>(smem + sm.scale);
   uint8_t* slots = smem + sm.slot;  // [listed expert][token]: the token's slot + 1
+  if constexpr (AF == FP4_FMT_NONE) (void)prepare_x<AF>(a, smem + sm.x, xf, tmp);  // on its way while the tokens are routed
   for (int e = tid; e < a.E; e += th) mask[e] = 0;
   for (int i = tid; i < min(a.E, P) * kFewTokens / 4; i += th) reinterpret_cast<uint32_t*>(slots)[i] = 0;
   if (tid == 0) s_amax = 0;
@@ -604,36 +639,38 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
       }
     }
   }
-  const float xs = prepare_x<AF>(a, smem + sm.x, xf, tmp);
+  float xs = 1.0f;
+  if constexpr (AF != FP4_FMT_NONE) xs = prepare_x<AF>(a, smem + sm.x, xf, tmp);
+  __builtin_amdgcn_s_waitcnt(vmcnt_only(0));  // x by DMA: a barrier alone does not wait for it
   __syncthreads();
   for (int p = tid; p < P; p += th)
     if (ids[p] >= 0) atomicOr(&mask[ids[p]], 1u << (p / k));
   __syncthreads();
-  if (wave == 0) {  // the touched experts, by id
-    int n = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 64) {
-      const uint32_t m = e0 + lane < a.E ? mask[e0 + lane] : 0u;
-      const uint64_t on = __ballot(m != 0);
-      if (m) {
-        const int at = n + __popcll(on & ((1ull << lane) - 1));
-        list[1 + at] = e0 + lane;
-        mask[e0 + lane] = m | (uint32_t)at << 16;
-        scale[at] = WF == FP4_FMT_NVFP4 ? a.w13s2[e0 + lane] * xs : 1.0f;
-      }
-      n += __popcll(on);
+  // the touched experts by id: 64 to a ballot, every wave a run of them; the counts of the runs before come first
+  const int runs = (a.E + 63) / 64;
+  int before = 0;
+  for (int c = 0; c < runs; ++c) {
+    const int e = 64 * c + lane;
+    const uint32_t m = e < a.E ? mask[e] & 0xFFFFu : 0u;
+    const uint64_t on = __ballot(m != 0);
+    if (m && c % nw == wave) {
+      const int at = before + __popcll(on & ((1ull << lane) - 1));
+      list[1 + at] = e;
+      place[e] = (uint16_t)at;
     }
-    if (lane == 0) list[0] = n;
+    before += __popcll(on);
   }
+  const int nd = before;
   __syncthreads();
   for (int p = tid; p < P; p += th)
-    if (ids[p] >= 0) slots[(mask[ids[p]] >> 16) * kFewTokens + p / k] = (uint8_t)(p % k + 1);
+    if (ids[p] >= 0) slots[place[ids[p]] * kFewTokens + p / k] = (uint8_t)(p % k + 1);
   __syncthreads();
-  const int nd = list[0];
   if (blockIdx.x == 0) {  // for the down kernel
     for (int i = tid; i < (H + 127) / 128; i += th) a.done[i] = 0;
     if (a.ids_out)
       for (int p = tid; p < P; p += th) a.ids_out[p] = ids[p];
-    for (int i = tid; i <= nd; i += th) a.list[i] = list[i];
+    if (tid == 0) a.list[0] = nd;
+    for (int i = tid; i < nd; i += th) a.list[1 + i] = list[1 + i];
     for (int i = tid; i < nd; i += th) {
       int n = 0;
       for (int t = 0; t < T; ++t)
@@ -644,21 +681,25 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
 
   const int I = a.I, strips = I / 16, units = nd * strips, base = blockIdx.x * per, first = base + wave / split, step = a.routed_wgs * per;
   const int64_t rb = code_row_bytes<WF>(H), rs = scale_row_bytes<WF>(H);
-  const int NB = (H + Blk<WF>::K - 1) / Blk<WF>::K, lo = ks * NB / split, hi = (ks + 1) * NB / split;
+  const int NB = (H + 127) / 128, lo = ks * NB / split, hi = (ks + 1) * NB / split;
   float hmax = 0.0f;
   gu_stream<WF, D>(
-      max(0, (units - base + step - 1) / step), max(0, (units - first + step - 1) / step), lo, hi, H, rb, rs, smem + sm.x, xf, xt, ring,
-      [&](int j, Strip<WF>& sg, Strip<WF>& su) __attribute__((always_inline)) {
+      max(0, (units - base + step - 1) / step), max(0, (units - first + step - 1) / step), lo, hi, H, I, smem + sm.x, xf, xt, ring,
+      [&](int j, Strip<WF>& st) __attribute__((always_inline)) {
         const int u = first + j * step, e = __builtin_amdgcn_readfirstlane(list[1 + u / strips]);
         const int64_t row = (int64_t)e * 2 * I + (u % strips) * 16;
-        const uint8_t* ss = static_cast<const uint8_t*>(a.w13s);
-        sg.set(a.w13 + row * rb, ss + row * rs, rb, rs);
-        su.set(a.w13 + (row + I) * rb, ss + (row + I) * rs, rb, rs);
+        st.set(a.w13 + row * rb, static_cast<const uint8_t*>(a.w13s) + row * rs, (uint32_t)((I + 16) * rb), (uint32_t)((I + 16) * rs));
       },
       [&](int j, const float*& fg, const float*& fu) __attribute__((always_inline)) {
         const int u = first + j * step, e = __builtin_amdgcn_readfirstlane(list[1 + u / strips]), KB = H / 128;
         fg = static_cast<const float*>(a.w13s) + ((int64_t)e * (2 * I / 128) + (u % strips) / 8) * KB;
         fu = fg + (int64_t)(I / 128) * KB;
+      },
+      [&]() __attribute__((always_inline)) {
+        if constexpr (WF == FP4_FMT_NVFP4) {
+          for (int i = tid; i < nd; i += th) scale[i] = a.w13s2[list[1 + i]] * xs;
+          __syncthreads();
+        }
       },
       [&](int j, floatx4& ag, floatx4& au) __attribute__((always_inline)) {
         gu_reduce(ag, au, red, ks, split);
@@ -667,7 +708,7 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
         const int ai = u / strips, i0 = (u % strips) * 16, slot = slots[ai * kFewTokens + r];
         if (slot == 0) return;  // not a token of this expert
         const int64_t p = (int64_t)r * k + slot - 1;
-        const float s = scale[ai];
+        const float s = WF == FP4_FMT_NVFP4 ? scale[ai] : 1.0f;
         floatx4 h;
 #pragma unroll
         for (int q = 0; q < 4; ++q) h[q] = silu_f32(ag[q] * s) * (au[q] * s);
@@ -756,7 +797,16 @@ __global__ void __launch_bounds__(256) few_hquant_kernel(FewArgs a) {
 // LDS of the down kernel: the waves' rings, then h of two passes, then the
 // waves' outputs (f32 [16 tokens][16]).
 template <int FMT>
-constexpr int dn_ring() { return kDnRing * Blk<FMT>::SLOT; }
+constexpr int dn_depth() { return Blk<FMT>::FP4 ? 8 : 4; }  // slots: 1 KB (E2M1) or 2 KB (E4M3) of codes
+template <int FMT>
+constexpr int dn_ring() { return dn_depth<FMT>() * slot_bytes<FMT>(1); }
+
+// Waits until at most the loads of the last min(n, MOST) slots are on their way.
+template <int MOST, int ND>
+__device__ __forceinline__ void wait_vm(int n) {
+  if (n >= MOST) __builtin_amdgcn_s_waitcnt(vmcnt_only(ND * MOST));
+  else if constexpr (MOST > 0) wait_vm<MOST - 1, ND>(n);
+}
 
 // One workgroup's share of the down products: a row group (128 outputs, a
 // strip of 16 a wave) times the passes of the experts [a0, a1) of a list; a
@@ -768,11 +818,9 @@ constexpr int dn_ring() { return kDnRing * Blk<FMT>::SLOT; }
 template <int FMT, int NT, typename Expert, typename Pair, typename Factor, typename Token>
 __device__ __forceinline__ void dn_stream(const uint8_t* w, const uint8_t* ws, const float* wf, int H, int K, int n0, int lo, int hi, int a0, int a1,
                                           const uint16_t* h, uint32_t h_bytes, int PP, uint8_t* smem, Expert expert, Pair pair, Factor factor, Token token) {
-  using B = Blk<FMT>;
-  constexpr int D = kDnRing, ND = B::NDMA;
-  static_assert(D == 4, "the waits below count 3 blocks");
+  constexpr int D = dn_depth<FMT>(), ND = slot_dmas<FMT>(1), SLOT = slot_bytes<FMT>(1);
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t rb = code_row_bytes<FMT>(K), rs = scale_row_bytes<FMT>(K);
+  const int rb = (int)code_row_bytes<FMT>(K), rs = (int)scale_row_bytes<FMT>(K);
   uint8_t* ring = smem + wave * dn_ring<FMT>();
   uint8_t* hbuf = smem + kDnWaves * dn_ring<FMT>();
   const int RC = K / 8, rows = PP * NT, hbytes = rows * RC * 16;  // 16-byte chunks of a row of h
@@ -785,11 +833,11 @@ __device__ __forceinline__ void dn_stream(const uint8_t* w, const uint8_t* ws, c
   int li = a0, lp = 0, lb = lo;
   auto set_strip = [&](int i) __attribute__((always_inline)) {
     const int64_t row = (int64_t)expert(i).x * H + n0;
-    st.set(w + row * rb, ws + row * rs, rb, rs);
+    st.set(w + row * rb, ws + row * rs, 16 * rb, 16 * rs);
   };
   auto load_next = [&](int slot) __attribute__((always_inline)) {
     if (lb == lo) set_strip(min(li, a1 - 1));
-    load_block<FMT>(st, lb, rb, rs, ring + slot * B::SLOT);
+    load_slot<FMT, 1>(st, lb, rb, rs, 0, 0, ring + slot * SLOT);
     if (++lb == hi) {
       lb = lo;
       lp += PP;
@@ -825,47 +873,38 @@ __device__ __forceinline__ void dn_stream(const uint8_t* w, const uint8_t* ws, c
     if (np >= n) { np = 0; ++ni; }
     // h of this pass was issued a pass ago (the first before the ring's first D - 1 blocks): only the weight blocks
     // issued since may still be on their way
-    if (!strip_on || !dma_scales) __builtin_amdgcn_s_waitcnt(0);
-    else if (hi - lo >= 3) __builtin_amdgcn_s_waitcnt(vmcnt_only(3 * ND));
-    else if (hi - lo == 2) __builtin_amdgcn_s_waitcnt(vmcnt_only(2 * ND));
-    else __builtin_amdgcn_s_waitcnt(vmcnt_only(ND));
+    if (!strip_on || !dma_scales) __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+    else wait_vm<D - 1, ND>(hi - lo);
     asm volatile("s_barrier" ::: "memory");  // h of this pass is there for every wave, and every wave is past the last one's
     if (ni < a1) load_h(ni, np, buf ^ 1);
     const uint8_t* hrow = hbuf + buf * hbytes + hr * RC * 16;
     floatx4 acc{0.f, 0.f, 0.f, 0.f};
     if (strip_on) {
       const float* fw = FMT == FP4_FMT_FP8_BLOCK ? wf + ((int64_t)expert(i).x * (H / 128) + n0 / 128) * (K / 128) : nullptr;
-      for (int blk = lo; blk < hi; ++blk) {
+      for (int kb = lo; kb < hi; ++kb) {
         load_next(slot == 0 ? D - 1 : slot - 1);
         if (dma_scales) __builtin_amdgcn_s_waitcnt(vmcnt_only(ND * (D - 1)));
         else __builtin_amdgcn_s_waitcnt(0);
         asm volatile("" ::: "memory");
-        const uint8_t* at = ring + slot * B::SLOT;
+        WStep<FMT> v;
+        v.template read<1>(ring + slot * SLOT, 0, g, r);
         slot = slot == D - 1 ? 0 : slot + 1;
+        floatx4 pr = FMT == FP4_FMT_FP8_BLOCK ? floatx4{0.f, 0.f, 0.f, 0.f} : acc;
+        const bool in = 128 * kb + 32 * g < K;
 #pragma unroll
-        for (int s = 0; s < B::STEPS; ++s) {
-          const int kb = blk * B::STEPS + s;
-          if (128 * kb < K) {
-            WStep<FMT> v;
-            v.read(at, s, g, r);
-            floatx4 pr = FMT == FP4_FMT_FP8_BLOCK ? floatx4{0.f, 0.f, 0.f, 0.f} : acc;
-            const bool in = 128 * kb + 32 * g < K;
+        for (int q = 0; q < 4; ++q) {
+          int c = 16 * kb + 4 * g + q + rot;
+          c -= c >= RC ? RC : 0;
+          u32x4 hv = ld16(hrow + 16 * (in ? c : 0));
+          if (!in) hv = u32x4{0, 0, 0, 0};
+          pr = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wstep_frag<FMT>(v, q), __builtin_bit_cast(bf16x8_t, hv), pr, 0, 0, 0);
+        }
+        if (FMT == FP4_FMT_FP8_BLOCK) {
+          const float f = scalar_load(fw + kb);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              int c = 16 * kb + 4 * g + q + rot;
-              c -= c >= RC ? RC : 0;
-              u32x4 hv = ld16(hrow + 16 * (in ? c : 0));
-              if (!in) hv = u32x4{0, 0, 0, 0};
-              pr = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wstep_frag<FMT>(v, q), __builtin_bit_cast(bf16x8_t, hv), pr, 0, 0, 0);
-            }
-            if (FMT == FP4_FMT_FP8_BLOCK) {
-              const float f = scalar_load(fw + kb);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) acc[q] = fmaf(pr[q], f, acc[q]);
-            } else {
-              acc = pr;
-            }
-          }
+          for (int q = 0; q < 4; ++q) acc[q] = fmaf(pr[q], f, acc[q]);
+        } else {
+          acc = pr;
         }
       }
       // the terms' columns of a pair add up, then go to its token's outputs (a token is in an expert's list once)
@@ -921,7 +960,7 @@ __global__ void __launch_bounds__(64 * kDnWaves, 2) few_down_kernel(FewArgs a) {
     }
     __syncthreads();
     dn_stream<WF, NT>(
-        a.w2, static_cast<const uint8_t*>(a.w2s), static_cast<const float*>(a.w2s), H, a.I, n0, 0, (a.I + Blk<WF>::K - 1) / Blk<WF>::K, 0, a1 - a0,
+        a.w2, static_cast<const uint8_t*>(a.w2s), static_cast<const float*>(a.w2s), H, a.I, n0, 0, (a.I + 127) / 128, 0, a1 - a0,
         a.hb, (uint32_t)(T * k) * NT * a.I * 2, a.pass_pairs, smem,
         [&](int i) __attribute__((always_inline)) {
           return int2{__builtin_amdgcn_readfirstlane(s_expert[i].x), __builtin_amdgcn_readfirstlane(s_expert[i].y)};
@@ -980,7 +1019,7 @@ __global__ void __launch_bounds__(64 * kDnWaves, 2) few_down_kernel(FewArgs a) {
 
 struct FewPlan {
   int mode, splits, shared_splits, pass_pairs, shared_pairs;
-  int nw, deep;  // gate_up: waves of a workgroup, ring of 4 blocks instead of 2
+  int nw, depth;  // gate_up: waves of a workgroup, slots of a wave's ring
   size_t wts, list, pairs, done, sgate, amax_part, h_ts, h, hb, sh, shb, ypart, total;
 };
 
@@ -989,9 +1028,13 @@ constexpr int kLds = 160 * 1024;
 constexpr int kGuLds = kLds - 64;   // dynamic LDS beside the gate_up kernel's static bytes
 constexpr int kDnHBytes = 48 * 1024;  // LDS for h of two passes
 
-static int ring_slot(int w_fmt) {  // gate and up block
-  const int slot = w_fmt == FP4_FMT_NVFP4 ? Blk<FP4_FMT_NVFP4>::SLOT : w_fmt == FP4_FMT_MXFP4 ? Blk<FP4_FMT_MXFP4>::SLOT : Blk<FP4_FMT_FP8_BLOCK>::SLOT;
-  return 2 * std::max(slot, Blk<FP4_FMT_MXFP8>::SLOT);
+template <int D>
+static int ring_bytes(int mode, bool shared) {
+  switch (mode) {
+    case FM_NV: case FM_NVNV: return gu_ring<FM_NV, D>(shared);
+    case FM_MX: case FM_MXMX: return gu_ring<FM_MX, D>(shared);
+    default: return gu_ring<FM_FP8, D>(shared);
+  }
 }
 
 static int few_plan(const moe_fp4_layer* L, int64_t T, FewPlan* out) {
@@ -1005,13 +1048,15 @@ static int few_plan(const moe_fp4_layer* L, int64_t T, FewPlan* out) {
   p.mode = L->w_fmt == FP4_FMT_FP8_BLOCK ? FM_FP8 : L->a_fmt == FP4_FMT_NONE ? (nv ? FM_NV : FM_MX) : (nv ? FM_NVNV : FM_MXMX);
   const int nt = L->a_fmt == FP4_FMT_NONE || L->a_fmt == FP4_FMT_FP8_ROW ? 3 : 1;
   const size_t P = (size_t)T * L->top_k, D = std::min<size_t>(P, L->num_experts), I = L->inter, S = L->shared_inter, H = L->hidden;
-  // gate_up: the most waves whose rings fit beside x, with deep rings if they fit
-  const int rings[][2] = {{8, 4}, {8, 2}, {4, 2}, {2, 2}, {1, 2}};
-  for (auto& r : rings)
-    if (p.nw == 0 && gu_smem((int)T, L->num_experts, L->top_k, L->hidden, r[0], r[1] * ring_slot(L->w_fmt), true).total <= kGuLds) {
+  // gate_up: the most waves whose rings fit beside x, with the deepest rings that do
+  const int rings[][2] = {{8, 4}, {8, 3}, {8, 2}, {4, 2}, {2, 2}, {1, 2}};
+  for (auto& r : rings) {
+    const int ring = r[1] == 4 ? ring_bytes<4>(p.mode, S > 0) : r[1] == 3 ? ring_bytes<3>(p.mode, S > 0) : ring_bytes<2>(p.mode, S > 0);
+    if (p.nw == 0 && gu_smem((int)T, L->num_experts, L->top_k, L->hidden, p.mode == FM_FP8, r[0], ring, D * (I / 16) < (size_t)kFewCus * r[0]).total <= kGuLds) {
       p.nw = r[0];
-      p.deep = r[1] == 4;
+      p.depth = r[1];
     }
+  }
   if (p.nw == 0 && T > 0)
     return fail(FP4_ERR_UNSUPPORTED, "few-token forward: %lld tokens of width %d do not fit the LDS", (long long)T, L->hidden);
   p.pass_pairs = (int)std::min<size_t>(std::min<size_t>(16 / nt, std::max<int64_t>(T, 1)), kDnHBytes / (4 * nt * I));
@@ -1050,11 +1095,11 @@ static int launch_few(FewArgs a, const FewPlan& p, int y_dtype, hipStream_t st) 
   constexpr int AF = act_fmt(MODE), WF = weight_fmt(MODE), NT = AF == FP4_FMT_NONE || AF == FP4_FMT_FP8_ROW ? 3 : 1;
   static std::atomic<uint64_t> gu_raised{0}, dn32_raised{0}, dn16_raised{0};
   FP4_CHECK(raise_dyn_lds(reinterpret_cast<const void*>(&few_gateup_kernel<MODE, D>), kGuLds, gu_raised));
-  const int ring = D * ring_slot(WF), strips = a.I / 16, max_units = std::min(a.E, a.T * a.k) * strips;
+  const int ring = gu_ring<MODE, D>(a.S > 0), strips = a.I / 16, max_units = std::min(a.E, a.T * a.k) * strips;
   // a unit is split between waves (each a run of K) until the units there may be fill the chip's waves
   a.k_split = 1;
   while (a.k_split < p.nw && max_units * a.k_split < kFewCus * p.nw) a.k_split *= 2;
-  const int lds = gu_smem(a.T, a.E, a.k, a.H, p.nw, ring, a.k_split > 1).total;
+  const int lds = gu_smem(a.T, a.E, a.k, a.H, MODE == FM_FP8, p.nw, ring, a.k_split > 1).total;
   const int per = p.nw / a.k_split, fit = kFewCus * std::max(1, std::min(2, kLds / (lds + 64)));
   int shared = 0;  // workgroups of the shared expert, by its share of the bytes
   if (a.S > 0) {
@@ -1087,7 +1132,8 @@ static int launch_few(FewArgs a, const FewPlan& p, int y_dtype, hipStream_t st) 
 
 template <int MODE>
 static int launch_few(const FewArgs& a, const FewPlan& p, int y_dtype, hipStream_t st) {
-  return p.deep ? launch_few<MODE, 4>(a, p, y_dtype, st) : launch_few<MODE, 2>(a, p, y_dtype, st);
+  if (p.depth == 4) return launch_few<MODE, 4>(a, p, y_dtype, st);
+  return p.depth == 3 ? launch_few<MODE, 3>(a, p, y_dtype, st) : launch_few<MODE, 2>(a, p, y_dtype, st);
 }
 
 }  // namespace fp4
