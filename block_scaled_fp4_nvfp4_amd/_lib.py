@@ -426,8 +426,9 @@ class FewTokenLayer:
     Masked experts have logit -inf; slots left over get id -1, weight 0.
 
     The workspace serves one call at a time: calls on several streams, or
-    captured graphs that may replay at once, need a FewTokenLayer each.  The
-    layer's tensors are those at construction."""
+    captured graphs that may replay at once, need a FewTokenLayer each, which
+    has to live as long as the graphs.  The layer's tensors are those at
+    construction."""
 
     def __init__(self, layer: MoELayer, max_tokens: int, out_dtype: torch.dtype = torch.float32):
         if out_dtype not in (torch.float32, torch.bfloat16):

@@ -279,9 +279,9 @@ def test_streams_and_captured_graphs():
         gr = torch.cuda.CUDAGraph()
         with torch.cuda.graph(gr):
             few(x, lg, None, *out)
-        runs.append((eager, x, lg, out, gr))
+        runs.append((eager, x, lg, out, gr, few))  # the graph works in few's workspace
     for rep in range(4):
-        for eager, x, lg, out, gr in runs:
+        for eager, x, lg, out, gr, _ in runs:
             x.copy_(torch.roll(x, 3, dims=1))
             lg.copy_(torch.roll(lg, 1 + rep, dims=1))
             if rep == 2:
