@@ -48,7 +48,6 @@ typedef float floatx4 __attribute__((ext_vector_type(4)));
 constexpr int kFewTokens = 16;  // columns of the MFMA tile
 constexpr int kGuWaves = 8;     // most waves per workgroup of the gate_up kernel
 constexpr int kDnWaves = 8;     // most waves per workgroup of the down kernel
-constexpr int kDnSeg = 64;      // most experts of one split
 
 // format pairs of the layer
 enum FewMode { FM_NV = 0, FM_MX = 1, FM_NVNV = 2, FM_MXMX = 3, FM_FP8 = 4 };
@@ -58,6 +57,16 @@ constexpr int weight_fmt(int mode) {
 constexpr int act_fmt(int mode) {
   return mode == FM_NVNV ? FP4_FMT_NVFP4 : mode == FM_MXMX ? FP4_FMT_MXFP8 : mode == FM_FP8 ? FP4_FMT_FP8_ROW : FP4_FMT_NONE;
 }
+
+// One pass of the down products: up to pass_pairs pairs of one expert.  gate_up's
+// first workgroup writes a record for each.
+struct DnPass {
+  int32_t expert, n;
+  uint16_t pair[kFewTokens];  // t * k + j | t << 9; those past n repeat the first
+  int32_t pad[6];
+  float factor[kFewTokens];   // routing weight times the expert's tensor scale
+};
+static_assert(sizeof(DnPass) == 128);
 
 struct FewArgs {
   const uint16_t* x;       // bf16 [T, H]
@@ -71,17 +80,17 @@ struct FewArgs {
   int T, E, k, H, I, S;    // S: shared width, 0 without a shared expert
   int routed_wgs;          // gate_up workgroups of the routed experts; the rest take the shared expert
   int k_split;             // waves that share one unit of the routed gate_up
-  int splits, shared_splits;  // down workgroups of a strip: of the routed experts, of the shared expert
-  int pass_pairs, seg_steps;  // pairs of an expert and 128-wide K steps that a wave of the down kernel takes at once
+  int down_wgs;            // down workgroups of the routed experts; the rest take the shared expert
+  int pass_pairs, seg_steps;  // of the down kernel: pairs of an expert at once, 128-wide K steps of a slot
   // workspace
-  int32_t *list, *pairs;   // touched experts [1 + min(E, T k)] (count first); [.., 16] their pairs, then -1
-  int32_t* done;           // [H / 16] arrivals of the down kernel's splits
-  float *wts, *sgate, *amax_part, *h_ts;
+  int32_t* list;           // passes, then the selected experts of every token
+  DnPass* passes;          // [T k]
+  float *sgate, *amax_part, *h_ts;
   float* h;                // f32 [T k, I] (quantized modes)
   uint16_t* hb;            // bf16 [T k, I] quantized values, or [T k, 3, I] terms
   float* sh;               // f32 [T, S]
   uint16_t* shb;           // bf16 [T, S]
-  float* ypart;            // f32 [splits + shared_splits, T, H]
+  float* d;                // f32 [T k + S / 128 * T, H] weighted down products of the pairs, of the shared expert's K steps
   // outputs
   int32_t* ids_out;
   float* wts_out;
@@ -377,7 +386,7 @@ __device__ __forceinline__ void select_topk(const float* logits, const float* bi
 // ------------------------------------------------------------------ gate_up
 
 struct GuSmem {
-  int x, xf, ids, list, scale, slot, red, ring, total;
+  int x, xf, ids, wts, list, scale, slot, red, ring, total;
 };
 // byte offsets of the gate_up kernel's dynamic LDS: x~ (with `factors` one per
 // token and K step), the routing's tables, nw waves with `ring` bytes each, their
@@ -388,7 +397,8 @@ __host__ __device__ inline GuSmem gu_smem(int T, int E, int k, int K, bool facto
   s.x = 0;  // rows padded by 16 bytes: 16 lanes that read one chunk of 16 rows hit different banks
   s.xf = s.x + T * (kp + 8) * 2;
   s.ids = s.xf + (factors ? T * (kp / 128) * 4 : 0);
-  s.list = s.ids + T * k * 4;
+  s.wts = s.ids + T * k * 4;
+  s.list = s.wts + T * k * 4;
   s.scale = s.list + D * 4;
   s.slot = s.scale + D * 4;
   s.red = (s.slot + D * kFewTokens + 15) / 16 * 16;
@@ -636,6 +646,7 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ float tmp[kGuWaves], xs[kFewTokens];
   __shared__ uint32_t s_amax;
+  __shared__ int s_np;
   __shared__ unsigned long long touched[16];
   const int tid = threadIdx.x, th = blockDim.x, nw = th >> 6, lane = tid & 63, g = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -688,11 +699,12 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
 
   int* ids = reinterpret_cast<int*>(smem + sm.ids);
   int* list = reinterpret_cast<int*>(smem + sm.list);
+  float* wts = reinterpret_cast<float*>(smem + sm.wts);
   float* scale = reinterpret_cast<float*>(smem + sm.scale);
   uint8_t* slots = smem + sm.slot;  // [listed expert][token]: the token's slot + 1
   if constexpr (AF == FP4_FMT_NONE) prepare_x<WF, AF>(a, smem + sm.x, xf, xs, tmp);
   for (int i = tid; i < min(a.E, P) * kFewTokens / 4; i += th) reinterpret_cast<uint32_t*>(slots)[i] = 0;
-  if (tid == 0) s_amax = 0;
+  if (tid == 0) s_amax = 0, s_np = 0;
   if (tid < 16) touched[tid] = 0;
   auto weights = [&](int t, uint32_t key) __attribute__((always_inline)) {  // softmax over the selected values in f64; slots left over: weight 0
     const uint32_t top = (uint32_t)__builtin_amdgcn_readfirstlane((int)key);
@@ -703,7 +715,7 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
     sum = __shfl(sum, 0);
     if (lane < k) {
       const float w = key ? (float)(z / sum) : 0.0f;
-      a.wts[t * k + lane] = w;
+      wts[t * k + lane] = w;
       if (a.wts_out) a.wts_out[t * k + lane] = w;
     }
   };
@@ -748,17 +760,36 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
   }
   __syncthreads();
   if (blockIdx.x == 0) {  // for the down kernel
-    for (int i = tid; i < H / 16; i += th) a.done[i] = 0;
     if (a.ids_out)
       for (int p = tid; p < P; p += th) a.ids_out[p] = ids[p];
-    if (tid == 0) a.list[0] = nd;
-    for (int i = tid; i < nd; i += th) a.list[1 + i] = list[i];
-    for (int i = tid; i < nd; i += th) {
+    if (tid < T) {
       int n = 0;
-      for (int t = 0; t < T; ++t)
-        if (const int j = slots[i * kFewTokens + t]) a.pairs[i * kFewTokens + n++] = t * k + j - 1;
-      for (; n < kFewTokens; ++n) a.pairs[i * kFewTokens + n] = -1;
+      for (int j = 0; j < k; ++j) n += ids[tid * k + j] >= 0;
+      a.list[1 + tid] = n;
     }
+    for (int i = tid; i < nd; i += th) {  // the order of the passes does not matter: every pair's products have a row of their own
+      const uint8_t* sl = slots + i * kFewTokens;
+      int n = 0, q = 0;
+      for (int t = 0; t < T; ++t) n += sl[t] != 0;
+      DnPass* pass = a.passes + atomicAdd(&s_np, (n + a.pass_pairs - 1) / a.pass_pairs);
+      const float f = WF == FP4_FMT_NVFP4 ? a.w2s2[list[i]] : 1.0f;
+      for (int t = 0; t < T; ++t) {
+        if (sl[t] == 0) continue;
+        const int p = t * k + sl[t] - 1;
+        pass->pair[q] = (uint16_t)(p | t << 9);
+        pass->factor[q] = wts[p] * f;
+        --n;
+        if (++q == a.pass_pairs || n == 0) {
+          pass->expert = list[i];
+          pass->n = q;
+          for (; q < a.pass_pairs; ++q) pass->pair[q] = pass->pair[0];
+          ++pass;
+          q = 0;
+        }
+      }
+    }
+    __syncthreads();
+    if (tid == 0) a.list[0] = s_np;
   }
 
   const int I = a.I, strips = I / 16, units = nd * strips, base = blockIdx.x * per, first = base + wave / split, step = a.routed_wgs * per;
@@ -878,32 +909,37 @@ __global__ void __launch_bounds__(256) few_hquant_kernel(FewArgs a) {
 
 // --------------------------------------------------------------------- down
 
-// A slot of the down kernel: one work item of a wave, a segment of m K steps of
-// 16 weight rows (codes, then scales) and of h of up to PP pairs (NT terms
-// each).  A row's 16-byte chunk c lies at place c + row (modulo the row), so
-// that the 16 lanes that read one chunk of 16 rows hit different banks.
-struct DnSlot {
-  int cs, sd, hc;            // chunks of a code row, dwords of a scale row, chunks of an h row
-  int scales, h, bytes, dmas;
+// A wave's LDS in the down kernel: two slots for a segment of m K steps of 16
+// weight rows (codes, then scales), h of a pass (rows of `steps` K steps), its
+// record, and the products of up to `hold` strips.  A row's 16-byte chunk c
+// lies at place c + row (modulo the row), so that the 16 lanes that read one
+// chunk of 16 rows hit different banks.
+struct DnWave {
+  int cs, sd, hc;  // chunks of a code row, dwords of a scale row, chunks of an h row
+  int scales, slot, dmas, h, rec, out, hold, bytes;
 };
 template <int FMT>
-__host__ __device__ inline DnSlot dn_slot(int m, int rows) {
-  DnSlot s;
+__host__ __device__ inline DnWave dn_wave(int m, int steps, int pairs, int terms) {
+  DnWave s;
   s.cs = Rows<FMT>::STEP / 16 * m;
   s.sd = Rows<FMT>::SSTEP / 4 * m;
-  s.hc = 16 * m;
+  s.hc = 16 * steps;
   s.scales = 256 * s.cs;
-  s.h = s.scales + 64 * s.sd;
-  s.bytes = s.h + rows * s.hc * 16;
-  s.dmas = s.cs / 4 + (16 * s.sd + 63) / 64 + rows * ((s.hc + 63) / 64);
+  s.slot = s.scales + 64 * s.sd;
+  s.dmas = s.cs / 4 + (16 * s.sd + 63) / 64;
+  s.h = 2 * s.slot;
+  s.rec = s.h + pairs * terms * s.hc * 16;
+  s.out = s.rec + (int)sizeof(DnPass);
+  s.hold = pairs > 2 ? 32 / pairs : 16;
+  s.bytes = s.out + s.hold * pairs * 64;
   return s;
 }
 template <int FMT>
-constexpr int dn_most_steps() { return Rows<FMT>::FP4 ? 8 : 4; }  // of an item: 8 DMA instructions of codes
+constexpr int dn_most_steps() { return Rows<FMT>::FP4 ? 8 : 4; }  // of a slot: 8 DMA instructions of codes
 constexpr int dn_terms(int mode) { return act_fmt(mode) == FP4_FMT_NONE || act_fmt(mode) == FP4_FMT_FP8_ROW ? 3 : 1; }
 
-// Waits until at most n loads are on their way (more than 63: 63).
-template <int LO = 0, int HI = 63>
+// Waits until at most n loads are on their way (more than 15: 15).
+template <int LO = 0, int HI = 15>
 __device__ __forceinline__ void wait_vm(int n) {
   if constexpr (LO == HI) {
     __builtin_amdgcn_s_waitcnt(vmcnt_only(LO));
@@ -914,44 +950,64 @@ __device__ __forceinline__ void wait_vm(int n) {
   }
 }
 
-// One wave's share of the down products of a strip of 16 outputs (rows n0 ..):
-// experts i0, i0 + istep, .. < i1 of a list, up to PP of an expert's pairs at a
-// time, segments [lo, hi) of m steps of K.  An item's weights and h come by
-// DMA into one of the wave's two slots while the other is computed; nothing is
-// shared between waves, so none waits for another.  h's rows (term * PP +
-// pair) are the columns of the MFMA tile.  expert(i) gives the expert's number
-// and pair count, pair(i, q) its q-th pair, factor(i, q) what multiplies that
-// pair's product, token(p) its row of the wave's sums yl [T][16].
-template <int FMT, int NT, typename Expert, typename Pair, typename Factor, typename Token>
-__device__ __forceinline__ void dn_stream(const uint8_t* w, const uint8_t* ws, const float* wf, int H, int K, int n0, int m, int lo, int hi, int i0, int istep,
-                                          int i1, const uint16_t* h, uint32_t h_bytes, int PP, uint8_t* slots, float* yl, Expert expert, Pair pair,
-                                          Factor factor, Token token) {
+// A word that the kernel before wrote, at an address all lanes share.
+__device__ __forceinline__ uint32_t scalar_word(const void* p) {
+  return *reinterpret_cast<const __attribute__((address_space(4))) uint32_t*>(reinterpret_cast<uintptr_t>(p));
+}
+__device__ __forceinline__ int pass_pair(const DnPass* p, int q) {
+  return (int)(scalar_word(p->pair + (q & ~1)) >> (16 * (q & 1)) & 511);
+}
+
+// One wave's down products of one pass: strips [s0, s1) of 16 outputs of an
+// expert (rows row0 + 16 strip of w), PP pairs with NT terms of h each, all of
+// K or (the shared expert) its K steps [first, first + steps).  h's rows (term *
+// PP + pair) are the columns of the MFMA tile and stay in LDS; the weights
+// stream through two slots, one being copied while the other is computed.
+// Nothing is shared between waves, so none waits for another.  h_row(pair,
+// term) gives a row's byte offset; pair q's product times factor(q) goes to
+// row out_row(q) of d.
+template <int FMT, int NT, typename HRow, typename Factor, typename OutRow>
+__device__ __forceinline__ void dn_run(const uint8_t* w, const uint8_t* ws, const float* wf, int64_t row0, int H, int K, int first, int steps, int m, int s0, int s1,
+                                       __amdgpu_buffer_rsrc_t hb, const DnPass* rec, int n, int PP, uint8_t* lds, float* d, HRow h_row,
+                                       Factor factor, OutRow out_row) {
   using R = Rows<FMT>;
-  if (i0 >= i1 || lo >= hi) return;
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
-  const int rb = (int)code_row_bytes<FMT>(K), rs = (int)scale_row_bytes<FMT>(K), rows = PP * NT, steps = (K + 127) / 128;
-  const DnSlot sl = dn_slot<FMT>(m, rows);
+  const int rb = (int)code_row_bytes<FMT>(K), rs = (int)scale_row_bytes<FMT>(K), rows = PP * NT, segs = (steps + m - 1) / m;
+  const DnWave sl = dn_wave<FMT>(m, steps, PP, NT);
   const bool by4 = (((uint32_t)rs | (uint32_t)(uintptr_t)ws) & 3) == 0;
-  const auto hb = buffer_of(h, h_bytes);
-  uint32_t coff[8], soff[4];  // a lane's byte offsets in the item's code rows and scale rows
+  // the record and h
+  if (rec) {
+    const auto b = buffer_of(rec, sizeof(DnPass));
+    if (lane < (int)sizeof(DnPass) / 4) dma_buffer4(b, 4 * lane, 0, lds + sl.rec);
+  }
+  for (int pq = 0; pq < PP; ++pq)
+    for (int t = 0; t < NT; ++t) {
+      const int q = t * PP + pq;
+      const uint32_t at = h_row(pq, t) + 256 * first;
+      for (int c0 = 0; c0 < sl.hc; c0 += 64) {
+        const int c = c0 + lane - q;
+        if (c0 + lane < sl.hc) dma_buffer(hb, at + 16 * (c < 0 ? c + sl.hc : c), 0, lds + sl.h + (q * sl.hc + c0) * 16);
+      }
+    }
+  // n / d = n (2^16 / d + 1) >> 16 for n < 512, d <= 32 (off by less than 512 / 2^16 < 1 / d)
+  const uint32_t inv_cs = 65536u / sl.cs + 1, inv_sd = 65536u / max(sl.sd, 1) + 1;
+  uint32_t coff[8], soff[4];  // a lane's byte offsets in a slot's code rows and scale rows
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t at = 64 * j + lane, row = at / (uint32_t)sl.cs, c = at - row * sl.cs, rot = row % (uint32_t)sl.cs;
+    const uint32_t at = 64 * j + lane, row = at * inv_cs >> 16, c = at - row * sl.cs, rot = row - (row * inv_cs >> 16) * sl.cs;
     coff[j] = row * rb + 16 * (c >= rot ? c - rot : c - rot + sl.cs);
   }
   if constexpr (R::SSTEP > 0) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t at = 64 * j + lane, row = at / (uint32_t)sl.sd;
+      const uint32_t at = 64 * j + lane, row = at * inv_sd >> 16;
       soff[j] = row * rs + 4 * (at - row * sl.sd);
     }
   }
-  struct Item { int i, p0, seg; };
-  auto issue = [&](const Item& it, uint8_t* slot) __attribute__((always_inline)) {
-    const int2 ex = expert(it.i);
-    const int64_t row = (int64_t)ex.x * H + n0;
-    // rows and h past K give what lies behind them or zeros; the products skip it
-    const int cat = 16 * sl.cs * it.seg, sat = 4 * sl.sd * it.seg;
+  auto issue = [&](int strip, int seg, uint8_t* slot) __attribute__((always_inline)) {
+    const int64_t row = row0 + 16 * strip;
+    // rows past K give what lies behind them or zeros; the products skip it
+    const int kb = first + m * seg, cat = R::STEP * kb, sat = R::SSTEP * kb;
     const auto bc = buffer_of(w + row * rb + cat, (uint32_t)(16 * rb - cat));
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -969,198 +1025,196 @@ __device__ __forceinline__ void dn_stream(const uint8_t* w, const uint8_t* ws, c
         }
       }
     }
-    for (int q = 0; q < rows; ++q) {
-      const int t = q / PP, pq = q - t * PP, n = ex.y - it.p0;
-      const int p = __builtin_amdgcn_readfirstlane(pair(it.i, it.p0 + (pq < n ? pq : 0)));  // rows past the pairs repeat the first
-      const uint32_t at = (uint32_t)(2 * ((p * NT + t) * K + 128 * m * it.seg));
-      for (int c0 = 0; c0 < sl.hc; c0 += 64) {
-        const int c = c0 + lane - q;
-        if (c0 + lane < sl.hc) dma_buffer(hb, at + 16 * (c < 0 ? c + sl.hc : c), 0, slot + sl.h + (q * sl.hc + c0) * 16);
-      }
-    }
   };
-  auto advance = [&](Item& it) __attribute__((always_inline)) {
-    if (++it.seg < hi) return;
-    it.seg = lo;
-    it.p0 += PP;
-    if (it.p0 >= expert(it.i).y) { it.p0 = 0; it.i += istep; }
-  };
-  Item now{i0, 0, lo}, next = now;
-  issue(next, slots);
-  advance(next);
-  uint8_t *slot = slots, *other = slots + sl.bytes;
-  const int hr = r < rows ? r : 0;
+  const int hr = r < rows ? r : 0, rot = r - (int)(r * inv_cs >> 16) * sl.cs;
+  const uint8_t* hrow = lds + sl.h + 16 * sl.hc * hr;
+  float* out = reinterpret_cast<float*>(lds + sl.out);
+  int strip = s0, seg = 0, base = s0;  // base: the first strip whose products `out` holds
+  uint8_t *slot = lds, *other = lds + sl.slot;
+  issue(strip, seg, slot);
   floatx4 acc{0.f, 0.f, 0.f, 0.f};
-  while (now.i < i1) {
-    if (next.i < i1) {
+  while (strip < s1) {
+    const bool end = seg + 1 == segs;
+    const int nstrip = end ? strip + 1 : strip, nseg = end ? 0 : seg + 1;
+    if (nstrip < s1) {
       __builtin_amdgcn_s_waitcnt(lgkmcnt0());  // the other slot's values are in registers
-      issue(next, other);
-      advance(next);
+      issue(nstrip, nseg, other);
       if (R::SSTEP > 0 && !by4) __builtin_amdgcn_s_waitcnt(0);
       else wait_vm(sl.dmas);
     } else {
       __builtin_amdgcn_s_waitcnt(0);
     }
     asm volatile("" ::: "memory");
-    const uint8_t *crow = slot + 16 * sl.cs * r, *srow = slot + sl.scales + 4 * sl.sd * r, *hrow = slot + sl.h + 16 * sl.hc * hr;
-    const int rot = r % (uint32_t)sl.cs;
-    const float* fw = FMT == FP4_FMT_FP8_BLOCK ? wf + ((int64_t)expert(now.i).x * (H / 128) + n0 / 128) * (K / 128) : nullptr;
-    const int last = min(m, steps - m * now.seg);
-    for (int s = 0; s < last; ++s) {
-      const int kb = m * now.seg + s;
-      const bool in = 128 * kb + 32 * g < K;
-      WStep<FMT> v;
-      v.read([&](int c) {
+    const uint8_t *crow = slot + 16 * sl.cs * r, *srow = slot + sl.scales + 4 * sl.sd * r;
+    const float* fw = FMT == FP4_FMT_FP8_BLOCK ? wf + ((row0 + 16 * strip) / 128) * (K / 128) + first + m * seg : nullptr;
+    const int last = min(m, steps - m * seg);
+    struct Step {
+      WStep<FMT> w;
+      u32x4 x[4];
+    };
+    auto read = [&](Step& v, int s) __attribute__((always_inline)) {
+      v.w.read([&](int c) {
         c += R::STEP / 16 * s + rot;
         return crow + 16 * (c >= sl.cs ? c - sl.cs : c);
       }, srow + R::SSTEP * s, g);
-      u32x4 x[4];
+      const int hs = m * seg + s, k0 = 128 * (first + hs);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        int c = 16 * s + 4 * g + q + hr;
+        int c = 16 * hs + 4 * g + q + hr;
         c -= c >= sl.hc ? sl.hc : 0;
-        x[q] = ld16(hrow + 16 * c);
+        v.x[q] = ld16(hrow + 16 * c);
       }
-      if (128 * kb + 128 > K && !in) {  // what lies behind a row may be NaN: weights and h both give way to zeros
-        v.c[0] = u32x4{0, 0, 0, 0};
-        if constexpr (!R::FP4) v.c[1] = v.c[0];
-        v.s = 0;
+      if (k0 + 128 > K && k0 + 32 * g >= K) {  // what lies behind a row may be NaN: weights and h both give way to zeros
+        v.w.c[0] = u32x4{0, 0, 0, 0};
+        if constexpr (!R::FP4) v.w.c[1] = v.w.c[0];
+        v.w.s = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) x[q] = u32x4{0, 0, 0, 0};
+        for (int q = 0; q < 4; ++q) v.x[q] = u32x4{0, 0, 0, 0};
       }
+    };
+    auto product = [&](const Step& v, int s) __attribute__((always_inline)) {
       floatx4 pr = FMT == FP4_FMT_FP8_BLOCK ? floatx4{0.f, 0.f, 0.f, 0.f} : acc;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) pr = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wstep_frag<FMT>(v, q), __builtin_bit_cast(bf16x8_t, x[q]), pr, 0, 0, 0);
+      for (int q = 0; q < 4; ++q) pr = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wstep_frag<FMT>(v.w, q), __builtin_bit_cast(bf16x8_t, v.x[q]), pr, 0, 0, 0);
       if (FMT == FP4_FMT_FP8_BLOCK) {
-        const float f = scalar_load(fw + kb);
+        const float f = scalar_load(fw + s);
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[q] = fmaf(pr[q], f, acc[q]);
       } else {
         acc = pr;
       }
+    };
+    Step a, b;  // a step's values leave LDS while the one before is multiplied
+    read(a, 0);
+    for (int s = 0;;) {
+      if (s + 1 < last) read(b, s + 1);
+      product(a, s);
+      if (++s >= last) break;
+      if (s + 1 < last) read(a, s + 1);
+      product(b, s);
+      if (++s >= last) break;
     }
-    if (now.seg == hi - 1) {
-      // the terms' columns of a pair add up, then go to its token's outputs (a token is in an expert's list once)
-      floatx4 v = acc;
+    if (end) {
+      floatx4 v = acc;  // the terms' columns of a pair add up
       if constexpr (NT == 3) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] += __shfl(acc[q], lane + PP) + __shfl(acc[q], lane + 2 * PP);
       }
-      if (r < PP && now.p0 + r < expert(now.i).y) {
-        const float f = factor(now.i, now.p0 + r);
-        floatx4* y = reinterpret_cast<floatx4*>(yl + token(pair(now.i, now.p0 + r)) * 16 + 4 * g);
-        floatx4 o = *y;
+      if (r < PP) {
+        const float f = factor(r);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = fmaf(v[q], f, o[q]);
-        *y = o;
+        for (int q = 0; q < 4; ++q) v[q] *= f;
+        *reinterpret_cast<floatx4*>(out + (r * sl.hold + strip - base) * 16 + 4 * g) = v;
       }
       acc = floatx4{0.f, 0.f, 0.f, 0.f};
+      const int held = strip + 1 - base;
+      if (held == sl.hold || strip + 1 == s1) {  // a store's acknowledgement would hold up the loads behind it: few stores
+        for (int q = 0; q < n; ++q) {
+          const int64_t at = (int64_t)out_row(q) * H + 16 * base;
+          if (lane < 4 * held) *reinterpret_cast<floatx4*>(d + at + 4 * lane) = *reinterpret_cast<const floatx4*>(out + q * sl.hold * 16 + 4 * lane);
+        }
+        base = strip + 1;
+      }
     }
-    advance(now);
+    strip = nstrip;
+    seg = nseg;
     uint8_t* t = slot;
     slot = other;
     other = t;
   }
 }
 
-// Grid: (strips of 16 outputs, splits).  The waves of a workgroup share the
-// experts of its split (a run of the touched ones), or (the last shared_splits)
-// a run of the shared expert's K, then their sums are added in the waves'
-// order.  More than one split: the sums go to ypart, and the last workgroup of
-// a strip to arrive adds all splits up, in their order, and writes y.  Partial
-// sums are stored and read at device scope, past the XCDs' L2s; no workgroup
-// waits for another.
-template <int MODE, typename OutT>
+// The (pass, strip) pairs, pass by pass, are cut into one run a wave; the
+// shared expert's (K step, strip) pairs go to the last workgroups in the same
+// way.  The products of every pair (and of every K step of the shared expert)
+// are rows of d in the workspace, which few_sum_kernel adds up: waves that added
+// the strips they completed took 2.5 us for each, one after another, a tail
+// of up to 27 us at 16 tokens.
+template <int MODE>
 __global__ void __launch_bounds__(64 * kDnWaves, 2) few_down_kernel(FewArgs a) {
   constexpr int WF = weight_fmt(MODE), AF = act_fmt(MODE), NT = dn_terms(MODE);
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  __shared__ int2 s_expert[kDnSeg];                 // this split's experts: number, pairs
-  __shared__ int16_t s_pair[kDnSeg][kFewTokens];
-  __shared__ float s_factor[kDnSeg][kFewTokens];    // routing weight times the tensor scales
-  __shared__ int s_last;
-  const int tid = threadIdx.x, th = blockDim.x, nw = th >> 6, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int T = a.T, H = a.H, k = a.k, split = blockIdx.y, total = gridDim.y, n0 = blockIdx.x * 16;
-  float* yl = reinterpret_cast<float*>(smem) + wave * T * 16;  // the waves' sums, then their slots
-  uint8_t* slots = smem + nw * T * 64;
-  for (int q = tid & 63; q < T * 16; q += 64) yl[q] = 0.0f;
-  if (split < a.splits) {
-    const int nd = a.list[0], a0 = split * nd / a.splits, a1 = (split + 1) * nd / a.splits;
-    for (int i = tid; i < (a1 - a0) * kFewTokens; i += th) {
-      const int e = a.list[1 + a0 + (i >> 4)], p = a.pairs[a0 * kFewTokens + i];
-      float f = a.wts[max(p, 0)];
-      if (WF == FP4_FMT_NVFP4) f *= a.w2s2[e];
-      if (AF == FP4_FMT_NVFP4) f *= a.h_ts[0];
-      s_pair[i >> 4][i & 15] = (int16_t)p;
-      s_factor[i >> 4][i & 15] = f;
-      const uint64_t on = __ballot(p >= 0) >> (threadIdx.x & 48) & 0xFFFFull;  // 16 lanes hold one expert's pairs
-      if ((i & 15) == 0) s_expert[i >> 4] = int2{e, __popcll(on)};
+  const int nw = blockDim.x >> 6, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int T = a.T, H = a.H, S = a.S, P = T * a.k, strips = H / 16;
+  const int np = (int)scalar_word(a.list), shared_parts = S / 128;
+  const bool shared = (int)blockIdx.x >= a.down_wgs;
+  const uint32_t waves = (shared ? gridDim.x - a.down_wgs : a.down_wgs) * nw, at = (shared ? blockIdx.x - a.down_wgs : blockIdx.x) * nw + wave;
+  const uint64_t items = (uint64_t)(shared ? shared_parts : np) * strips;
+  const uint32_t lo = (uint32_t)(items * at / waves), hi = (uint32_t)(items * (at + 1) / waves);
+  if (!shared) {
+    const int steps = (a.I + 127) / 128, PP = a.pass_pairs;
+    const DnWave sl = dn_wave<WF>(a.seg_steps, steps, PP, NT);
+    uint8_t* lds = smem + wave * sl.bytes;
+    const DnPass* ldp = reinterpret_cast<const DnPass*>(lds + sl.rec);
+    const auto hb = buffer_of(a.hb, (uint32_t)P * NT * a.I * 2);
+    const float ts = AF == FP4_FMT_NVFP4 ? a.h_ts[0] : 1.0f;
+    for (uint32_t it = lo; it < hi;) {
+      const uint32_t pass = it / strips, s0 = it - pass * strips, s1 = min((uint32_t)strips, s0 + hi - it);
+      const DnPass* rec = a.passes + pass;
+      const int n = (int)scalar_word(&rec->n);
+      dn_run<WF, NT>(
+          a.w2, static_cast<const uint8_t*>(a.w2s), static_cast<const float*>(a.w2s), (int64_t)scalar_word(&rec->expert) * H, H, a.I, 0, steps, a.seg_steps, (int)s0, (int)s1,
+          hb, rec, n, PP, lds, a.d,
+          [&](int q, int t) __attribute__((always_inline)) { return (uint32_t)((pass_pair(rec, q) * NT + t) * a.I * 2); },
+          [&](int q) __attribute__((always_inline)) { return ldp->factor[q] * ts; },
+          [&](int q) __attribute__((always_inline)) { return pass_pair(rec, q); });
+      it += s1 - s0;
     }
-    __syncthreads();
-    dn_stream<WF, NT>(
-        a.w2, static_cast<const uint8_t*>(a.w2s), static_cast<const float*>(a.w2s), H, a.I, n0, a.seg_steps, 0,
-        ((a.I + 127) / 128 + a.seg_steps - 1) / a.seg_steps, wave, nw, a1 - a0, a.hb, (uint32_t)(T * k) * NT * a.I * 2, a.pass_pairs,
-        slots + wave * 2 * dn_slot<WF>(a.seg_steps, a.pass_pairs * NT).bytes, yl,
-        [&](int i) __attribute__((always_inline)) {
-          return int2{__builtin_amdgcn_readfirstlane(s_expert[i].x), __builtin_amdgcn_readfirstlane(s_expert[i].y)};
-        },
-        [&](int i, int q) __attribute__((always_inline)) { return (int)s_pair[i][q]; },
-        [&](int i, int q) __attribute__((always_inline)) { return s_factor[i][q]; },
-        [&](int p) __attribute__((always_inline)) { return p / k; });
   } else {
-    const int S = a.S, NB = S / 128, part = (split - a.splits) * nw + wave, parts = a.shared_splits * nw;
-    if (tid < T) s_factor[0][tid] = a.sgate[tid];
-    __syncthreads();
-    dn_stream<FP4_FMT_MXFP8, 1>(
-        a.ws2, a.ws2s, nullptr, H, S, n0, 1, part * NB / parts, (part + 1) * NB / parts, 0, 1, 1, a.shb, (uint32_t)(T * S * 2), T,
-        slots + wave * 2 * dn_slot<FP4_FMT_MXFP8>(1, T).bytes, yl,
-        [&](int) __attribute__((always_inline)) { return int2{0, T}; }, [](int, int q) __attribute__((always_inline)) { return q; },
-        [&](int, int q) __attribute__((always_inline)) { return s_factor[0][q]; }, [](int p) __attribute__((always_inline)) { return p; });
-  }
-  __syncthreads();
-  for (int q0 = tid; q0 < T * 16; q0 += th) {
-    const float* y0 = reinterpret_cast<const float*>(smem) + q0;
-    float v = 0.0f;
-    for (int i = 0; i < nw; ++i) v += y0[i * T * 16];
-    const int64_t at = (int64_t)(q0 >> 4) * H + n0 + (q0 & 15);
-    if (total > 1) __hip_atomic_store(a.ypart + (int64_t)split * T * H + at, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    else if constexpr (sizeof(OutT) == 4) static_cast<OutT*>(a.y)[at] = v;
-    else static_cast<OutT*>(a.y)[at] = __builtin_bit_cast(uint16_t, (__bf16)v);
-  }
-  if (total == 1) return;
-  __builtin_amdgcn_s_waitcnt(0);  // this thread's stores acknowledged
-  __syncthreads();
-  if (tid == 0) s_last = __hip_atomic_fetch_add(a.done + blockIdx.x, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == total - 1;
-  __syncthreads();
-  if (!s_last) return;
-  for (int q0 = tid; q0 < T * 16; q0 += th) {
-    const int64_t at = (int64_t)(q0 >> 4) * H + n0 + (q0 & 15);
-    float v = 0.0f;
-    for (int s0 = 0; s0 < total; s0 += 8) {
-      float t[8];
-#pragma unroll
-      for (int s = 0; s < 8; ++s)
-        t[s] = __hip_atomic_load(a.ypart + (int64_t)min(s0 + s, total - 1) * T * H + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-#pragma unroll
-      for (int s = 0; s < 8; ++s) v += s0 + s < total ? t[s] : 0.0f;
+    const DnWave sl = dn_wave<FP4_FMT_MXFP8>(1, 1, T, 1);
+    const auto hb = buffer_of(a.shb, (uint32_t)(T * S * 2));
+    const float gate = a.sgate[min(lane & 15, T - 1)];
+    for (uint32_t it = lo; it < hi;) {
+      const uint32_t part = it / strips, s0 = it - part * strips, s1 = min((uint32_t)strips, s0 + hi - it);
+      dn_run<FP4_FMT_MXFP8, 1>(
+          a.ws2, a.ws2s, nullptr, 0, H, S, (int)part, 1, 1, (int)s0, (int)s1, hb, nullptr, T, T, smem + wave * sl.bytes, a.d,
+          [&](int q, int) __attribute__((always_inline)) { return (uint32_t)(q * S * 2); }, [&](int) __attribute__((always_inline)) { return gate; },
+          [&](int q) __attribute__((always_inline)) { return (int)(P + part * T) + q; });
+      it += s1 - s0;
     }
-    if constexpr (sizeof(OutT) == 4) static_cast<OutT*>(a.y)[at] = v;
-    else static_cast<OutT*>(a.y)[at] = __builtin_bit_cast(uint16_t, (__bf16)v);
+  }
+}
+
+// y: the sum of a token's rows of d, in the order of its slots, then of the
+// shared expert's K steps; a lane four outputs of a token.
+template <typename OutT>
+__global__ void __launch_bounds__(256) few_sum_kernel(FewArgs a) {
+  const int quads = a.H / 4, i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.T * quads) return;
+  const int t = i / quads, c = 4 * (i - t * quads), P = a.T * a.k;
+  floatx4 v{0.f, 0.f, 0.f, 0.f};
+  auto rows = [&](int row, int step, int n) __attribute__((always_inline)) {
+    for (int j0 = 0; j0 < n; j0 += 10) {
+      floatx4 w[10];
+#pragma unroll
+      for (int j = 0; j < 10; ++j) w[j] = *reinterpret_cast<const floatx4*>(a.d + (int64_t)(row + min(j0 + j, n - 1) * step) * a.H + c);
+#pragma unroll
+      for (int j = 0; j < 10; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] += j0 + j < n ? w[j][q] : 0.0f;
+    }
+  };
+  rows(t * a.k, 1, a.list[1 + t]);
+  rows(P + t, a.T, a.S / 128);
+  OutT* y = static_cast<OutT*>(a.y) + (int64_t)t * a.H + c;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (sizeof(OutT) == 4) y[q] = v[q];
+    else y[q] = __builtin_bit_cast(uint16_t, (__bf16)v[q]);
   }
 }
 
 // --------------------------------------------------------------------- host
 
 struct FewPlan {
-  int mode, splits, shared_splits, pass_pairs, seg_steps;
+  int mode, pass_pairs, seg_steps;
   int nw, depth, dn_waves;  // gate_up: waves of a workgroup, slots of a wave's ring; down: waves of a workgroup
-  size_t wts, list, pairs, done, sgate, amax_part, h_ts, h, hb, sh, shb, ypart, total;
+  size_t list, passes, sgate, amax_part, h_ts, h, hb, sh, shb, d, total;
 };
 
 constexpr int kFewCus = 256;        // workgroups that a launch aims at: the card's compute units
 constexpr int kLds = 160 * 1024;
 constexpr int kGuLds = kLds - 256;  // dynamic LDS beside the gate_up kernel's static bytes
-constexpr int kMoreSplits = 15;     // of a strip, above the fewest
-constexpr int kDnLds = kLds - kDnSeg * (8 + kFewTokens * 6) - 64;
 
 template <int D>
 static int ring_bytes(int mode, bool shared) {
@@ -1171,14 +1225,13 @@ static int ring_bytes(int mode, bool shared) {
   }
 }
 
-// LDS of a down workgroup: the waves' sums and two slots each
-static size_t dn_smem(int mode, int T, int pairs, int m, int nw) {
-  const int rows = pairs * dn_terms(mode);
-  const DnSlot s = mode == FM_FP8 ? dn_slot<FP4_FMT_FP8_BLOCK>(m, rows)
-                   : mode == FM_NV || mode == FM_NVNV ? dn_slot<FP4_FMT_NVFP4>(m, rows) : dn_slot<FP4_FMT_MXFP4>(m, rows);
-  return (size_t)nw * (64 * T + 2 * s.bytes);
+static size_t dn_smem(int mode, int steps, int pairs, int m, int nw) {
+  const int terms = dn_terms(mode);
+  const DnWave s = mode == FM_FP8 ? dn_wave<FP4_FMT_FP8_BLOCK>(m, steps, pairs, terms)
+                   : mode == FM_NV || mode == FM_NVNV ? dn_wave<FP4_FMT_NVFP4>(m, steps, pairs, terms) : dn_wave<FP4_FMT_MXFP4>(m, steps, pairs, terms);
+  return (size_t)nw * s.bytes;
 }
-static size_t dn_smem_shared(int T, int nw) { return (size_t)nw * (64 * T + 2 * dn_slot<FP4_FMT_MXFP8>(1, T).bytes); }
+static size_t dn_smem_shared(int T, int nw) { return (size_t)nw * dn_wave<FP4_FMT_MXFP8>(1, 1, T, 1).bytes; }
 
 static int few_plan(const moe_fp4_layer* L, int64_t T, FewPlan* out) {
   FP4_CHECK(validate_layer(L, T));
@@ -1202,39 +1255,27 @@ static int few_plan(const moe_fp4_layer* L, int64_t T, FewPlan* out) {
   }
   if (p.nw == 0 && T > 0)
     return fail(FP4_ERR_UNSUPPORTED, "few-token forward: %lld tokens of width %d do not fit the LDS", (long long)T, L->hidden);
-  // down: items as long in K as they may be (whole rows lie behind each other in memory) with enough waves beside each
+  // down: slots as long in K as they may be (whole rows lie behind each other in memory) with enough waves beside each
   // other, as many pairs at once as a touched expert has on average
-  const int steps = ((int)I + 127) / 128, strips = (int)H / 16, most = p.mode == FM_FP8 ? dn_most_steps<FP4_FMT_FP8_BLOCK>() : dn_most_steps<FP4_FMT_NVFP4>();
-  const double touched = L->num_experts * (1.0 - std::pow(1.0 - (double)L->top_k / L->num_experts, (double)T));
-  p.pass_pairs = (int)std::max(1.0, std::min({std::floor((double)P / std::max(touched, 1.0) + 0.5), 16.0 / dn_terms(p.mode), (double)std::max<int64_t>(T, 1)}));
-  for (int segs = (steps + most - 1) / most; p.dn_waves < 6 && segs <= steps; ++segs) {
-    p.seg_steps = (steps + segs - 1) / segs;
-    for (p.dn_waves = kDnWaves; p.dn_waves > 1 && dn_smem(p.mode, (int)T, p.pass_pairs, p.seg_steps, p.dn_waves) > kDnLds;) --p.dn_waves;
-  }
-  // splits of a strip: the shortest rounds of the card, counting 1 us to begin a workgroup, 2 us to join splits, and items
-  // at 24 GB/s a compute unit
-  p.shared_splits = S ? (int)((S / 128 + 15) / 16) : 0;
-  const double item = 16.0 * p.seg_steps * (p.mode == FM_FP8 ? 128 : 72) / 24e3, passes = (double)((steps + p.seg_steps - 1) / p.seg_steps);
-  const int least = std::max(1, (int)((D + kDnSeg - 1) / kDnSeg));
-  double best = 1e30;
-  for (int s = least; s <= least + kMoreSplits; ++s) {
-    const int wgs = strips * (s + p.shared_splits), per = (int)std::ceil(std::ceil(touched / s) / p.dn_waves);
-    const double t = (wgs + kFewCus - 1) / kFewCus * (1.0 + per * passes * p.dn_waves * item) + (s + p.shared_splits > 1 ? 2.0 : 0.0);
-    if (t < best) {
-      best = t;
-      p.splits = s;
+  const int steps = ((int)I + 127) / 128, most = p.mode == FM_FP8 ? dn_most_steps<FP4_FMT_FP8_BLOCK>() : dn_most_steps<FP4_FMT_NVFP4>();
+  const double touched = std::max(1.0, L->num_experts * (1.0 - std::pow(1.0 - (double)L->top_k / L->num_experts, (double)T)));
+  int pairs = (int)std::max(1.0, std::min({std::floor((double)P / touched + 0.5), 16.0 / dn_terms(p.mode), (double)std::max<int64_t>(T, 1)}));
+  for (; p.dn_waves < 4 && pairs > 0; --pairs) {
+    p.pass_pairs = pairs;
+    for (int segs = (steps + most - 1) / most; p.dn_waves < 6 && segs <= steps; ++segs) {
+      p.seg_steps = (steps + segs - 1) / segs;
+      for (p.dn_waves = kDnWaves; p.dn_waves > 0 && dn_smem(p.mode, steps, pairs, p.seg_steps, p.dn_waves) > kLds;) --p.dn_waves;
     }
   }
+  if (p.dn_waves == 0) return fail(FP4_ERR_UNSUPPORTED, "few-token forward: intermediate width too large for the LDS");
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
     off += (bytes + 255) / 256 * 256;
     return at;
   };
-  p.wts = take(4 * P);
-  p.list = take(4 * (1 + D));
-  p.pairs = take(4 * D * kFewTokens);
-  p.done = take(4 * strips);
+  p.list = take(4 * (1 + kFewTokens));
+  p.passes = take(sizeof(DnPass) * P);
   p.sgate = take(4 * T);
   p.amax_part = take(4 * 2 * kFewCus);
   p.h_ts = take(4);
@@ -1242,7 +1283,7 @@ static int few_plan(const moe_fp4_layer* L, int64_t T, FewPlan* out) {
   p.hb = take(2 * nt * P * I);
   p.sh = take(4 * T * S);
   p.shb = take(2 * T * S);
-  p.ypart = take(4 * (size_t)(least + kMoreSplits + p.shared_splits) * T * H);  // for the most splits: more tokens, more bytes
+  p.d = take(4 * (P + S / 128 * T) * H);
   p.total = off;
   *out = p;
   return FP4_OK;
@@ -1251,7 +1292,7 @@ static int few_plan(const moe_fp4_layer* L, int64_t T, FewPlan* out) {
 template <int MODE, int D>
 static int launch_few(FewArgs a, const FewPlan& p, int y_dtype, hipStream_t st) {
   constexpr int AF = act_fmt(MODE);
-  static std::atomic<uint64_t> gu_raised{0}, dn32_raised{0}, dn16_raised{0};
+  static std::atomic<uint64_t> gu_raised{0}, dn_raised{0};
   FP4_CHECK(raise_dyn_lds(reinterpret_cast<const void*>(&few_gateup_kernel<MODE, D>), kGuLds, gu_raised));
   const int ring = gu_ring<MODE, D>(a.S > 0), strips = a.I / 16, max_units = std::min(a.E, a.T * a.k) * strips;
   // a unit is split between waves (each a run of its pieces) until the units there may be fill the chip's waves
@@ -1260,9 +1301,11 @@ static int launch_few(FewArgs a, const FewPlan& p, int y_dtype, hipStream_t st) 
   const int lds = gu_smem(a.T, a.E, a.k, a.H, MODE == FM_FP8, p.nw, ring, a.k_split > 1).total;
   const int per = p.nw / a.k_split, fit = kFewCus * std::max(1, std::min(2, kLds / (lds + 64)));
   int shared = 0;  // workgroups of the shared expert, by its share of the bytes
+  double share = 0;
   if (a.S > 0) {
     const double sb = 2.0 * a.S, rb = (double)std::min(a.E, a.T * a.k) * 2 * a.I * (MODE == FM_FP8 ? 1.0 : 0.55);
-    shared = std::max(1, std::min((a.S / 16 + per - 1) / per, (int)(fit * sb / (sb + rb))));
+    share = sb / (sb + rb);
+    shared = std::max(1, std::min((a.S / 16 + per - 1) / per, (int)(fit * share)));
   }
   a.routed_wgs = std::max(1, std::min(fit - shared, (max_units + per - 1) / per));
   hipLaunchKernelGGL((few_gateup_kernel<MODE, D>), dim3((unsigned)(a.routed_wgs + shared)), dim3(64 * p.nw), (size_t)lds, st, a);
@@ -1272,16 +1315,19 @@ static int launch_few(FewArgs a, const FewPlan& p, int y_dtype, hipStream_t st) 
     hipLaunchKernelGGL(few_hquant_kernel<AF>, dim3(grid_1d(lanes, 256)), dim3(256), 0, st, a);
     FP4_CHECK(check_launch("few_hquant"));
   }
-  const size_t dn_lds = std::max(dn_smem(MODE, a.T, a.pass_pairs, a.seg_steps, p.dn_waves), a.S ? dn_smem_shared(a.T, p.dn_waves) : 0);
-  const dim3 grid((unsigned)(a.H / 16), (unsigned)(a.splits + a.shared_splits)), block(64 * p.dn_waves);
-  if (y_dtype == FP4_DT_F32) {
-    FP4_CHECK(raise_dyn_lds(reinterpret_cast<const void*>(&few_down_kernel<MODE, float>), kDnLds, dn32_raised));
-    hipLaunchKernelGGL((few_down_kernel<MODE, float>), grid, block, dn_lds, st, a);
-  } else {
-    FP4_CHECK(raise_dyn_lds(reinterpret_cast<const void*>(&few_down_kernel<MODE, uint16_t>), kDnLds, dn16_raised));
-    hipLaunchKernelGGL((few_down_kernel<MODE, uint16_t>), grid, block, dn_lds, st, a);
-  }
-  return check_launch("few_down");
+  const size_t dn_lds = std::max(dn_smem(MODE, (a.I + 127) / 128, a.pass_pairs, a.seg_steps, p.dn_waves), a.S ? dn_smem_shared(a.T, p.dn_waves) : 0);
+  const int64_t strips2 = a.H / 16;
+  const int dn_fit = kFewCus * std::max(1, std::min(2, (int)(kLds / dn_lds)));
+  shared = a.S > 0 ? std::max(1, (int)(dn_fit * share)) : 0;
+  a.down_wgs = (int)std::min<int64_t>(dn_fit - shared, (strips2 * a.T * a.k + p.dn_waves - 1) / p.dn_waves);
+  const dim3 grid((unsigned)(a.down_wgs + shared)), block(64 * p.dn_waves);
+  FP4_CHECK(raise_dyn_lds(reinterpret_cast<const void*>(&few_down_kernel<MODE>), kLds, dn_raised));
+  hipLaunchKernelGGL(few_down_kernel<MODE>, grid, block, dn_lds, st, a);
+  FP4_CHECK(check_launch("few_down"));
+  const dim3 sum_grid(grid_1d((int64_t)a.T * (a.H / 4), 256));
+  if (y_dtype == FP4_DT_F32) hipLaunchKernelGGL(few_sum_kernel<float>, sum_grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL(few_sum_kernel<uint16_t>, sum_grid, dim3(256), 0, st, a);
+  return check_launch("few_sum");
 }
 
 template <int MODE>
@@ -1332,11 +1378,9 @@ int moe_fp4_forward_few(const moe_fp4_layer* L, const uint16_t* x, int64_t token
   a.x_scale = L->input_scale; a.h_scale = L->inter_scale;
   a.ws13 = L->ws13; a.ws13s = L->ws13_scale; a.ws2 = L->ws2; a.ws2s = L->ws2_scale; a.gate = L->shared_gate;
   a.T = (int)tokens; a.E = L->num_experts; a.k = L->top_k; a.H = L->hidden; a.I = L->inter; a.S = L->shared_inter;
-  a.splits = p.splits; a.shared_splits = p.shared_splits; a.pass_pairs = p.pass_pairs; a.seg_steps = p.seg_steps;
+  a.pass_pairs = p.pass_pairs; a.seg_steps = p.seg_steps;
   a.list = reinterpret_cast<int32_t*>(b + p.list);
-  a.pairs = reinterpret_cast<int32_t*>(b + p.pairs);
-  a.done = reinterpret_cast<int32_t*>(b + p.done);
-  a.wts = reinterpret_cast<float*>(b + p.wts);
+  a.passes = reinterpret_cast<DnPass*>(b + p.passes);
   a.sgate = reinterpret_cast<float*>(b + p.sgate);
   a.amax_part = reinterpret_cast<float*>(b + p.amax_part);
   a.h_ts = reinterpret_cast<float*>(b + p.h_ts);
@@ -1344,7 +1388,7 @@ int moe_fp4_forward_few(const moe_fp4_layer* L, const uint16_t* x, int64_t token
   a.hb = reinterpret_cast<uint16_t*>(b + p.hb);
   a.sh = reinterpret_cast<float*>(b + p.sh);
   a.shb = reinterpret_cast<uint16_t*>(b + p.shb);
-  a.ypart = reinterpret_cast<float*>(b + p.ypart);
+  a.d = reinterpret_cast<float*>(b + p.d);
   a.ids_out = topk_ids; a.wts_out = topk_weights; a.y = y;
   hipStream_t st = as_stream(stream);
   switch (p.mode) {
