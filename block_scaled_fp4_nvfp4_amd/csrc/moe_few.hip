@@ -85,11 +85,9 @@ struct FewArgs {
   // workspace
   int32_t* list;           // passes, then the selected experts of every token
   DnPass* passes;          // [T k]
-  float *sgate, *amax_part, *h_ts;
-  float* h;                // f32 [T k, I] (quantized modes)
-  uint16_t* hb;            // bf16 [T k, I] quantized values, or [T k, 3, I] terms
-  float* sh;               // f32 [T, S]
-  uint16_t* shb;           // bf16 [T, S]
+  float *sgate, *amax_part;
+  float* h;                // [T k, I]
+  float* sh;               // [T, S]
   float* d;                // f32 [T k + S / 128 * T, H] weighted down products of the pairs, of the shared expert's K steps
   // outputs
   int32_t* ids_out;
@@ -233,17 +231,53 @@ __device__ __forceinline__ float quantize32(float (&v)[32], float ts) {
   } else if constexpr (FMT == FP4_FMT_NVFP4) {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      float amax = 0.0f;
+      uint32_t top = 0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[16 * b + i]));
+      for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[16 * b + i]) & 0x7FFFFFFFu);
+      float amax = __uint_as_float(top);
+      const bool finite = top < 0x7F800000u;
+      if (!finite) {
+        amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[16 * b + i]));
+      }
       uint32_t sc = 0xFFu;
       if (ts > 0x1p-100f && ts < 0x1p100f) sc = e4m3_of_quotient(amax, amax / (6.0f * ts), 6.0f, ts);
       if (sc == 0xFFu) sc = ts > 0.0f ? e4m3_rne_sat_f64((double)amax / (6.0 * (double)ts)) : 0u;  // subnormal scales
       const float s = __builtin_amdgcn_cvt_f32_fp8((int)sc, 0);
-      const E2M1Thresholds th = e2m1_thresholds((double)s * (double)ts);
+      // v / unit lies between v lo and v hi (the rounded unit, its reciprocal and the products are less than 2^-21 off):
+      // where both round to the same code, so does the quotient.  One of them may not only near a border.
+      const float unit = s * ts, inv = __builtin_amdgcn_rcpf(unit), lo = inv * (1.0f - 0x1p-20f), hi = inv * (1.0f + 0x1p-20f);
+      uint32_t dl[2], dh[2];
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        v[16 * b + i] = copysignf(e2m1_mag_to_f32(e2m1_code(fabsf(v[16 * b + i]), th)) * s, v[16 * b + i]);
+      for (int w = 0; w < 2; ++w) {
+        uint32_t l = 0, h = 0;
+        const float* x = v + 16 * b + 8 * w;
+        l = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(l, x[0] * lo, x[1] * lo, 1.0f, 0);
+        l = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(l, x[2] * lo, x[3] * lo, 1.0f, 1);
+        l = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(l, x[4] * lo, x[5] * lo, 1.0f, 2);
+        l = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(l, x[6] * lo, x[7] * lo, 1.0f, 3);
+        h = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(h, x[0] * hi, x[1] * hi, 1.0f, 0);
+        h = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(h, x[2] * hi, x[3] * hi, 1.0f, 1);
+        h = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(h, x[4] * hi, x[5] * hi, 1.0f, 2);
+        h = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(h, x[6] * hi, x[7] * hi, 1.0f, 3);
+        dl[w] = l;
+        dh[w] = h;
+      }
+      if (finite && unit > 0x1p-100f && unit < 0x1p100f && dl[0] == dh[0] && dl[1] == dh[1]) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          float f[8];
+          e2m1x8_to_f32x8(dl[w], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[16 * b + 8 * w + i] = f[i] * s;
+        }
+      } else {
+        const E2M1Thresholds th = e2m1_thresholds((double)s * (double)ts);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          v[16 * b + i] = copysignf(e2m1_mag_to_f32(e2m1_code(fabsf(v[16 * b + i]), th)) * s, v[16 * b + i]);
+      }
     }
     return 1.0f;
   }
@@ -523,6 +557,17 @@ constexpr int gu_srow() { return Rows<FMT>::SSTEP * Rows<FMT>::STEPS; }
 template <int FMT>
 constexpr int gu_slot() { return 32 * (128 + gu_srow<FMT>()); }
 
+// Waits until at most the loads of n <= MOST slots are on their way.
+template <int MOST, int ND16, int ND>
+__device__ __forceinline__ void wait_slots(int n, bool by16) {
+  if (n >= MOST) {
+    if (by16) __builtin_amdgcn_s_waitcnt(vmcnt_only(ND16 * MOST));
+    else __builtin_amdgcn_s_waitcnt(vmcnt_only(ND * MOST));
+  } else if constexpr (MOST > 0) {
+    wait_slots<MOST - 1, ND16, ND>(n, by16);
+  }
+}
+
 // One wave's stream of gate_up units: in every round j < rounds it multiplies
 // the pieces [lo, hi) of a unit's 16 gate rows and 16 up rows with all tokens'
 // x~ (if j < mine) and hands the sums to finish(j, gate, up).  unit(j, codes,
@@ -548,10 +593,13 @@ __device__ __forceinline__ void gu_stream(int rounds, int mine, int lo, int hi, 
   const uint32_t odd = (uint32_t)rs | (uint32_t)(uintptr_t)scales;
   const bool by16 = SR == 16 && (odd & 15) == 0, by4 = (odd & 3) == 0;
   int lj = 0, lb = lo;
+  int ahead = 0;  // slots on their way or unread
   auto load_next = [&](int s) __attribute__((always_inline)) {
     uint8_t* to = ring + s * SLOT;
+    if (lj >= mine) return;
+    ++ahead;
     if (lb == lo) {
-      unit(min(lj, mine - 1), codes, scales);  // past the end the last unit again: every step issues as many loads
+      unit(lj, codes, scales);
       bc = buffer_of(codes, (uint32_t)(I + 16) * (uint32_t)rb);
       if (SR > 0) bs = buffer_of(scales, (uint32_t)(I + 16) * (uint32_t)rs);
     }
@@ -593,9 +641,9 @@ __device__ __forceinline__ void gu_stream(int rounds, int mine, int lo, int hi, 
       if (FMT == FP4_FMT_FP8_BLOCK) factors(j, fg, fu);
       for (int b = lo; b < hi; ++b) {
         load_next(slot == 0 ? D - 1 : slot - 1);  // read a step ago: its values are in registers
+        --ahead;
         if (SR > 0 && !by4) __builtin_amdgcn_s_waitcnt(0);
-        else if (by16) __builtin_amdgcn_s_waitcnt(vmcnt_only(ND16 * (D - 1)));
-        else __builtin_amdgcn_s_waitcnt(vmcnt_only(ND * (D - 1)));
+        else wait_slots<D - 1, ND16, ND>(ahead, by16);
         asm volatile("" ::: "memory");
         const uint8_t *cg = ring + slot * SLOT + 128 * r, *sc = ring + slot * SLOT + 32 * 128 + SR * r;
         slot = slot == D - 1 ? 0 : slot + 1;
@@ -630,7 +678,6 @@ __device__ __forceinline__ void gu_stream(int rounds, int mine, int lo, int hi, 
     }
     finish(j, ag, au);
   }
-  __builtin_amdgcn_s_waitcnt(vmcnt_only(0));  // no DMA outlives the workgroup
 }
 
 // a wave's ring of D slots (the shared expert's MXFP8 slots share its bytes)
@@ -827,15 +874,8 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
         floatx4 h;
 #pragma unroll
         for (int q = 0; q < 4; ++q) h[q] = silu_f32(ag[q] * s) * (au[q] * s);
-        if constexpr (AF == FP4_FMT_NONE) {
-          uint32_t t[4][3];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) bf16_terms(h[q], t[q]);
-#pragma unroll
-          for (int i = 0; i < 3; ++i)
-            *reinterpret_cast<u32x2*>(a.hb + (p * 3 + i) * I + i0 + 4 * g) = u32x2{t[0][i] | t[1][i] << 16, t[2][i] | t[3][i] << 16};
-        } else {
-          *reinterpret_cast<floatx4*>(a.h + p * I + i0 + 4 * g) = h;
+        *reinterpret_cast<floatx4*>(a.h + p * I + i0 + 4 * g) = h;
+        if constexpr (AF == FP4_FMT_NVFP4) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) hmax = fmaxf(hmax, fabsf(h[q]));
         }
@@ -844,66 +884,6 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
     if (hmax > 0.0f) atomicMax(&s_amax, __float_as_uint(hmax));
     __syncthreads();
     if (tid == 0) a.amax_part[blockIdx.x] = __uint_as_float(s_amax);
-  }
-}
-
-// ------------------------------------------------------------ h quantization
-
-// Quantizes h of the pairs (format AF, f32 [P, I]) and of the shared expert
-// (MXFP8, f32 [T, S]); a lane takes 32 values, the four lanes of a 128-block
-// are neighbours.
-template <int AF>
-__global__ void __launch_bounds__(256) few_hquant_kernel(FewArgs a) {
-  const int routed = AF == FP4_FMT_NONE ? 0 : a.T * a.k * (a.I / 32), shared = a.T * (a.S / 32);
-  float ts = 1.0f;
-  if constexpr (AF == FP4_FMT_NVFP4) {
-    if (a.h_scale) {
-      ts = a.h_scale[0];
-    } else {
-      float m = 0.0f;
-      for (int i = threadIdx.x & 63; i < a.routed_wgs; i += 64) m = fmaxf(m, a.amax_part[i]);
-#pragma unroll
-      for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
-      ts = (float)((double)m / kNvTensorDivisor);
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.h_ts[0] = ts;
-  }
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  float v[32];
-  auto load = [&](const float* p) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const floatx4 w = *reinterpret_cast<const floatx4*>(p + 4 * i);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[4 * i + j] = w[j];
-    }
-  };
-  if (c < routed) {
-    load(a.h + 32 * (int64_t)c);
-    const float f = quantize32<AF>(v, ts);
-    if constexpr (AF == FP4_FMT_FP8_ROW) {  // code times scale, as three terms
-      const int p = c / (a.I / 32), i0 = 32 * (c - p * (a.I / 32));
-#pragma unroll
-      for (int i = 0; i < 32; i += 8) {
-        u32x4 w[3];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t lo[3], hi[3];
-          bf16_terms(v[i + 2 * q] * f, lo);
-          bf16_terms(v[i + 2 * q + 1] * f, hi);
-#pragma unroll
-          for (int t = 0; t < 3; ++t) w[t][q] = lo[t] | hi[t] << 16;
-        }
-#pragma unroll
-        for (int t = 0; t < 3; ++t) st16(a.hb + ((int64_t)p * 3 + t) * a.I + i0 + i, w[t]);
-      }
-    } else {
-      store_bf16x32(a.hb + 32 * (int64_t)c, v);
-    }
-  } else if (c < routed + shared) {
-    load(a.sh + 32 * (int64_t)(c - routed));
-    quantize32<FP4_FMT_MXFP8>(v, ts);
-    store_bf16x32(a.shb + 32 * (int64_t)(c - routed), v);
   }
 }
 
@@ -959,36 +939,22 @@ __device__ __forceinline__ int pass_pair(const DnPass* p, int q) {
 }
 
 // One wave's down products of one pass: strips [s0, s1) of 16 outputs of an
-// expert (rows row0 + 16 strip of w), PP pairs with NT terms of h each, all of
-// K or (the shared expert) its K steps [first, first + steps).  h's rows (term *
-// PP + pair) are the columns of the MFMA tile and stay in LDS; the weights
-// stream through two slots, one being copied while the other is computed.
-// Nothing is shared between waves, so none waits for another.  h_row(pair,
-// term) gives a row's byte offset; pair q's product times factor(q) goes to
-// row out_row(q) of d.
-template <int FMT, int NT, typename HRow, typename Factor, typename OutRow>
+// expert (rows row0 + 16 strip of w), PP pairs of h, all of K or (the shared
+// expert) its K steps [first, first + steps).  The wave quantizes the pass's h
+// (format AF, tensor scale ts) itself, into NT bf16 terms: the rows term * PP +
+// pair are the columns of the MFMA tile and stay in LDS.  The weights stream
+// through two slots, one being copied while the other is computed.  Nothing is
+// shared between waves, so none waits for another.  h_row(q) is where pair q's
+// h begins; its product times factor(q) goes to row out_row(q) of d.
+template <int FMT, int AF, int NT, typename HRow, typename Factor, typename OutRow>
 __device__ __forceinline__ void dn_run(const uint8_t* w, const uint8_t* ws, const float* wf, int64_t row0, int H, int K, int first, int steps, int m, int s0, int s1,
-                                       __amdgpu_buffer_rsrc_t hb, const DnPass* rec, int n, int PP, uint8_t* lds, float* d, HRow h_row,
+                                       float ts, const DnPass* rec, int n, int PP, uint8_t* lds, float* d, HRow h_row,
                                        Factor factor, OutRow out_row) {
   using R = Rows<FMT>;
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int rb = (int)code_row_bytes<FMT>(K), rs = (int)scale_row_bytes<FMT>(K), rows = PP * NT, segs = (steps + m - 1) / m;
   const DnWave sl = dn_wave<FMT>(m, steps, PP, NT);
   const bool by4 = (((uint32_t)rs | (uint32_t)(uintptr_t)ws) & 3) == 0;
-  // the record and h
-  if (rec) {
-    const auto b = buffer_of(rec, sizeof(DnPass));
-    if (lane < (int)sizeof(DnPass) / 4) dma_buffer4(b, 4 * lane, 0, lds + sl.rec);
-  }
-  for (int pq = 0; pq < PP; ++pq)
-    for (int t = 0; t < NT; ++t) {
-      const int q = t * PP + pq;
-      const uint32_t at = h_row(pq, t) + 256 * first;
-      for (int c0 = 0; c0 < sl.hc; c0 += 64) {
-        const int c = c0 + lane - q;
-        if (c0 + lane < sl.hc) dma_buffer(hb, at + 16 * (c < 0 ? c + sl.hc : c), 0, lds + sl.h + (q * sl.hc + c0) * 16);
-      }
-    }
   // n / d = n (2^16 / d + 1) >> 16 for n < 512, d <= 32 (off by less than 512 / 2^16 < 1 / d)
   const uint32_t inv_cs = 65536u / sl.cs + 1, inv_sd = 65536u / max(sl.sd, 1) + 1;
   uint32_t coff[8], soff[4];  // a lane's byte offsets in a slot's code rows and scale rows
@@ -1029,9 +995,47 @@ __device__ __forceinline__ void dn_run(const uint8_t* w, const uint8_t* ws, cons
   const int hr = r < rows ? r : 0, rot = r - (int)(r * inv_cs >> 16) * sl.cs;
   const uint8_t* hrow = lds + sl.h + 16 * sl.hc * hr;
   float* out = reinterpret_cast<float*>(lds + sl.out);
+  issue(s0, 0, lds);
+  // the record, and h, 32 values a lane
+  if (rec) {
+    const auto b = buffer_of(rec, sizeof(DnPass));
+    if (lane < (int)sizeof(DnPass) / 4) dma_buffer4(b, 4 * lane, 0, lds + sl.rec);
+  }
+  for (int u = lane; u < PP * 4 * steps; u += 64) {
+    const int pq = u / (4 * steps), b = u - pq * 4 * steps, k = 128 * first + 32 * b;
+    float v[32];
+    const float* p = h_row(pq) + min(k, K - 32);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const floatx4 w = *reinterpret_cast<const floatx4*>(p + 4 * i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * i + j] = w[j];
+    }
+    const float f = quantize32<AF>(v, ts);
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+      u32x4 w[NT];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (NT == 1) {
+          w[0][j] = pack_exact_bf16(v[i + 2 * j], v[i + 2 * j + 1]);
+        } else {
+          uint32_t x[3], y[3];
+          bf16_terms(v[i + 2 * j] * f, x);
+          bf16_terms(v[i + 2 * j + 1] * f, y);
+#pragma unroll
+          for (int t = 0; t < 3; ++t) w[t][j] = x[t] | y[t] << 16;
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int q = t * PP + pq, c = 4 * b + i / 8 + q;
+        st16(lds + sl.h + (q * sl.hc + (c >= sl.hc ? c - sl.hc : c)) * 16, w[t]);
+      }
+    }
+  }
   int strip = s0, seg = 0, base = s0;  // base: the first strip whose products `out` holds
   uint8_t *slot = lds, *other = lds + sl.slot;
-  issue(strip, seg, slot);
   floatx4 acc{0.f, 0.f, 0.f, 0.f};
   while (strip < s1) {
     const bool end = seg + 1 == segs;
@@ -1146,29 +1150,38 @@ __global__ void __launch_bounds__(64 * kDnWaves, 2) few_down_kernel(FewArgs a) {
     const DnWave sl = dn_wave<WF>(a.seg_steps, steps, PP, NT);
     uint8_t* lds = smem + wave * sl.bytes;
     const DnPass* ldp = reinterpret_cast<const DnPass*>(lds + sl.rec);
-    const auto hb = buffer_of(a.hb, (uint32_t)P * NT * a.I * 2);
-    const float ts = AF == FP4_FMT_NVFP4 ? a.h_ts[0] : 1.0f;
+    float ts = 1.0f;
+    if constexpr (AF == FP4_FMT_NVFP4) {
+      if (a.h_scale) {
+        ts = a.h_scale[0];
+      } else {
+        float m = 0.0f;
+        for (int i = lane; i < a.routed_wgs; i += 64) m = fmaxf(m, a.amax_part[i]);
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+        ts = (float)((double)m / kNvTensorDivisor);
+      }
+    }
     for (uint32_t it = lo; it < hi;) {
       const uint32_t pass = it / strips, s0 = it - pass * strips, s1 = min((uint32_t)strips, s0 + hi - it);
       const DnPass* rec = a.passes + pass;
       const int n = (int)scalar_word(&rec->n);
-      dn_run<WF, NT>(
+      dn_run<WF, AF, NT>(
           a.w2, static_cast<const uint8_t*>(a.w2s), static_cast<const float*>(a.w2s), (int64_t)scalar_word(&rec->expert) * H, H, a.I, 0, steps, a.seg_steps, (int)s0, (int)s1,
-          hb, rec, n, PP, lds, a.d,
-          [&](int q, int t) __attribute__((always_inline)) { return (uint32_t)((pass_pair(rec, q) * NT + t) * a.I * 2); },
+          ts, rec, n, PP, lds, a.d,
+          [&](int q) __attribute__((always_inline)) { return a.h + (int64_t)(PP == 1 ? pass_pair(rec, 0) : rec->pair[q] & 511) * a.I; },
           [&](int q) __attribute__((always_inline)) { return ldp->factor[q] * ts; },
           [&](int q) __attribute__((always_inline)) { return pass_pair(rec, q); });
       it += s1 - s0;
     }
   } else {
     const DnWave sl = dn_wave<FP4_FMT_MXFP8>(1, 1, T, 1);
-    const auto hb = buffer_of(a.shb, (uint32_t)(T * S * 2));
     const float gate = a.sgate[min(lane & 15, T - 1)];
     for (uint32_t it = lo; it < hi;) {
       const uint32_t part = it / strips, s0 = it - part * strips, s1 = min((uint32_t)strips, s0 + hi - it);
-      dn_run<FP4_FMT_MXFP8, 1>(
-          a.ws2, a.ws2s, nullptr, 0, H, S, (int)part, 1, 1, (int)s0, (int)s1, hb, nullptr, T, T, smem + wave * sl.bytes, a.d,
-          [&](int q, int) __attribute__((always_inline)) { return (uint32_t)(q * S * 2); }, [&](int) __attribute__((always_inline)) { return gate; },
+      dn_run<FP4_FMT_MXFP8, FP4_FMT_MXFP8, 1>(
+          a.ws2, a.ws2s, nullptr, 0, H, S, (int)part, 1, 1, (int)s0, (int)s1, 1.0f, nullptr, T, T, smem + wave * sl.bytes, a.d,
+          [&](int q) __attribute__((always_inline)) { return a.sh + (int64_t)q * S; }, [&](int) __attribute__((always_inline)) { return gate; },
           [&](int q) __attribute__((always_inline)) { return (int)(P + part * T) + q; });
       it += s1 - s0;
     }
@@ -1209,7 +1222,7 @@ __global__ void __launch_bounds__(256) few_sum_kernel(FewArgs a) {
 struct FewPlan {
   int mode, pass_pairs, seg_steps;
   int nw, depth, dn_waves;  // gate_up: waves of a workgroup, slots of a wave's ring; down: waves of a workgroup
-  size_t list, passes, sgate, amax_part, h_ts, h, hb, sh, shb, d, total;
+  size_t list, passes, sgate, amax_part, h, sh, d, total;
 };
 
 constexpr int kFewCus = 256;        // workgroups that a launch aims at: the card's compute units
@@ -1242,7 +1255,6 @@ static int few_plan(const moe_fp4_layer* L, int64_t T, FewPlan* out) {
   const bool nv = L->w_fmt == FP4_FMT_NVFP4;
   FewPlan p{};
   p.mode = L->w_fmt == FP4_FMT_FP8_BLOCK ? FM_FP8 : L->a_fmt == FP4_FMT_NONE ? (nv ? FM_NV : FM_MX) : (nv ? FM_NVNV : FM_MXMX);
-  const int nt = L->a_fmt == FP4_FMT_NONE || L->a_fmt == FP4_FMT_FP8_ROW ? 3 : 1;
   const size_t P = (size_t)T * L->top_k, D = std::min<size_t>(P, L->num_experts), I = L->inter, S = L->shared_inter, H = L->hidden;
   // gate_up: the most waves whose rings fit beside x, with the deepest rings that do
   const int rings[][2] = {{8, 4}, {8, 3}, {8, 2}, {4, 2}, {2, 2}, {1, 2}};
@@ -1278,11 +1290,8 @@ static int few_plan(const moe_fp4_layer* L, int64_t T, FewPlan* out) {
   p.passes = take(sizeof(DnPass) * P);
   p.sgate = take(4 * T);
   p.amax_part = take(4 * 2 * kFewCus);
-  p.h_ts = take(4);
-  p.h = take(L->a_fmt == FP4_FMT_NONE ? 0 : 4 * P * I);
-  p.hb = take(2 * nt * P * I);
+  p.h = take(4 * P * I);
   p.sh = take(4 * T * S);
-  p.shb = take(2 * T * S);
   p.d = take(4 * (P + S / 128 * T) * H);
   p.total = off;
   *out = p;
@@ -1291,7 +1300,6 @@ static int few_plan(const moe_fp4_layer* L, int64_t T, FewPlan* out) {
 
 template <int MODE, int D>
 static int launch_few(FewArgs a, const FewPlan& p, int y_dtype, hipStream_t st) {
-  constexpr int AF = act_fmt(MODE);
   static std::atomic<uint64_t> gu_raised{0}, dn_raised{0};
   FP4_CHECK(raise_dyn_lds(reinterpret_cast<const void*>(&few_gateup_kernel<MODE, D>), kGuLds, gu_raised));
   const int ring = gu_ring<MODE, D>(a.S > 0), strips = a.I / 16, max_units = std::min(a.E, a.T * a.k) * strips;
@@ -1310,11 +1318,6 @@ static int launch_few(FewArgs a, const FewPlan& p, int y_dtype, hipStream_t st) 
   a.routed_wgs = std::max(1, std::min(fit - shared, (max_units + per - 1) / per));
   hipLaunchKernelGGL((few_gateup_kernel<MODE, D>), dim3((unsigned)(a.routed_wgs + shared)), dim3(64 * p.nw), (size_t)lds, st, a);
   FP4_CHECK(check_launch("few_gateup"));
-  const int64_t lanes = (AF == FP4_FMT_NONE ? 0 : (int64_t)a.T * a.k * (a.I / 32)) + (int64_t)a.T * (a.S / 32);
-  if (lanes > 0) {
-    hipLaunchKernelGGL(few_hquant_kernel<AF>, dim3(grid_1d(lanes, 256)), dim3(256), 0, st, a);
-    FP4_CHECK(check_launch("few_hquant"));
-  }
   const size_t dn_lds = std::max(dn_smem(MODE, (a.I + 127) / 128, a.pass_pairs, a.seg_steps, p.dn_waves), a.S ? dn_smem_shared(a.T, p.dn_waves) : 0);
   const int64_t strips2 = a.H / 16;
   const int dn_fit = kFewCus * std::max(1, std::min(2, (int)(kLds / dn_lds)));
@@ -1383,11 +1386,8 @@ int moe_fp4_forward_few(const moe_fp4_layer* L, const uint16_t* x, int64_t token
   a.passes = reinterpret_cast<DnPass*>(b + p.passes);
   a.sgate = reinterpret_cast<float*>(b + p.sgate);
   a.amax_part = reinterpret_cast<float*>(b + p.amax_part);
-  a.h_ts = reinterpret_cast<float*>(b + p.h_ts);
   a.h = reinterpret_cast<float*>(b + p.h);
-  a.hb = reinterpret_cast<uint16_t*>(b + p.hb);
   a.sh = reinterpret_cast<float*>(b + p.sh);
-  a.shb = reinterpret_cast<uint16_t*>(b + p.shb);
   a.d = reinterpret_cast<float*>(b + p.d);
   a.ids_out = topk_ids; a.wts_out = topk_weights; a.y = y;
   hipStream_t st = as_stream(stream);
