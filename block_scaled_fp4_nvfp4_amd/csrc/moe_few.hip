@@ -180,7 +180,7 @@ __device__ __forceinline__ half8_t wstep_frag_f16(const WStep<FP4_FMT_NVFP4>& v,
 
 // acc + 16 rows of weights times 16 columns of x (bf16, or fp16 for NVFP4).
 template <int FMT>
-__device__ __forceinline__ floatx4 gu_mfma(const WStep<FMT>& w, int j, u32x4 x, floatx4 acc) {
+__device__ __forceinline__ floatx4 w_mfma(const WStep<FMT>& w, int j, u32x4 x, floatx4 acc) {
   if constexpr (FMT == FP4_FMT_NVFP4)
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(wstep_frag_f16(w, j), __builtin_bit_cast(half8_t, x), acc, 0, 0, 0);
   else
@@ -245,32 +245,31 @@ __device__ __forceinline__ float quantize32(float (&v)[32], float ts) {
       if (ts > 0x1p-100f && ts < 0x1p100f) sc = e4m3_of_quotient(amax, amax / (6.0f * ts), 6.0f, ts);
       if (sc == 0xFFu) sc = ts > 0.0f ? e4m3_rne_sat_f64((double)amax / (6.0 * (double)ts)) : 0u;  // subnormal scales
       const float s = __builtin_amdgcn_cvt_f32_fp8((int)sc, 0);
-      // v / unit lies between v lo and v hi (the rounded unit, its reciprocal and the products are less than 2^-21 off):
-      // where both round to the same code, so does the quotient.  One of them may not only near a border.
-      const float unit = s * ts, inv = __builtin_amdgcn_rcpf(unit), lo = inv * (1.0f - 0x1p-20f), hi = inv * (1.0f + 0x1p-20f);
-      uint32_t dl[2], dh[2];
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        uint32_t l = 0, h = 0;
-        const float* x = v + 16 * b + 8 * w;
-        l = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(l, x[0] * lo, x[1] * lo, 1.0f, 0);
-        l = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(l, x[2] * lo, x[3] * lo, 1.0f, 1);
-        l = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(l, x[4] * lo, x[5] * lo, 1.0f, 2);
-        l = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(l, x[6] * lo, x[7] * lo, 1.0f, 3);
-        h = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(h, x[0] * hi, x[1] * hi, 1.0f, 0);
-        h = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(h, x[2] * hi, x[3] * hi, 1.0f, 1);
-        h = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(h, x[4] * hi, x[5] * hi, 1.0f, 2);
-        h = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(h, x[6] * hi, x[7] * hi, 1.0f, 3);
-        dl[w] = l;
-        dh[w] = h;
-      }
-      if (finite && unit > 0x1p-100f && unit < 0x1p100f && dl[0] == dh[0] && dl[1] == dh[1]) {
+      // E2M1's borders have at most 8 significant bits.  q: the quotient |v| / (s ts) rounded to 8 bits (from an f32 one
+      // that is less than 2^-21 off); the sign of the exact rest |v| - q s ts (q s has 12 bits, the fma rounds once) says
+      // on which side of q the quotient lies, and q moves a quarter of its last place there: the hardware's rounding of
+      // what results is the quotient's.
+      const float unit = s * ts, inv = __builtin_amdgcn_rcpf(unit);
+      if (finite && unit > 0x1p-100f && unit < 0x1p100f) {
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          float f[8];
-          e2m1x8_to_f32x8(dl[w], f);
+          float* x = v + 16 * b + 8 * w;
+          float q[8], f[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[16 * b + 8 * w + i] = f[i] * s;
+          for (int i = 0; i < 8; ++i) {
+            const float y = fabsf(x[i]);
+            const uint32_t n = (__float_as_uint(fminf(y * inv, 8.0f)) + 0x8000u) & 0xFFFF0000u;
+            const float rest = fmaf(-(__uint_as_float(n) * s), ts, y);
+            q[i] = __uint_as_float(n + (rest > 0.0f ? 0x4000u : rest < 0.0f ? 0u - 0x4000u : 0u));
+          }
+          uint32_t d = 0;
+          d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, q[0], q[1], 1.0f, 0);
+          d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, q[2], q[3], 1.0f, 1);
+          d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, q[4], q[5], 1.0f, 2);
+          d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, q[6], q[7], 1.0f, 3);
+          e2m1x8_to_f32x8(d, f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = copysignf(f[i] * s, x[i]);
         }
       } else {
         const E2M1Thresholds th = e2m1_thresholds((double)s * (double)ts);
@@ -441,36 +440,51 @@ __host__ __device__ inline GuSmem gu_smem(int T, int E, int k, int K, bool facto
   return s;
 }
 
-// Prepares x~ in LDS, [T][kp + 8]: bf16, or fp16 for NVFP4 weights (WF). xs[t]
-// gets the factor of a token's products, xf those of its K steps (FP8 rows).
-// Plain x meets NVFP4 weights as fp16 scaled by the power of two that brings
-// the token's largest value to [2^14, 2^15): exact down to 2^-29 of that
-// value, and 2^-40 of it off below, far inside the f32 sums' own rounding.
+// Copies x into LDS by DMA, [T][kp + 8] with zeros behind H; the last waves,
+// which route fewer tokens, first.
+__device__ __forceinline__ void copy_x(const FewArgs& a, uint8_t* sx) {
+  const int H = a.H, kp = (H + 127) / 128 * 128, T = a.T, nw = (int)blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const auto xb = buffer_of(a.x, (uint32_t)(T * H * 2));
+  for (int t = nw - 1 - wave; t < T; t += nw) {
+    uint8_t* row = sx + t * (kp + 8) * 2;
+    for (int c = 0; c < H / 8; c += 64)
+      if (c + lane < H / 8) dma_buffer(xb, (uint32_t)(t * H * 2 + 16 * (c + lane)), 0, row + 16 * c);
+    if (H / 8 + lane < kp / 8) st16(row + 16 * (H / 8 + lane), u32x4{0, 0, 0, 0});
+  }
+}
+
+__device__ __forceinline__ float amax_bf16x8(u32x4 w, float m) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
+  return m;
+}
+__device__ __forceinline__ float wave_amax(float m) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+  return m;
+}
+
+// Makes x~ of the copied x, in place: bf16, or fp16 for NVFP4 weights (WF).
+// xs[t] gets the factor of a token's products, xf those of its K steps (FP8
+// rows).  Plain x meets NVFP4 weights as fp16 scaled by the power of two that
+// brings the token's largest value to [2^14, 2^15): exact down to 2^-29 of
+// that value, and 2^-40 of it off below, far inside the f32 sums' own
+// rounding.
 template <int WF, int AF>
 __device__ __forceinline__ void prepare_x(const FewArgs& a, uint8_t* sx, float* xf, float* xs, float* tmp) {
   const int H = a.H, kp = (H + 127) / 128 * 128, T = a.T, nw = (int)blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  __builtin_amdgcn_s_waitcnt(vmcnt_only(0));  // this wave's rows of x
+  asm volatile("" ::: "memory");
   if constexpr (AF == FP4_FMT_NONE) {
-    const auto xb = buffer_of(a.x, (uint32_t)(T * H * 2));
-    for (int t = nw - 1 - wave; t < T; t += nw) {  // the waves that route fewer tokens first
+    for (int t = nw - 1 - wave; t < T; t += nw) {
       uint8_t* row = sx + t * (kp + 8) * 2;
+      int e = 15;
       if constexpr (WF == FP4_FMT_NVFP4) {
         float m = 0.0f;
-        for (int c0 = 0; c0 < H / 8; c0 += 8 * 64) {
-          u32x4 w[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = ld16(a.x + (int64_t)t * H + 8 * min(c0 + 64 * i + lane, H / 8 - 1));
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[i][j] << 16)), fabsf(__uint_as_float(w[i][j] & 0xFFFF0000u))));
-            if (c0 + 64 * i + lane < H / 8) st16(row + 16 * (c0 + 64 * i + lane), w[i]);
-          }
-        }
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
-        const int e = __builtin_amdgcn_frexp_expf(m);
-        if (lane == 0) xs[t] = ldexpf(1.0f, e - 15);
+        for (int c = lane; c < H / 8; c += 64) m = amax_bf16x8(ld16(row + 16 * c), m);
+        e = __builtin_amdgcn_frexp_expf(fminf(wave_amax(m), 3.4028234663852886e38f));
         for (int c = lane; c < H / 8; c += 64) {
           const u32x4 w = ld16(row + 16 * c);
           half8_t h;
@@ -481,28 +495,21 @@ __device__ __forceinline__ void prepare_x(const FewArgs& a, uint8_t* sx, float* 
           }
           st16(row + 16 * c, __builtin_bit_cast(u32x4, h));
         }
-      } else {  // as it is, by DMA; the caller waits for it
-        for (int c = 0; c < H / 8; c += 64)
-          if (c + lane < H / 8) dma_buffer(xb, (uint32_t)(t * H * 2 + 16 * (c + lane)), 0, row + 16 * c);
-        if (lane == 0) xs[t] = 1.0f;
       }
-      if (H / 8 + lane < kp / 8) st16(row + 16 * (H / 8 + lane), u32x4{0, 0, 0, 0});
+      if (lane == 0) xs[t] = ldexpf(1.0f, e - 15);
     }
     return;
   }
+  __syncthreads();
   float ts = 1.0f;
   if constexpr (AF == FP4_FMT_NVFP4) {
     if (a.x_scale) {
       ts = a.x_scale[0];
     } else {
       float m = 0.0f;
-      for (int c = threadIdx.x; c < T * H / 8; c += (int)blockDim.x) {
-        const u32x4 w = ld16(a.x + 8 * (int64_t)c);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
-      }
-#pragma unroll
-      for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+      for (int t = wave; t < T; t += nw)
+        for (int c = lane; c < H / 8; c += 64) m = amax_bf16x8(ld16(sx + t * (kp + 8) * 2 + 16 * c), m);
+      m = wave_amax(m);
       if (lane == 0) tmp[wave] = m;
       __syncthreads();
       m = tmp[0];
@@ -516,11 +523,12 @@ __device__ __forceinline__ void prepare_x(const FewArgs& a, uint8_t* sx, float* 
   const int per = H / 32;  // H is a multiple of 128 where x is quantized
   for (int c = threadIdx.x; c < T * per; c += (int)blockDim.x) {
     const int t = c / per, q = c - t * per;
+    uint8_t* at = sx + (t * (kp + 8) + 32 * q) * 2;
     float v[32];
-    load_bf16x32(a.x + (int64_t)t * H + 32 * q, v);
+    load_bf16x32(reinterpret_cast<const uint16_t*>(at), v);
     const float f = quantize32<AF>(v, ts);
-    if constexpr (WF == FP4_FMT_NVFP4) store_f16x32(sx + (t * (kp + 8) + 32 * q) * 2, v);
-    else store_bf16x32(sx + (t * (kp + 8) + 32 * q) * 2, v);
+    if constexpr (WF == FP4_FMT_NVFP4) store_f16x32(at, v);
+    else store_bf16x32(at, v);
     if (AF == FP4_FMT_FP8_ROW && (q & 3) == 0) xf[t * (kp / 128) + (q >> 2)] = f;
   }
 }
@@ -659,8 +667,8 @@ __device__ __forceinline__ void gu_stream(int rounds, int mine, int lo, int hi, 
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const u32x4 x = ld16(xrow + (128 * kb + 8 * q) * 2);
-            pg = gu_mfma<FMT>(wg, q, x, pg);
-            pu = gu_mfma<FMT>(wu, q, x, pu);
+            pg = w_mfma<FMT>(wg, q, x, pg);
+            pu = w_mfma<FMT>(wu, q, x, pu);
           }
           if (FMT == FP4_FMT_FP8_BLOCK) {
             const float f = xf[xt * steps + kb], fa = f * scalar_load(fg + kb), fb = f * scalar_load(fu + kb);
@@ -706,6 +714,7 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
 
   if ((int)blockIdx.x >= a.routed_wgs) {  // shared expert
     const int S = a.S, units = S / 16, wgs = gridDim.x - a.routed_wgs, first = (blockIdx.x - a.routed_wgs) * per + wave / split;
+    copy_x(a, smem + sm.x);
     prepare_x<FP4_FMT_MXFP8, FP4_FMT_MXFP8>(a, smem + sm.x, xf, xs, tmp);
     if ((int)blockIdx.x == a.routed_wgs) {  // sigmoid(x_t . g) on unquantized x
       for (int t = wave; t < T; t += nw) {
@@ -749,7 +758,7 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
   float* wts = reinterpret_cast<float*>(smem + sm.wts);
   float* scale = reinterpret_cast<float*>(smem + sm.scale);
   uint8_t* slots = smem + sm.slot;  // [listed expert][token]: the token's slot + 1
-  if constexpr (AF == FP4_FMT_NONE) prepare_x<WF, AF>(a, smem + sm.x, xf, xs, tmp);
+  copy_x(a, smem + sm.x);  // on its way while the tokens are routed
   for (int i = tid; i < min(a.E, P) * kFewTokens / 4; i += th) reinterpret_cast<uint32_t*>(slots)[i] = 0;
   if (tid == 0) s_amax = 0, s_np = 0;
   if (tid < 16) touched[tid] = 0;
@@ -781,8 +790,7 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
     if (t + nw < T) { route(std::integral_constant<int, 2>{}, t); t += 2 * nw; }
     else { route(std::integral_constant<int, 1>{}, t); t += nw; }
   }
-  if constexpr (AF != FP4_FMT_NONE) prepare_x<WF, AF>(a, smem + sm.x, xf, xs, tmp);
-  __builtin_amdgcn_s_waitcnt(vmcnt_only(0));  // x by DMA: a barrier alone does not wait for it
+  prepare_x<WF, AF>(a, smem + sm.x, xf, xs, tmp);
   __syncthreads();
   // the touched experts by id: a bit each, an expert's place in the list is the number of bits below its own
   for (int p = tid; p < P; p += th)
@@ -916,7 +924,11 @@ __host__ __device__ inline DnWave dn_wave(int m, int steps, int pairs, int terms
 }
 template <int FMT>
 constexpr int dn_most_steps() { return Rows<FMT>::FP4 ? 8 : 4; }  // of a slot: 8 DMA instructions of codes
-constexpr int dn_terms(int mode) { return act_fmt(mode) == FP4_FMT_NONE || act_fmt(mode) == FP4_FMT_FP8_ROW ? 3 : 1; }
+// terms whose sum is h: one where its quantized values are exact in a term, three in bf16 for codes times a scale (FP8)
+// and for a plain h; a plain h meets NVFP4 weights as two fp16 terms, scaled by the power of two that brings the pair's
+// largest value to [2^14, 2^15): off by less than 2^-22 of a value, or 2^-39 of that largest one, like the f32 sums' own
+// roundings
+constexpr int dn_terms(int mode) { return mode == FM_NV ? 2 : mode == FM_MX || mode == FM_FP8 ? 3 : 1; }
 
 // Waits until at most n loads are on their way (more than 15: 15).
 template <int LO = 0, int HI = 15>
@@ -1001,36 +1013,76 @@ __device__ __forceinline__ void dn_run(const uint8_t* w, const uint8_t* ws, cons
     const auto b = buffer_of(rec, sizeof(DnPass));
     if (lane < (int)sizeof(DnPass) / 4) dma_buffer4(b, 4 * lane, 0, lds + sl.rec);
   }
-  for (int u = lane; u < PP * 4 * steps; u += 64) {
-    const int pq = u / (4 * steps), b = u - pq * 4 * steps, k = 128 * first + 32 * b;
-    float v[32];
-    const float* p = h_row(pq) + min(k, K - 32);
+  const int blocks = 4 * steps;
+  auto load = [&](const float* p, int b, float (&v)[32]) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const floatx4 w = *reinterpret_cast<const floatx4*>(p + 4 * i);
+      const floatx4 w = *reinterpret_cast<const floatx4*>(p + min(128 * first + 32 * b, K - 32) + 4 * i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[4 * i + j] = w[j];
     }
-    const float f = quantize32<AF>(v, ts);
+  };
+  auto store = [&](int pq, int b, int i, const u32x4 (&w)[NT]) __attribute__((always_inline)) {  // values 8 i .. of the block
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) {
-      u32x4 w[NT];
+    for (int t = 0; t < NT; ++t) {
+      const int q = t * PP + pq, c = 4 * b + i + q;
+      st16(lds + sl.h + (q * sl.hc + (c >= sl.hc ? c - sl.hc : c)) * 16, w[t]);
+    }
+  };
+  float unscale = 1.0f;  // of pair r
+  if constexpr (NT == 2) {
+    for (int pq = 0; pq < PP; ++pq) {
+      const float* p = h_row(pq);
+      float v[32], top = 0.0f;
+      for (int b = (blocks - 1) / 64 * 64 + lane; b >= 0; b -= 64)  // the lane's first block last: its values stay
+        if (b < blocks) {
+          load(p, b, v);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (NT == 1) {
-          w[0][j] = pack_exact_bf16(v[i + 2 * j], v[i + 2 * j + 1]);
-        } else {
-          uint32_t x[3], y[3];
-          bf16_terms(v[i + 2 * j] * f, x);
-          bf16_terms(v[i + 2 * j + 1] * f, y);
+          for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(v[i]));
+        }
+      const int e = __builtin_amdgcn_frexp_expf(fminf(wave_amax(top), 3.4028234663852886e38f));
+      if (r == pq) unscale = ldexpf(1.0f, e - 15);
+      for (int b = lane; b < blocks; b += 64) {
+        if (b != lane) load(p, b, v);
 #pragma unroll
-          for (int t = 0; t < 3; ++t) w[t][j] = x[t] | y[t] << 16;
+        for (int i = 0; i < 32; i += 8) {
+          half8_t a, c;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float x = ldexpf(v[i + j], 15 - e);
+            a[j] = (_Float16)x;
+            const float rest = x - (float)a[j];  // exact; NaN after an infinity
+            c[j] = (_Float16)(rest == rest ? rest : 0.0f);
+          }
+          store(pq, b, i / 8, {__builtin_bit_cast(u32x4, a), __builtin_bit_cast(u32x4, c)});
         }
       }
+    }
+  } else {
+    for (int u = lane; u < PP * blocks; u += 64) {
+      const int pq = u / blocks, b = u - pq * blocks;
+      float v[32];
+      load(h_row(pq), b, v);
+      const float f = quantize32<AF>(v, ts);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int q = t * PP + pq, c = 4 * b + i / 8 + q;
-        st16(lds + sl.h + (q * sl.hc + (c >= sl.hc ? c - sl.hc : c)) * 16, w[t]);
+      for (int i = 0; i < 32; i += 8) {
+        u32x4 w[NT];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x = v[i + 2 * j], y = v[i + 2 * j + 1];
+          if constexpr (NT == 3) {
+            uint32_t tx[3], ty[3];
+            bf16_terms(x * f, tx);
+            bf16_terms(y * f, ty);
+#pragma unroll
+            for (int t = 0; t < 3; ++t) w[t][j] = tx[t] | ty[t] << 16;
+          } else if constexpr (FMT == FP4_FMT_NVFP4) {
+            w[0][j] = __builtin_bit_cast(uint32_t, half2_t{(_Float16)x, (_Float16)y});
+          } else {
+            w[0][j] = pack_exact_bf16(x, y);
+          }
+        }
+        store(pq, b, i / 8, w);
       }
     }
   }
@@ -1079,7 +1131,7 @@ __device__ __forceinline__ void dn_run(const uint8_t* w, const uint8_t* ws, cons
     auto product = [&](const Step& v, int s) __attribute__((always_inline)) {
       floatx4 pr = FMT == FP4_FMT_FP8_BLOCK ? floatx4{0.f, 0.f, 0.f, 0.f} : acc;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) pr = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wstep_frag<FMT>(v.w, q), __builtin_bit_cast(bf16x8_t, v.x[q]), pr, 0, 0, 0);
+      for (int q = 0; q < 4; ++q) pr = w_mfma<FMT>(v.w, q, v.x[q], pr);
       if (FMT == FP4_FMT_FP8_BLOCK) {
         const float f = scalar_load(fw + s);
 #pragma unroll
@@ -1100,12 +1152,13 @@ __device__ __forceinline__ void dn_run(const uint8_t* w, const uint8_t* ws, cons
     }
     if (end) {
       floatx4 v = acc;  // the terms' columns of a pair add up
-      if constexpr (NT == 3) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] += __shfl(acc[q], lane + PP) + __shfl(acc[q], lane + 2 * PP);
+      for (int q = 0; q < 4; ++q) {
+        if constexpr (NT == 2) v[q] += __shfl(acc[q], lane + PP);
+        if constexpr (NT == 3) v[q] += __shfl(acc[q], lane + PP) + __shfl(acc[q], lane + 2 * PP);
       }
       if (r < PP) {
-        const float f = factor(r);
+        const float f = factor(r) * unscale;
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] *= f;
         *reinterpret_cast<floatx4*>(out + (r * sl.hold + strip - base) * 16 + 4 * g) = v;
