@@ -565,24 +565,14 @@ constexpr int gu_srow() { return Rows<FMT>::SSTEP * Rows<FMT>::STEPS; }
 template <int FMT>
 constexpr int gu_slot() { return 32 * (128 + gu_srow<FMT>()); }
 
-// Waits until at most the loads of n <= MOST slots are on their way.
-template <int MOST, int ND16, int ND>
-__device__ __forceinline__ void wait_slots(int n, bool by16) {
-  if (n >= MOST) {
-    if (by16) __builtin_amdgcn_s_waitcnt(vmcnt_only(ND16 * MOST));
-    else __builtin_amdgcn_s_waitcnt(vmcnt_only(ND * MOST));
-  } else if constexpr (MOST > 0) {
-    wait_slots<MOST - 1, ND16, ND>(n, by16);
-  }
-}
-
 // One wave's stream of gate_up units: in every round j < rounds it multiplies
 // the pieces [lo, hi) of a unit's 16 gate rows and 16 up rows with all tokens'
 // x~ (if j < mine) and hands the sums to finish(j, gate, up).  unit(j, codes,
 // scales) gives a round's first gate row, factors(j, ..) its first block
 // scales of block FP8, started() runs once the first loads are on their way.
-// A ring of D slots; D - 1 are being loaded, over the rounds' borders.
-template <int FMT, int D, typename Unit, typename Factors, typename Started, typename Finish>
+// Two slots: one is loaded, over the rounds' borders, while the other is
+// multiplied (three and four slots measured the same).
+template <int FMT, typename Unit, typename Factors, typename Started, typename Finish>
 __device__ __forceinline__ void gu_stream(int rounds, int mine, int lo, int hi, int K, int I, const uint8_t* sx, const float* xf, int xt, uint8_t* ring,
                                           Unit unit, Factors factors, Started started, Finish finish) {
   using R = Rows<FMT>;
@@ -601,11 +591,8 @@ __device__ __forceinline__ void gu_stream(int rounds, int mine, int lo, int hi, 
   const uint32_t odd = (uint32_t)rs | (uint32_t)(uintptr_t)scales;
   const bool by16 = SR == 16 && (odd & 15) == 0, by4 = (odd & 3) == 0;
   int lj = 0, lb = lo;
-  int ahead = 0;  // slots on their way or unread
   auto load_next = [&](int s) __attribute__((always_inline)) {
     uint8_t* to = ring + s * SLOT;
-    if (lj >= mine) return;
-    ++ahead;
     if (lb == lo) {
       unit(lj, codes, scales);
       bc = buffer_of(codes, (uint32_t)(I + 16) * (uint32_t)rb);
@@ -636,10 +623,7 @@ __device__ __forceinline__ void gu_stream(int rounds, int mine, int lo, int hi, 
     }
     if (++lb == hi) { lb = lo; ++lj; }
   };
-  if (any) {
-#pragma unroll
-    for (int d = 0; d < D - 1; ++d) load_next(d);
-  }
+  if (any) load_next(0);
   started();
   int slot = 0;
   for (int j = 0; j < rounds; ++j) {
@@ -648,13 +632,14 @@ __device__ __forceinline__ void gu_stream(int rounds, int mine, int lo, int hi, 
       const float *fg = nullptr, *fu = nullptr;
       if (FMT == FP4_FMT_FP8_BLOCK) factors(j, fg, fu);
       for (int b = lo; b < hi; ++b) {
-        load_next(slot == 0 ? D - 1 : slot - 1);  // read a step ago: its values are in registers
-        --ahead;
-        if (SR > 0 && !by4) __builtin_amdgcn_s_waitcnt(0);
-        else wait_slots<D - 1, ND16, ND>(ahead, by16);
+        const bool more = lj < mine;
+        if (more) load_next(slot ^ 1);  // read a piece ago: its values are in registers
+        if (!more || (SR > 0 && !by4)) __builtin_amdgcn_s_waitcnt(0);
+        else if (by16) __builtin_amdgcn_s_waitcnt(vmcnt_only(ND16));
+        else __builtin_amdgcn_s_waitcnt(vmcnt_only(ND));
         asm volatile("" ::: "memory");
         const uint8_t *cg = ring + slot * SLOT + 128 * r, *sc = ring + slot * SLOT + 32 * 128 + SR * r;
-        slot = slot == D - 1 ? 0 : slot + 1;
+        slot ^= 1;
 #pragma unroll
         for (int s = 0; s < R::STEPS; ++s) {
           const int kb = R::STEPS * b + s;
@@ -688,14 +673,14 @@ __device__ __forceinline__ void gu_stream(int rounds, int mine, int lo, int hi, 
   }
 }
 
-// a wave's ring of D slots (the shared expert's MXFP8 slots share its bytes)
-template <int MODE, int D>
+// a wave's two slots (the shared expert's MXFP8 slots share their bytes)
+template <int MODE>
 __host__ __device__ constexpr int gu_ring(bool shared) {
-  constexpr int own = D * gu_slot<weight_fmt(MODE)>(), sh = D * gu_slot<FP4_FMT_MXFP8>();
+  constexpr int own = 2 * gu_slot<weight_fmt(MODE)>(), sh = 2 * gu_slot<FP4_FMT_MXFP8>();
   return shared && sh > own ? sh : own;
 }
 
-template <int MODE, int D>
+template <int MODE>
 __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a) {
   constexpr int WF = weight_fmt(MODE), AF = act_fmt(MODE);
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -706,10 +691,10 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
   const int tid = threadIdx.x, th = blockDim.x, nw = th >> 6, lane = tid & 63, g = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int T = a.T, k = a.k, H = a.H, P = T * k, split = a.k_split, ks = wave % split, per = nw / split;
-  const GuSmem sm = gu_smem(T, a.E, k, H, AF == FP4_FMT_FP8_ROW, nw, gu_ring<MODE, D>(a.S > 0), split > 1);
+  const GuSmem sm = gu_smem(T, a.E, k, H, AF == FP4_FMT_FP8_ROW, nw, gu_ring<MODE>(a.S > 0), split > 1);
   float* xf = reinterpret_cast<float*>(smem + sm.xf);
   float* red = reinterpret_cast<float*>(smem + sm.red);
-  uint8_t* ring = smem + sm.ring + wave * gu_ring<MODE, D>(a.S > 0);
+  uint8_t* ring = smem + sm.ring + wave * gu_ring<MODE>(a.S > 0);
   const int xt = min(r, T - 1);  // columns past the last token repeat it and are not kept
 
   if ((int)blockIdx.x >= a.routed_wgs) {  // shared expert
@@ -733,7 +718,7 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
     const int NB = H / 128, lo = ks * NB / split, hi = (ks + 1) * NB / split;
     const int base = (blockIdx.x - a.routed_wgs) * per, rounds = (units - base + wgs * per - 1) / (wgs * per);
     const int mine = max(0, (units - first + wgs * per - 1) / (wgs * per));
-    gu_stream<FP4_FMT_MXFP8, D>(
+    gu_stream<FP4_FMT_MXFP8>(
         rounds, mine, lo, hi, H, S, smem + sm.x, xf, xt, ring,
         [&](int j, const uint8_t*& codes, const uint8_t*& scales) __attribute__((always_inline)) {
           const int64_t row = 16 * (int64_t)(first + j * wgs * per);
@@ -852,7 +837,7 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
   constexpr int piece = 128 * Rows<WF>::STEPS;
   const int NB = (H + piece - 1) / piece, lo = ks * NB / split, hi = (ks + 1) * NB / split;
   float hmax = 0.0f;
-  gu_stream<WF, D>(
+  gu_stream<WF>(
       max(0, (units - base + step - 1) / step), max(0, (units - first + step - 1) / step), lo, hi, H, I, smem + sm.x, xf, xt, ring,
       [&](int j, const uint8_t*& codes, const uint8_t*& scales) __attribute__((always_inline)) {
         const int u = min(first + j * step, units - 1), e = __builtin_amdgcn_readfirstlane(list[u / strips]);
@@ -1274,7 +1259,7 @@ __global__ void __launch_bounds__(256) few_sum_kernel(FewArgs a) {
 
 struct FewPlan {
   int mode, pass_pairs, seg_steps;
-  int nw, depth, dn_waves;  // gate_up: waves of a workgroup, slots of a wave's ring; down: waves of a workgroup
+  int nw, dn_waves;  // waves of a gate_up, of a down workgroup
   size_t list, passes, sgate, amax_part, h, sh, d, total;
 };
 
@@ -1282,12 +1267,11 @@ constexpr int kFewCus = 256;        // workgroups that a launch aims at: the car
 constexpr int kLds = 160 * 1024;
 constexpr int kGuLds = kLds - 256;  // dynamic LDS beside the gate_up kernel's static bytes
 
-template <int D>
 static int ring_bytes(int mode, bool shared) {
   switch (mode) {
-    case FM_NV: case FM_NVNV: return gu_ring<FM_NV, D>(shared);
-    case FM_MX: case FM_MXMX: return gu_ring<FM_MX, D>(shared);
-    default: return gu_ring<FM_FP8, D>(shared);
+    case FM_NV: case FM_NVNV: return gu_ring<FM_NV>(shared);
+    case FM_MX: case FM_MXMX: return gu_ring<FM_MX>(shared);
+    default: return gu_ring<FM_FP8>(shared);
   }
 }
 
@@ -1309,15 +1293,10 @@ static int few_plan(const moe_fp4_layer* L, int64_t T, FewPlan* out) {
   FewPlan p{};
   p.mode = L->w_fmt == FP4_FMT_FP8_BLOCK ? FM_FP8 : L->a_fmt == FP4_FMT_NONE ? (nv ? FM_NV : FM_MX) : (nv ? FM_NVNV : FM_MXMX);
   const size_t P = (size_t)T * L->top_k, D = std::min<size_t>(P, L->num_experts), I = L->inter, S = L->shared_inter, H = L->hidden;
-  // gate_up: the most waves whose rings fit beside x, with the deepest rings that do
-  const int rings[][2] = {{8, 4}, {8, 3}, {8, 2}, {4, 2}, {2, 2}, {1, 2}};
-  for (auto& r : rings) {
-    const int ring = r[1] == 4 ? ring_bytes<4>(p.mode, S > 0) : r[1] == 3 ? ring_bytes<3>(p.mode, S > 0) : ring_bytes<2>(p.mode, S > 0);
-    if (p.nw == 0 && gu_smem((int)T, L->num_experts, L->top_k, L->hidden, p.mode == FM_FP8, r[0], ring, D * (I / 16) < (size_t)kFewCus * r[0]).total <= kGuLds) {
-      p.nw = r[0];
-      p.depth = r[1];
-    }
-  }
+  // gate_up: the most waves whose slots fit beside x
+  const int ring = ring_bytes(p.mode, S > 0);
+  for (int nw = kGuWaves; nw >= 1 && p.nw == 0; nw /= 2)
+    if (gu_smem((int)T, L->num_experts, L->top_k, L->hidden, p.mode == FM_FP8, nw, ring, D * (I / 16) < (size_t)kFewCus * nw).total <= kGuLds) p.nw = nw;
   if (p.nw == 0 && T > 0)
     return fail(FP4_ERR_UNSUPPORTED, "few-token forward: %lld tokens of width %d do not fit the LDS", (long long)T, L->hidden);
   // down: slots as long in K as they may be (whole rows lie behind each other in memory) with enough waves beside each
@@ -1351,11 +1330,11 @@ static int few_plan(const moe_fp4_layer* L, int64_t T, FewPlan* out) {
   return FP4_OK;
 }
 
-template <int MODE, int D>
+template <int MODE>
 static int launch_few(FewArgs a, const FewPlan& p, int y_dtype, hipStream_t st) {
   static std::atomic<uint64_t> gu_raised{0}, dn_raised{0};
-  FP4_CHECK(raise_dyn_lds(reinterpret_cast<const void*>(&few_gateup_kernel<MODE, D>), kGuLds, gu_raised));
-  const int ring = gu_ring<MODE, D>(a.S > 0), strips = a.I / 16, max_units = std::min(a.E, a.T * a.k) * strips;
+  FP4_CHECK(raise_dyn_lds(reinterpret_cast<const void*>(&few_gateup_kernel<MODE>), kGuLds, gu_raised));
+  const int ring = gu_ring<MODE>(a.S > 0), strips = a.I / 16, max_units = std::min(a.E, a.T * a.k) * strips;
   // a unit is split between waves (each a run of its pieces) until the units there may be fill the chip's waves
   a.k_split = 1;
   while (a.k_split < p.nw && max_units * a.k_split < kFewCus * p.nw) a.k_split *= 2;
@@ -1369,7 +1348,7 @@ static int launch_few(FewArgs a, const FewPlan& p, int y_dtype, hipStream_t st) 
     shared = std::max(1, std::min((a.S / 16 + per - 1) / per, (int)(fit * share)));
   }
   a.routed_wgs = std::max(1, std::min(fit - shared, (max_units + per - 1) / per));
-  hipLaunchKernelGGL((few_gateup_kernel<MODE, D>), dim3((unsigned)(a.routed_wgs + shared)), dim3(64 * p.nw), (size_t)lds, st, a);
+  hipLaunchKernelGGL((few_gateup_kernel<MODE>), dim3((unsigned)(a.routed_wgs + shared)), dim3(64 * p.nw), (size_t)lds, st, a);
   FP4_CHECK(check_launch("few_gateup"));
   const size_t dn_lds = std::max(dn_smem(MODE, (a.I + 127) / 128, a.pass_pairs, a.seg_steps, p.dn_waves), a.S ? dn_smem_shared(a.T, p.dn_waves) : 0);
   const int64_t strips2 = a.H / 16;
@@ -1384,13 +1363,6 @@ static int launch_few(FewArgs a, const FewPlan& p, int y_dtype, hipStream_t st) 
   if (y_dtype == FP4_DT_F32) hipLaunchKernelGGL(few_sum_kernel<float>, sum_grid, dim3(256), 0, st, a);
   else hipLaunchKernelGGL(few_sum_kernel<uint16_t>, sum_grid, dim3(256), 0, st, a);
   return check_launch("few_sum");
-}
-
-template <int MODE>
-static int launch_few(const FewArgs& a, const FewPlan& p, int y_dtype, hipStream_t st) {
-  if (p.depth == 4) return launch_few<MODE, 4>(a, p, y_dtype, st);
-  if (p.depth == 3) return launch_few<MODE, 3>(a, p, y_dtype, st);
-  return launch_few<MODE, 2>(a, p, y_dtype, st);
 }
 
 }  // namespace fp4
