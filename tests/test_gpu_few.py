@@ -290,3 +290,58 @@ def test_streams_and_captured_graphs():
             for a, b in zip(out, eager(x, lg)):
                 assert torch.equal(a, b), rep
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("T,E,H,I,k", [(1, 4, 256, 2304, 2), (16, 3, 128, 2304, 2), (6, 9, 384, 1280, 4), (16, 200, 128, 1152, 3)])
+def test_wide_intermediates(mode, T, E, H, I, k):
+    """K of the down products in several segments, many pairs of an expert in several passes."""
+    print_case(f"few wide {mode} T={T} E={E} H={H} I={I} k={k}")
+    _check(_layer(mode, E, H, I, k, seed=I + T), *_inputs(T, E, H, seed=E))
+
+
+@pytest.mark.parametrize("mode", ["nv", "nvnv", "mx", "mxmx"])
+@pytest.mark.parametrize("at", [2, 4, 12])
+@pytest.mark.parametrize("H,I", [(512, 256), (256, 128), (384, 384)])
+def test_scales_at_any_alignment(mode, at, H, I):
+    """Block scales that begin `at` bytes behind a multiple of 16 give the same bits."""
+    print_case(f"few scales at {at} {mode}")
+    layer = _layer(mode, 6, H, I, 2, seed=at)
+    x, lg = _inputs(3, 6, H, seed=at)
+    ref = _m().FewTokenLayer(layer, 3)(x, lg)
+    for name in ("w13_scale", "w2_scale"):
+        t = getattr(layer, name)
+        room = torch.zeros(t.numel() + 64, dtype=torch.uint8, device="cuda")
+        off = (at - room.data_ptr()) % 16
+        moved = room[off:off + t.numel()].view(t.dtype).view(t.shape)
+        moved.copy_(t)
+        setattr(layer, name, moved)
+    for a, b in zip(ref, _m().FewTokenLayer(layer, 3)(x, lg)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("sx,sh", [(0.25, 0.5), (2.0 ** -6, 2.0 ** -6), (700.0, 40.0), (1e-12, 1e-19), (2.0 ** -9 * 6, 100.0)])
+def test_static_scales_that_clip_and_tie(sx, sh):
+    """Tensor scales far from the data's (clipped blocks, subnormal and zero block scales), powers of
+    two with x on a grid of quarters (values at the borders between codes)."""
+    print_case(f"few static NVFP4 scales {sx} {sh}")
+    layer = _layer("nvnv", 8, 256, 128, 2, seed=6)
+    layer.input_scale = torch.tensor([sx / 6], device="cuda")
+    layer.inter_scale = torch.tensor([sh / 6], device="cuda")
+    x, lg = _inputs(5, 8, 256, seed=1)
+    x[::2] = torch.round(x[::2] * 4) / 4
+    x[1, :32] = 0.0
+    _check(layer, x, lg)
+
+
+def test_one_layer_for_every_count_of_tokens():
+    """One workspace, 1 to 16 tokens in turn: each call as if alone."""
+    print_case("few counts")
+    for mode in MODES:
+        layer = _layer(mode, 30, 256, 128, 3, seed=1, shared=256)
+        x, lg = _inputs(16, 30, 256, seed=2)
+        few = _m().FewTokenLayer(layer, 16)
+        for T in (16, 1, 9, 8, 2, 15, 3):
+            xs, ls = x[:T].contiguous(), lg[:T].contiguous()
+            for a, b in zip(few(xs, ls), _m().FewTokenLayer(layer, T)(xs, ls)):
+                assert torch.equal(a, b), (mode, T)

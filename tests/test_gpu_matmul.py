@@ -181,3 +181,15 @@ def test_streams_and_captured_graphs():
             gr.replay()
             assert torch.equal(y, _m().fp8_matmul(x, w)), rep
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("b,m,n,k", [(1, 2100, 3001, 640), (1, 4101, 4103, 256), (2, 1901, 4007, 256), (1, 3801, 4001, 128)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_large_products_with_ragged_edges(b, m, n, k, out):
+    """Sizes at which the larger tiles are chosen; neither m nor n is a multiple of one."""
+    print_case(f"matmul large b={b} m={m} n={n} k={k} {out}")
+    x, w = _case(b + m + n + k, b, m, n, k)
+    q = _m().quantize(x, "fp8_row")
+    y = _m().fp8_matmul(q, w, out_dtype=out)
+    _check(y, _x64(q), _w64(w))
+    assert torch.equal(y, _m().fp8_matmul(x, w, out_dtype=out))
