@@ -5,28 +5,35 @@
 //   h_tj = Qh(SiLU(G_e x~_t) * (U_e x~_t)),  e = ids[t][j],  x~ = Qx(x)
 //   y_t  = sum_j w_tj D_e h_tj  (+ sigmoid(x_t . g) * shared(x_t))
 //
-// Two kernels: routing, quantization of x and the gate_up products (every
-// workgroup routes the tokens by itself); then the down products with the
-// routing-weighted sum over experts kept on the chip, so that neither a
-// permutation nor per-pair down outputs exist.  Where h is quantized a small
-// kernel between the two does it.
+// Three kernels: routing, x~ and the gate_up products (every workgroup routes
+// the tokens by itself, so none waits for another); the down products, whose
+// waves make h~ themselves; the weighted sum of a token's products.
 //
 // What bounds it: the touched experts' weights, read once (2.76 MB an expert
-// at hidden 2560, intermediate 640 in NVFP4).  They stream through a ring of
-// blocks in LDS that belongs to one wave (16 rows x 128 bytes of codes and
-// their scales, by DMA, without barriers); loading MFMA fragments straight
+// at hidden 2560, intermediate 640 in NVFP4).  They come by DMA into LDS slots
+// that belong to one wave, without barriers; loading MFMA fragments straight
 // into registers touches four rows in every four lanes and measured twice the
-// time.  All tokens of the call are the 16 columns of one 16x16x32 bf16 MFMA
-// tile, so gate_up decodes an expert's weights once whatever the number of its
-// tokens and gathers nothing: it computes every column and keeps those of the
+// time.  All tokens of the call are the 16 columns of one 16x16x32 MFMA tile,
+// so gate_up decodes an expert's weights once whatever the number of its tokens
+// and gathers nothing: it computes every column and keeps those of the
 // expert's tokens.
 //
-// Everything the products read is exact in bf16: bf16 x, E4M3 values times
-// powers of two (MXFP8), E4M3 codes alone (FP8 rows; their scales multiply the
-// f32 sum of each 128-block), E2M1 codes times E4M3 block scales (6
-// significant bits), E2M1 codes times powers of two.  An h held in f32 (not
-// quantized, or FP8 codes times their scales) is split into three bf16 terms
-// whose sum is h (3 x 8 significant bits).  Sums are f32.
+// Measured at 512 experts, hidden 2560, intermediate 640, top 10, in graph
+// replays (us; in brackets the same layer through the router and the sorted
+// forward): NVFP4 weights 1 token 27.5 [33], 4 tokens 46 [47], 16 tokens 112
+// [96]; MXFP4/MXFP8 1 token 26 [39], 4 tokens 43 [53], 16 tokens 101 [100];
+// NVFP4/NVFP4 with a shared expert of 1280, top 5, 16 tokens 87 [129]; block
+// FP8 with that shared expert, 7 tokens 98 [130].  Of the 27.5 us at one token
+// routing takes 4.5, the list of experts 1.3, gate_up 9, the gap between two
+// kernels 1.5 each, the down products 7, the sum 2; of the 112 us at 16 tokens
+// routing and x~ 13, gate_up 56 (4.6 TB/s), the down products 34 (3.8 TB/s).
+//
+// Exactness.  Weights and x~ are exact where they meet: in fp16 for NVFP4
+// weights (E2M1 codes times E4M3 scales, 6 significant bits) with x~ of NVFP4
+// or a plain x scaled to fp16's range, in bf16 for MXFP4 (E2M1 codes times
+// powers of two) and block FP8 (E4M3 codes alone; their scales multiply the f32
+// sum of each 128-block).  An h held in f32 (not quantized, or FP8 codes times
+// their scales) is split into terms whose sum is h.  Sums are f32.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -863,10 +870,14 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
         const int ai = u / strips, i0 = (u % strips) * 16, slot = slots[ai * kFewTokens + r];
         if (slot == 0) return;  // not a token of this expert
         const int64_t p = (int64_t)r * k + slot - 1;
-        const float s = WF == FP4_FMT_NVFP4 ? scale[ai] * xs[r] : 1.0f;
         floatx4 h;
+        if constexpr (WF == FP4_FMT_NVFP4) {  // one after the other: their product may leave the f32 range
+          const float s = scale[ai], sx = xs[r];
+          ag = ag * s * sx;
+          au = au * s * sx;
+        }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) h[q] = silu_f32(ag[q] * s) * (au[q] * s);
+        for (int q = 0; q < 4; ++q) h[q] = silu_f32(ag[q]) * au[q];
         *reinterpret_cast<floatx4*>(a.h + p * I + i0 + 4 * g) = h;
         if constexpr (AF == FP4_FMT_NVFP4) {
 #pragma unroll
@@ -1143,9 +1154,9 @@ __device__ __forceinline__ void dn_run(const uint8_t* w, const uint8_t* ws, cons
         if constexpr (NT == 3) v[q] += __shfl(acc[q], lane + PP) + __shfl(acc[q], lane + 2 * PP);
       }
       if (r < PP) {
-        const float f = factor(r) * unscale;
+        const float f = factor(r);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] *= f;
+        for (int q = 0; q < 4; ++q) v[q] = v[q] * f * unscale;
         *reinterpret_cast<floatx4*>(out + (r * sl.hold + strip - base) * 16 + 4 * g) = v;
       }
       acc = floatx4{0.f, 0.f, 0.f, 0.f};
@@ -1289,6 +1300,9 @@ static int few_plan(const moe_fp4_layer* L, int64_t T, FewPlan* out) {
   if (L->num_experts > 1024) return fail(FP4_ERR_UNSUPPORTED, "few-token forward: more than 1024 experts");
   if (L->hidden > 1 << 16 || L->inter > 1 << 16 || L->shared_inter > 1 << 16)
     return fail(FP4_ERR_UNSUPPORTED, "few-token forward: a width above 65536");
+  // one expert's gate and up rows lie behind one buffer descriptor
+  if ((int64_t)(L->inter + 16) * L->hidden >> (L->w_fmt == FP4_FMT_FP8_BLOCK ? 31 : 32) || (int64_t)(L->shared_inter + 16) * L->hidden >> 31)
+    return fail(FP4_ERR_UNSUPPORTED, "few-token forward: an expert's gate_up codes of more than 2 GiB");
   const bool nv = L->w_fmt == FP4_FMT_NVFP4;
   FewPlan p{};
   p.mode = L->w_fmt == FP4_FMT_FP8_BLOCK ? FM_FP8 : L->a_fmt == FP4_FMT_NONE ? (nv ? FM_NV : FM_MX) : (nv ? FM_NVNV : FM_MXMX);
@@ -1388,7 +1402,7 @@ int moe_fp4_forward_few(const moe_fp4_layer* L, const uint16_t* x, int64_t token
   if (tokens == 0) return FP4_OK;
   if (!x || !logits || !y) return fail(FP4_ERR_INVALID_ARG, "null tensor pointer");
   FP4_CHECK(validate_layer_pointers(L));
-  // scales are read as pairs of bytes (NVFP4), bytes (MXFP4) or floats (block FP8)
+  // a lane reads block scales as a pair of bytes (NVFP4), a byte (MXFP4) or a float (block FP8)
   const uintptr_t sa = L->w_fmt == FP4_FMT_NVFP4 ? 2 : L->w_fmt == FP4_FMT_FP8_BLOCK ? 4 : 1;
   if ((uintptr_t)x % 16 || (uintptr_t)logits % 4 || (uintptr_t)bias % 4 || (uintptr_t)y % (y_dtype == FP4_DT_F32 ? 4 : 2) ||
       (uintptr_t)topk_ids % 4 || (uintptr_t)topk_weights % 4 || (uintptr_t)L->w13 % 16 || (uintptr_t)L->w2 % 16 ||

@@ -48,6 +48,9 @@ def test_layer_refusals(L):
     assert _size(L, _layer(hidden=96, inter=96), 1)[0] == 0
     assert _size(L, _layer(hidden=96, inter=96, shared_inter=128), 1)[0] == -2
     assert _size(L, _layer(hidden=4096), 8)[0] == 0 and _size(L, _layer(hidden=8192), 16)[0] == -3  # LDS
+    assert _size(L, _layer(a_fmt=0, hidden=32768, inter=65536), 1)[0] == 0
+    assert _size(L, _layer(a_fmt=0, hidden=65536, inter=65536), 1)[0] == -3  # an expert's rows exceed a buffer descriptor
+    assert _size(L, _layer(hidden=256, inter=65536), 1)[0] == -3             # two terms of h exceed the LDS
     assert L.moe_fp4_few_workspace_size(ctypes.byref(_layer()), 1, None) == -1
     assert L.moe_fp4_few_workspace_size(None, 1, ctypes.byref(ctypes.c_size_t())) == -1
     sizes = [_size(L, _layer(), t)[1] for t in range(1, 17)]
