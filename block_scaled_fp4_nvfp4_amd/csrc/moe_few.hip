@@ -1238,10 +1238,11 @@ __global__ void __launch_bounds__(64 * kDnWaves, 2) few_down_kernel(FewArgs a) {
 }
 
 // y: the sum of a token's rows of d, in the order of its slots, then of the
-// shared expert's K steps; a lane four outputs of a token.
+// shared expert's K steps; a lane four outputs of a token.  Bound by latency:
+// workgroups of one wave, over many compute units, took 1 us less than of four.
 template <typename OutT>
-__global__ void __launch_bounds__(256) few_sum_kernel(FewArgs a) {
-  const int quads = a.H / 4, i = blockIdx.x * 256 + threadIdx.x;
+__global__ void __launch_bounds__(64) few_sum_kernel(FewArgs a) {
+  const int quads = a.H / 4, i = blockIdx.x * 64 + threadIdx.x;
   if (i >= a.T * quads) return;
   const int t = i / quads, c = 4 * (i - t * quads), P = a.T * a.k;
   floatx4 v{0.f, 0.f, 0.f, 0.f};
@@ -1373,9 +1374,9 @@ static int launch_few(FewArgs a, const FewPlan& p, int y_dtype, hipStream_t st) 
   FP4_CHECK(raise_dyn_lds(reinterpret_cast<const void*>(&few_down_kernel<MODE>), kLds, dn_raised));
   hipLaunchKernelGGL(few_down_kernel<MODE>, grid, block, dn_lds, st, a);
   FP4_CHECK(check_launch("few_down"));
-  const dim3 sum_grid(grid_1d((int64_t)a.T * (a.H / 4), 256));
-  if (y_dtype == FP4_DT_F32) hipLaunchKernelGGL(few_sum_kernel<float>, sum_grid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL(few_sum_kernel<uint16_t>, sum_grid, dim3(256), 0, st, a);
+  const dim3 sum_grid(grid_1d((int64_t)a.T * (a.H / 4), 64));
+  if (y_dtype == FP4_DT_F32) hipLaunchKernelGGL(few_sum_kernel<float>, sum_grid, dim3(64), 0, st, a);
+  else hipLaunchKernelGGL(few_sum_kernel<uint16_t>, sum_grid, dim3(64), 0, st, a);
   return check_launch("few_sum");
 }
 
