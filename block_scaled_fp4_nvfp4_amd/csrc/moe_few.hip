@@ -20,13 +20,13 @@
 //
 // Measured at 512 experts, hidden 2560, intermediate 640, top 10, in graph
 // replays (us; in brackets the same layer through the router and the sorted
-// forward): NVFP4 weights 1 token 27.5 [33], 4 tokens 46 [47], 16 tokens 112
-// [96]; MXFP4/MXFP8 1 token 26 [39], 4 tokens 43 [53], 16 tokens 101 [100];
+// forward): NVFP4 weights 1 token 27 [33], 4 tokens 45 [46], 16 tokens 110
+// [95]; MXFP4/MXFP8 1 token 26 [39], 4 tokens 42 [53], 16 tokens 100 [99];
 // NVFP4/NVFP4 with a shared expert of 1280, top 5, 16 tokens 87 [129]; block
-// FP8 with that shared expert, 7 tokens 98 [130].  Of the 27.5 us at one token
-// routing takes 4.5, the list of experts 1.3, gate_up 9, the gap between two
-// kernels 1.5 each, the down products 7, the sum 2; of the 112 us at 16 tokens
-// routing and x~ 13, gate_up 56 (4.6 TB/s), the down products 34 (3.8 TB/s).
+// FP8 with that shared expert, 7 tokens 95 [129].  Of the 27 us at one token
+// routing takes 4.5, the list of experts 1.3, gate_up 9, each gap between
+// kernels 1.5, the down products 7, the sum 2; of the 110 us at 16 tokens
+// routing and x~ 12, gate_up 56 (4.6 TB/s), the down products 34 (3.8 TB/s).
 //
 // Exactness.  Weights and x~ are exact where they meet: in fp16 for NVFP4
 // weights (E2M1 codes times E4M3 scales, 6 significant bits) with x~ of NVFP4
@@ -39,6 +39,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "fp4_device.h"
 #include "host_common.h"
@@ -371,13 +372,15 @@ __device__ __forceinline__ void select_topk(const float* logits, const float* bi
   const int lane = threadIdx.x & 63;
   uint32_t key[N][PL];
   int id[N][PL], my_id[N];
+  using Order = std::conditional_t<(PL > 8), uint64_t, uint32_t>;
+  Order order[N];  // the i's of a lane's experts left, four bits each, the head's lowest
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
     const int e = lane + 64 * i;
     const float b = bias && e < E ? bias[e] : 0.0f;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      id[n][i] = e;
+      id[n][i] = i;
       key[n][i] = e < E ? route_key(logits[(int64_t)n * step * E + e] + b) : 0u;
     }
   }
@@ -396,7 +399,13 @@ __device__ __forceinline__ void select_topk(const float* logits, const float* bi
         id[n][i + 1] = swap ? ia : ib;
       }
 #pragma unroll
-  for (int n = 0; n < N; ++n) { mine[n] = 0; my_id[n] = -1; }
+  for (int n = 0; n < N; ++n) {
+    mine[n] = 0;
+    my_id[n] = -1;
+    order[n] = 0;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) order[n] |= (Order)id[n][i] << (4 * i);
+  }
   for (int j = 0; j < k; ++j) {
     uint32_t top[N];
 #pragma unroll
@@ -404,17 +413,18 @@ __device__ __forceinline__ void select_topk(const float* logits, const float* bi
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       uint64_t at = __ballot(key[n][0] == top[n]);
-      int win = __builtin_ctzll(at), e = __builtin_amdgcn_readlane(id[n][0], win);
+      int win = __builtin_ctzll(at), e = 64 * (__builtin_amdgcn_readlane((int)order[n], win) & 15) + win;
       if (top[n] != 0)
         for (at &= at - 1; at; at &= at - 1) {  // equal values: the lowest id
-          const int l = __builtin_ctzll(at), o = __builtin_amdgcn_readlane(id[n][0], l);
+          const int l = __builtin_ctzll(at), o = 64 * (__builtin_amdgcn_readlane((int)order[n], l) & 15) + l;
           if (o < e) { e = o; win = l; }
         }
       if (lane == j) { mine[n] = top[n]; my_id[n] = top[n] ? e : -1; }  // nothing selectable left: -1
       if (lane == win) {
 #pragma unroll
-        for (int i = 0; i + 1 < PL; ++i) { key[n][i] = key[n][i + 1]; id[n][i] = id[n][i + 1]; }
+        for (int i = 0; i + 1 < PL; ++i) key[n][i] = key[n][i + 1];
         key[n][PL - 1] = 0u;
+        order[n] >>= 4;
       }
     }
   }
