@@ -275,28 +275,33 @@ __global__ void __launch_bounds__(64 * NW) fp8_skinny_kernel(MatmulArgs a) {
 // touch four rows in every four lanes (it measured 1.5 to 2 times slower, the
 // more the larger the weights' share).  Chunks are XOR-swizzled by the row so
 // that the 16 rows a fragment read touches hit all banks once.  One barrier a
-// K step.
+// K step.  GROUPS groups of such waves share a tile, each with a run of its K
+// steps and a ring of its own, and the first adds the groups' sums up: a lone
+// step is mostly latency (0.33 us; deeper rings measured the same), so few
+// tiles of many steps take GROUPS times fewer of them one after another.
 constexpr int kTileTab = 24;  // K steps of scales held in LDS at once (even)
 
-template <int WM, int WN, int MS, int NS, int RING>
+template <int WM, int WN, int MS, int NS, int RING, int GROUPS>
 struct TileCfg {
   static constexpr int WAVES = WM * WN, BM = 16 * MS * WM, BN = 16 * NS * WN;
   static constexpr int STAGE = (BM + BN) * 128;
   static constexpr int XTAB = RING * STAGE;                    // f32 [kTileTab][BM]
   static constexpr int WTAB = XTAB + kTileTab * BM * 4;        // f32 [kTileTab][BN / 16]
-  static constexpr int LDS = WTAB + kTileTab * (BN / 16) * 4;
+  static constexpr int GLDS = WTAB + kTileTab * (BN / 16) * 4, LDS = GROUPS * GLDS;  // of a group, of a workgroup
   static constexpr int ND = (BM + BN) / 8 / WAVES;             // DMA instructions of a wave per K step
   static_assert((BM / 8) % WAVES == 0 && (BN / 8) % WAVES == 0, "whole DMA instructions per wave");
   static_assert(LDS <= 160 * 1024, "LDS");
 };
 
-template <int WM, int WN, int MS, int NS, int RING, typename OutT>
-__global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(MatmulArgs a, int mt, int nt) {
-  using C = TileCfg<WM, WN, MS, NS, RING>;
+template <int WM, int WN, int MS, int NS, int RING, int GROUPS, typename OutT>
+__global__ void __launch_bounds__(64 * WM * WN * GROUPS, GROUPS > 2 ? GROUPS : 2) fp8_tile_kernel(MatmulArgs a, int mt, int nt) {
+  using C = TileCfg<WM, WN, MS, NS, RING, GROUPS>;
   constexpr bool F32SUM = sizeof(OutT) == 4;
   constexpr int TH = 64 * C::WAVES, XD = C::BM / 8 / C::WAVES, WD = C::BN / 8 / C::WAVES;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[C::LDS];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, r = lane & 15;
+  __shared__ __attribute__((aligned(16))) uint8_t tile_lds[C::LDS];
+  const int group = GROUPS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / TH) : 0;
+  uint8_t* lds = tile_lds + group * C::GLDS;
+  const int tid = threadIdx.x - group * TH, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, r = lane & 15;
   const int wm = wave / WN, wn = wave % WN;
   // workgroups b, b + 8, ... run on one XCD: give it consecutive tiles (they
   // share x and W tiles in its L2), in groups of 8 rows of tiles
@@ -306,6 +311,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(MatmulArgs a,
   const int grp = t / (8 * nt), in = t - grp * 8 * nt, rows = min(8, mt - grp * 8);
   const int64_t m0 = (int64_t)(grp * 8 + in % rows) * C::BM, n0 = (int64_t)(in / rows) * C::BN, b = blockIdx.z;
   const int K = a.K, KB = K >> 7;
+  const int per_group = (KB + GROUPS - 1) / GROUPS, first = group * per_group, last = min(KB, first + per_group);  // this group's K steps
   const int64_t NB = (a.N + 127) >> 7;
   const float* xs = a.xs + (b * a.M + m0) * KB;
   const float* ws = a.ws + b * NB * KB;
@@ -336,6 +342,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(MatmulArgs a,
   // Scales of the K steps [kb0, kb0 + kTileTab): every thread's loads are
   // issued together, consecutive threads along a row's K steps.
   auto fill_tables = [&](int kb0) __attribute__((always_inline)) {
+    kb0 = min(kb0, KB - 1);
     const uint32_t n = min(kTileTab, KB - kb0), inv = ((1u << 20) + n - 1) / n;  // i / n = i inv >> 20 for i < 2^13
     constexpr int XI = (C::BM * kTileTab + TH - 1) / TH, WI = (C::BN / 16 * kTileTab + TH - 1) / TH;
     float xv[XI], wv[WI];
@@ -366,7 +373,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(MatmulArgs a,
 #pragma unroll
     for (int s = 0; s < NS; ++s) acc[i][s] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int v = 0; v < RING - 1; ++v) load(min(v, KB - 1), v);
+  for (int v = 0; v < RING - 1; ++v) load(min(first + v, KB - 1), v);
   // row 16 i + r of a tile: chunks g and 4 + g
   const int frag0 = r * 128 + 16 * (g ^ (r >> 1));
   int stage = 0;
@@ -378,6 +385,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(MatmulArgs a,
     const uint8_t* wr = lds + stage * C::STAGE + C::BM * 128 + wn * (16 * NS * 128);
     load(min(kb + RING - 1, KB - 1), stage == 0 ? RING - 1 : stage - 1);
     stage = stage == RING - 1 ? 0 : stage + 1;
+    if (GROUPS > 1 && kb >= last) return;  // the last groups may have fewer steps; every barrier is met
     float sw[NS];
 #pragma unroll
     for (int s = 0; s < NS; ++s) sw[s] = wtab[q * (C::BN / 16) + wn * NS + s];
@@ -419,19 +427,36 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(MatmulArgs a,
 #pragma unroll
       for (int s = 0; s < NS; ++s) asm volatile("" ::"v"(acc[i][s]));
   };
-  for (int kb0 = 0; kb0 < KB; kb0 += kTileTab) {
-    if (kb0 > 0) asm volatile("s_barrier" ::: "memory");  // every wave is past the tables' last use
-    fill_tables(kb0);
-    const int n = min(kTileTab, KB - kb0);
-    for (int q = 0; q < n; ++q) step(kb0 + q, q);  // the step's barrier follows the table stores
+  for (int k0 = 0; k0 < per_group; k0 += kTileTab) {
+    if (k0 > 0) asm volatile("s_barrier" ::: "memory");  // every wave is past the tables' last use
+    fill_tables(first + k0);
+    const int n = min(kTileTab, per_group - k0);
+    for (int q = 0; q < n; ++q) step(first + k0 + q, q);  // the step's barrier follows the table stores
   }
   __builtin_amdgcn_s_waitcnt(vmcnt_only(0));  // the last steps' DMA repeats step KB - 1: none outlives the workgroup
   // The tile is turned in LDS: straight from the accumulators every four lanes
   // of a store would touch four rows of y (7 of the 22 us of a lone tile's
   // fixed cost); from LDS consecutive lanes store consecutive 16 bytes.
   __syncthreads();
+  if constexpr (GROUPS > 1) {
+    static_assert(TH * MS * NS * 16 <= C::GLDS, "a group's sums fit its ring");
+    if (group > 0)
+#pragma unroll
+      for (int i = 0; i < MS; ++i)
+#pragma unroll
+        for (int s = 0; s < NS; ++s) *reinterpret_cast<floatx4*>(lds + ((i * NS + s) * TH + tid) * 16) = acc[i][s];
+    __syncthreads();
+    if (group == 0)
+#pragma unroll
+      for (int h = 1; h < GROUPS; ++h)
+#pragma unroll
+        for (int i = 0; i < MS; ++i)
+#pragma unroll
+          for (int s = 0; s < NS; ++s) acc[i][s] += *reinterpret_cast<const floatx4*>(lds + h * C::GLDS + ((i * NS + s) * TH + tid) * 16);
+  }
   constexpr int ROW = C::BN * (int)sizeof(OutT) + 16, PV = 16 / (int)sizeof(OutT), PIECES = C::BN / PV;
-  static_assert(C::BM * ROW <= C::LDS, "the output tile fits the ring");
+  static_assert(C::BM * ROW <= C::GLDS, "the output tile fits a ring");
+  if (group == 0)
 #pragma unroll
   for (int i = 0; i < MS; ++i)
 #pragma unroll
@@ -445,10 +470,10 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(MatmulArgs a,
   OutT* y = static_cast<OutT*>(a.y) + (b * a.M + m0) * a.N + n0;
   const bool vec = a.N % PV == 0 && (uintptr_t)a.y % 16 == 0;  // rows of y in whole 16-byte pieces
 #pragma unroll 4
-  for (int q = tid; q < C::BM * PIECES; q += TH) {
+  for (int q = threadIdx.x; q < C::BM * PIECES; q += TH * GROUPS) {
     const int m = q / PIECES, n = (q % PIECES) * PV;
     if (m > mlast || n > nlast) continue;
-    const u32x4 v = ld16(lds + m * ROW + n * (int)sizeof(OutT));
+    const u32x4 v = ld16(tile_lds + m * ROW + n * (int)sizeof(OutT));
     if (vec) {
       st16(y + (int64_t)m * a.N + n, v);
     } else {
@@ -463,13 +488,13 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(MatmulArgs a,
   }
 }
 
-template <int WM, int WN, int MS, int NS, int RING, typename OutT>
+template <int WM, int WN, int MS, int NS, int RING, int GROUPS, typename OutT>
 static int launch_tile(const MatmulArgs& a, int64_t batch, hipStream_t st) {
-  using C = TileCfg<WM, WN, MS, NS, RING>;
+  using C = TileCfg<WM, WN, MS, NS, RING, GROUPS>;
   const int64_t mt = (a.M + C::BM - 1) / C::BM, nt = (a.N + C::BN - 1) / C::BN;
   const int64_t grid = (mt * nt + 7) / 8 * 8;
   if (grid > INT32_MAX / 8 || batch > 65535) return fail(FP4_ERR_UNSUPPORTED, "matmul: too many rows, outputs or matrices");
-  hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, MS, NS, RING, OutT>), dim3((unsigned)grid, 1, (unsigned)batch), dim3(64 * C::WAVES), 0, st,
+  hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, MS, NS, RING, GROUPS, OutT>), dim3((unsigned)grid, 1, (unsigned)batch), dim3(64 * C::WAVES * GROUPS), 0, st,
                      a, (int)mt, (int)nt);
   return check_launch("fp8_block_matmul");
 }
@@ -516,20 +541,23 @@ struct TileModel {
 // fitted at K = 2560: a tile alone / a full round (us) 8.8 / 19.8 (64 x 64),
 // 16 / 28 (128 x 128), 27 / 36 (192 x 256), 34 / 46 (256 x 256).  Measured (us),
 // in that order: 1024 x 2560 15.4, 17.6, 28.8, 35.7; 8192 x 2560 98.8, 73.9, 68.4,
-// 78.6; 8192 x 10240 (128 up) 268, 247, 230.  f32 results take the fp16 MFMA, whose
+// 78.6; 8192 x 10240 (128 up) 268, 247, 230.  64 x 64 with the steps split over four
+// groups against without: 77 x 1000 x 2560 7.7, 8.8; 300 x 2560 x 2560 8.6, 9.4; 64 x
+// 2560 x 8192 14.8, 22.7; 512 x 2560 x 2560 15.5, 11.4.  f32 results take the fp16 MFMA, whose
 // converted operands leave registers for 64 x 64 and 128 x 128 only.
-constexpr TileModel kTile64{64, 64, 4, 2.0, 0.34, 0.89}, kTile128{128, 128, 2, 4.0, 0.60, 1.20}, kTile192{192, 256, 1, 4.4, 1.15, 1.58},
+constexpr TileModel kTile64{64, 64, 4, 2.0, 0.34, 0.89}, kTile64Split{64, 64, 1, 4.4, 0.16, 0.26}, kTile128{128, 128, 2, 4.0, 0.60, 1.20}, kTile192{192, 256, 1, 4.4, 1.15, 1.58},
     kTile256{256, 256, 1, 5.0, 1.45, 2.05};
 
 template <typename OutT>
 static int launch_tiles(const MatmulArgs& a, int64_t batch, hipStream_t st) {
-  const double t64 = kTile64.time(a, batch), t128 = kTile128.time(a, batch);
+  const double t64 = kTile64.time(a, batch), t128 = kTile128.time(a, batch), t64s = kTile64Split.time(a, batch);
   if constexpr (sizeof(OutT) == 2) {
     const double t192 = kTile192.time(a, batch), t256 = kTile256.time(a, batch);
-    if (t256 <= std::min(t192, std::min(t64, t128))) return launch_tile<2, 4, 8, 4, 2, OutT>(a, batch, st);
-    if (t192 <= std::min(t64, t128)) return launch_tile<2, 4, 6, 4, 2, OutT>(a, batch, st);
+    if (t256 <= std::min({t192, t64, t64s, t128})) return launch_tile<2, 4, 8, 4, 2, 1, OutT>(a, batch, st);
+    if (t192 <= std::min({t64, t64s, t128})) return launch_tile<2, 4, 6, 4, 2, 1, OutT>(a, batch, st);
   }
-  return t64 <= t128 ? launch_tile<2, 2, 2, 2, 2, OutT>(a, batch, st) : launch_tile<2, 2, 4, 4, 2, OutT>(a, batch, st);
+  if (t64s <= std::min(t64, t128)) return launch_tile<2, 2, 2, 2, 2, 4, OutT>(a, batch, st);
+  return t64 <= t128 ? launch_tile<2, 2, 2, 2, 2, 1, OutT>(a, batch, st) : launch_tile<2, 2, 4, 4, 2, 1, OutT>(a, batch, st);
 }
 
 constexpr int64_t kFewRows = 16;

@@ -193,3 +193,16 @@ def test_large_products_with_ragged_edges(b, m, n, k, out):
     y = _m().fp8_matmul(q, w, out_dtype=out)
     _check(y, _x64(q), _w64(w))
     assert torch.equal(y, _m().fp8_matmul(x, w, out_dtype=out))
+
+
+@pytest.mark.parametrize("b,m,n,k", [(1, 40, 200, 128 * 17), (1, 70, 129, 128 * 54), (2, 100, 130, 8192), (1, 20, 64, 128 * 97)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_few_tiles_of_many_steps(b, m, n, k, out):
+    """Sizes whose K is split between waves: runs of unequal length, more steps than a table of scales holds."""
+    print_case(f"matmul long b={b} m={m} n={n} k={k} {out}")
+    x, w = _case(b + m + n + k, b, m, n, k)
+    q = _m().quantize(x, "fp8_row")
+    y = _m().fp8_matmul(q, w, out_dtype=out)
+    _check(y, _x64(q), _w64(w))
+    assert torch.equal(y, _m().fp8_matmul(x, w, out_dtype=out))
+    assert torch.equal(y, _m().fp8_matmul(q, w, out_dtype=out))
