@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 from typing import Optional
 
@@ -251,6 +252,7 @@ def dequantize(q: dict, fmt: str, shape, out_dtype=torch.float32) -> torch.Tenso
     return out
 
 
+@functools.lru_cache(maxsize=4096)  # of the sizes alone: the library call takes 1 us of every product
 def fp8_matmul_workspace_size(x_dtype: torch.dtype, batch: int, m: int, n: int, k: int) -> int:
     """fp8_block_matmul_workspace_size for bf16 / f32 x (codes need none)."""
     need = ctypes.c_size_t()
