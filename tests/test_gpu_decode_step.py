@@ -61,3 +61,52 @@ def test_decode_step(mode, T):
         torch.cuda.synchronize()
         got = [t.clone() for t in kept]
         assert all(torch.equal(p, q) for p, q in zip(got, step(x))), rep
+
+
+def test_two_calls_at_once():
+    """Both operators on two streams at the same time, a workspace each: every result as if alone."""
+    print_case("two streams at once")
+    m, g = _m(), _gen(3)
+    H, E, k = 512, 40, 4
+    layer = _layer("nv", E, H, 256, k, seed=2)
+    w = _weight(g, 1, 1024, H)
+    xs = [torch.randn(1, t, H, device="cuda", generator=g).to(torch.bfloat16) for t in (3, 16)]
+    lg = [torch.randn(t, E, device="cuda", generator=g) for t in (3, 16)]
+    few = [m.FewTokenLayer(layer, 16) for _ in xs]
+    wide = [torch.randn(1, 40 + 60 * i, H, device="cuda", generator=g).to(torch.bfloat16) for i in range(2)]
+    alone = [(*f(x[0], l), m.fp8_matmul(a, w)) for f, x, l, a in zip(few, xs, lg, wide)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[] for _ in xs]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append((*few[i](xs[i][0], lg[i]), m.fp8_matmul(wide[i], w)))
+    torch.cuda.synchronize()
+    for i, ref in enumerate(alone):
+        for r in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(ref, r))
+
+
+@pytest.mark.parametrize("mode", ["nv", "nvnv", "mx", "mxmx", "fp8"])
+def test_what_a_workspace_held_does_not_matter(mode):
+    """Workspaces full of NaN bytes, tokens with some, one and no experts selected."""
+    print_case(f"poisoned workspace {mode}")
+    m, g = _m(), _gen(4)
+    layer = _layer(mode, 12, 256, 128, 3, seed=5, shared=128)
+    x = torch.randn(6, 256, device="cuda", generator=g).to(torch.bfloat16)
+    lg = torch.randn(6, 12, device="cuda", generator=g)
+    lg[1] = lg[5] = float("-inf")
+    lg[2, 1:] = float("-inf")
+    few = m.FewTokenLayer(layer, 6)
+    ref = [t.clone() for t in few(x, lg)]
+    for fill in (255, 0, 127):
+        few.workspace.fill_(fill)
+        assert all(torch.equal(a, b) for a, b in zip(ref, few(x, lg))), fill
+    w = _weight(g, 1, 200, 256)
+    xb = torch.randn(1, 50, 256, device="cuda", generator=g).to(torch.bfloat16)
+    ws = torch.empty(m.fp8_matmul_workspace_size(xb.dtype, 1, 50, 200, 256), dtype=torch.uint8, device="cuda")
+    y = m.fp8_matmul(xb, w)
+    for fill in (255, 0):
+        ws.fill_(fill)
+        assert torch.equal(y, m.fp8_matmul(xb, w, workspace=ws)), fill
