@@ -22,8 +22,8 @@
 // replays (us; in brackets the same layer through the router and the sorted
 // forward): NVFP4 weights 1 token 27 [33], 4 tokens 45 [46], 16 tokens 110
 // [95]; MXFP4/MXFP8 1 token 26 [39], 4 tokens 42 [53], 16 tokens 100 [99];
-// NVFP4/NVFP4 with a shared expert of 1280, top 5, 16 tokens 87 [129]; block
-// FP8 with that shared expert, 7 tokens 95 [129].  Of the 27 us at one token
+// NVFP4/NVFP4 with a shared expert of 1280, top 5, 16 tokens 86 [129]; block
+// FP8 with that shared expert, 7 tokens 93 [129].  Of the 27 us at one token
 // routing takes 4.5, the list of experts 1.3, gate_up 9, each gap between
 // kernels 1.5, the down products 7, the sum 2; of the 110 us at 16 tokens
 // routing and x~ 12, gate_up 56 (4.6 TB/s), the down products 34 (3.8 TB/s).
@@ -1365,10 +1365,11 @@ static int launch_few(FewArgs a, const FewPlan& p, int y_dtype, hipStream_t st) 
   while (a.k_split < p.nw && max_units * a.k_split < kFewCus * p.nw) a.k_split *= 2;
   const int lds = gu_smem(a.T, a.E, a.k, a.H, MODE == FM_FP8, p.nw, ring, a.k_split > 1).total;
   const int per = p.nw / a.k_split, fit = kFewCus * std::max(1, std::min(2, kLds / (lds + 64)));
-  int shared = 0;  // workgroups of the shared expert, by its share of the bytes
+  int shared = 0;  // workgroups of the shared expert, by 1.5 times its share of the bytes: its waves stage all tokens' h
+             // for each K step (shares of 1 / 1.5 / 2: 16 tokens of NVFP4/NVFP4 87.9 / 85.8 / 87.3 us, 7 of block FP8 98 / 93 / 94)
   double share = 0;
   if (a.S > 0) {
-    const double sb = 2.0 * a.S, rb = (double)std::min(a.E, a.T * a.k) * 2 * a.I * (MODE == FM_FP8 ? 1.0 : 0.55);
+    const double sb = 1.5 * 2.0 * a.S, rb = (double)std::min(a.E, a.T * a.k) * 2 * a.I * (MODE == FM_FP8 ? 1.0 : 0.55);
     share = sb / (sb + rb);
     shared = std::max(1, std::min((a.S / 16 + per - 1) / per, (int)(fit * share)));
   }

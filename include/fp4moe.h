@@ -374,7 +374,7 @@ int moe_fp4_forward_noalloc(const moe_fp4_layer* layer, const uint16_t* x, int64
  * and up to 16 with quantized ones (512 experts of hidden 2560, intermediate
  * 640, top 10, graph replays against moe_fp4_route + moe_fp4_forward: NVFP4
  * weights 1 token 27 against 33 us, 16 tokens 110 against 95; NVFP4/NVFP4 with
- * a shared expert, top 5, 16 tokens 87 against 129).
+ * a shared expert, top 5, 16 tokens 86 against 129).
  *  x            bf16 [tokens, H], finite.
  *  logits, bias f32 [tokens, E] and [E] (bias may be NULL), selected from as by
  *               moe_fp4_route.  An expert whose logit + bias is -inf (or NaN)
