@@ -145,18 +145,11 @@ struct WStep {
   }
 };
 
-// Values 8j .. 8j+7 of them as bf16 (exact).
+// Values 8j .. 8j+7 of them as bf16 (exact): MXFP4 and the E4M3 formats.
 template <int FMT>
 __device__ __forceinline__ bf16x8_t wstep_frag(const WStep<FMT>& v, int j) {
   u32x4 p;
-  if constexpr (FMT == FP4_FMT_NVFP4) {
-    const uint32_t d = v.c[0][j];
-    const float s = j < 2 ? __builtin_amdgcn_cvt_f32_fp8((int)v.s, 0) : __builtin_amdgcn_cvt_f32_fp8((int)v.s, 1);
-    float f[8];
-    e2m1x8_to_f32x8(d, f);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) p[q] = pack_exact_bf16(f[2 * q] * s, f[2 * q + 1] * s);
-  } else if constexpr (FMT == FP4_FMT_MXFP4) {
+  if constexpr (FMT == FP4_FMT_MXFP4) {
     const uint32_t d = v.c[0][j];
     const float s = ue8m0_f32(v.s);
     p.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 0));
