@@ -214,7 +214,9 @@ __device__ __forceinline__ uint32_t e4m3_exact_quotient(float a, float sigma) {
 // where the remainder is not zero) rounds on to E4M3 as the exact quotient
 // does: ties, which bf16 values hit all the time, need no branch.  Both are
 // scaled by the power of two that brings sigma into [0.5, 1), so that the
-// remainder of every quotient above E4M3's smallest midpoint is exact.
+// remainder of every quotient above E4M3's smallest midpoint is exact.  A
+// sigma of a few units of 2^-149 lies up to a third below amax / 448: quotients
+// stop at 448, above which the hardware converts to NaN (a NaN stays one).
 template <int N>
 __device__ __forceinline__ void e4m3_codes(const float (&v)[N], float sigma, uint32_t (&d)[(N + 3) / 4]) {
   const int e = -__builtin_amdgcn_frexp_expf(sigma);
@@ -228,7 +230,8 @@ __device__ __forceinline__ void e4m3_codes(const float (&v)[N], float sigma, uin
     for (int j = 0; j < 2; ++j) {
       const float a = ldexpf(fabsf(v[2 * w + j]), e), q1 = a * inv, q2 = fmaf(fmaf(-q1, s, a), inv, q1), rem = fmaf(-q2, s, a);
       const uint32_t odd = (__float_as_uint(q2) - (uint32_t)(rem < 0.0f)) | (uint32_t)(rem != 0.0f);
-      q[j] = copysignf(__uint_as_float(odd), v[2 * w + j]);
+      const float o = __uint_as_float(odd);
+      q[j] = copysignf(o > kE4M3Max ? kE4M3Max : o, v[2 * w + j]);
     }
     d[w >> 1] = (uint32_t)((w & 1) ? __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], (int)d[w >> 1], true)
                                    : __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], (int)d[w >> 1], false));
