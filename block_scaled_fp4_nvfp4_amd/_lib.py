@@ -430,11 +430,13 @@ class FewTokenLayer:
     The workspace serves one call at a time: calls on several streams, or
     captured graphs that may replay at once, need a FewTokenLayer each, which
     has to live as long as the graphs.  The layer's tensors are those at
-    construction."""
+    construction, kept here: what is set in the layer afterwards does not
+    matter."""
 
     def __init__(self, layer: MoELayer, max_tokens: int, out_dtype: torch.dtype = torch.float32):
         if out_dtype not in (torch.float32, torch.bfloat16):
             raise TypeError(f"unsupported dtype {out_dtype}")
+        layer = dataclasses.replace(layer)  # the struct's pointers are those of tensors that live as long as it
         self.layer, self.max_tokens, self.out_dtype = layer, max_tokens, out_dtype
         self.device = layer.w13.device
         self._experts, self._top_k, self._hidden = layer.num_experts, layer.top_k, layer.hidden
