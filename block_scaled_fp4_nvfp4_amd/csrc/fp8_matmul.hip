@@ -238,14 +238,12 @@ __global__ void __launch_bounds__(64 * NW) fp8_skinny_kernel(MatmulArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (u < nu) {
-        const float f = sx[u] * scalar_load(ws + ((n0 >> 7) * KB + wave + NW * u));
+        const float sw = scalar_load(ws + ((n0 >> 7) * KB + wave + NW * u));
         load_next(slot == 0 ? D - 1 : slot - 1);
         __builtin_amdgcn_s_waitcnt(vmcnt_only(2 * (D - 1)));  // this item has arrived; the D - 1 later ones may be on their way
         asm volatile("" ::: "memory");
         const uint8_t* w = ring + 2048 * slot;
-        const floatx4 p = block_product<F32SUM>(frag_of(ld16(w + frag0), ld16(w + (frag0 ^ 64))), xf[u]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[q] = fmaf(p[q], f, acc[q]);
+        add_scaled(acc, block_product<F32SUM>(frag_of(ld16(w + frag0), ld16(w + (frag0 ^ 64))), xf[u]), sx[u], sw);
         slot = slot == D - 1 ? 0 : slot + 1;
       }
     }
@@ -287,11 +285,43 @@ struct TileCfg {
   static constexpr int STAGE = (BM + BN) * 128;
   static constexpr int XTAB = RING * STAGE;                    // f32 [kTileTab][BM]
   static constexpr int WTAB = XTAB + kTileTab * BM * 4;        // f32 [kTileTab][BN / 16]
-  static constexpr int GLDS = WTAB + kTileTab * (BN / 16) * 4, LDS = GROUPS * GLDS;  // of a group, of a workgroup
+  static constexpr int GLDS = WTAB + kTileTab * (BN / 16) * 4, FARTAB = GROUPS * GLDS;  // of a group; i32 [GROUPS * WAVES] of the workgroup
+  static constexpr int LDS = FARTAB + GROUPS * WAVES * 4;
   static constexpr int ND = (BM + BN) / 8 / WAVES;             // DMA instructions of a wave per K step
   static_assert((BM / 8) % WAVES == 0 && (BN / 8) % WAVES == 0, "whole DMA instructions per wave");
   static_assert(LDS <= 160 * 1024, "LDS");
 };
+
+// One wave's 16 MS rows and 16 NS outputs from row m0 and output n0 on where
+// scales are so far from 1 that their products may leave f32's normal range:
+// from memory, one 16 x 16 tile after another, K's runs of `per_group` steps
+// each summed up by itself, as the tile kernel's groups do.  It starts over, so
+// that the tile kernel's registers need not hold both forms of a step.
+template <int GROUPS, int MS, int NS, typename OutT>
+__device__ __forceinline__ void far_tile(const MatmulArgs& a, int64_t b, int64_t m0, int64_t n0, int per_group) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15, KB = a.K >> 7;
+  const float* ws = a.ws + b * ((a.N + 127) >> 7) * KB;
+#pragma unroll 1
+  for (int i = 0; i < MS * NS; ++i) {
+    const int64_t m = m0 + 16 * (i / NS) + r, n = n0 + 16 * (i % NS);
+    // rows past the end of an operand repeat its last one; their results are not stored
+    const int64_t xm = b * a.M + min(m, a.M - 1), wn = min(n + r, a.N - 1), wt = min(n, a.N - 1) >> 7;
+    const uint8_t *x = a.x + xm * a.K + 16 * g, *w = a.w + (b * a.N + wn) * a.K + 16 * g;
+    block_sums sum{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int h = 0; h < GROUPS; ++h) {
+      block_sums acc{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int kb = h * per_group; kb < min(KB, (h + 1) * per_group); ++kb)
+        add_far_scaled(acc, block_product<sizeof(OutT) == 4>(frag_of(ld16(w + 128 * kb), ld16(w + 128 * kb + 64)), frag_of(ld16(x + 128 * kb), ld16(x + 128 * kb + 64))),
+                       a.xs[xm * KB + kb], ws[wt * KB + kb]);
+      sum += acc;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (m < a.M && n + 4 * g + c < a.N) static_cast<OutT*>(a.y)[(b * a.M + m) * a.N + n + 4 * g + c] = out_of<OutT>(sum[c]);
+  }
+}
 
 template <int WM, int WN, int MS, int NS, int RING, int GROUPS, typename OutT>
 __global__ void __launch_bounds__(64 * WM * WN * GROUPS, GROUPS > 2 ? GROUPS : 2) fp8_tile_kernel(MatmulArgs a, int mt, int nt) {
@@ -339,6 +369,7 @@ __global__ void __launch_bounds__(64 * WM * WN * GROUPS, GROUPS > 2 ? GROUPS : 2
   };
   float* xtab = reinterpret_cast<float*>(lds + C::XTAB);
   float* wtab = reinterpret_cast<float*>(lds + C::WTAB);
+  int* fartab = reinterpret_cast<int*>(tile_lds + C::FARTAB);  // whether a wave put far scales into the tables
   // Scales of the K steps [kb0, kb0 + kTileTab): every thread's loads are
   // issued together, consecutive threads along a row's K steps.
   auto fill_tables = [&](int kb0) __attribute__((always_inline)) {
@@ -356,6 +387,13 @@ __global__ void __launch_bounds__(64 * WM * WN * GROUPS, GROUPS > 2 ? GROUPS : 2
       const uint32_t i = min(tid + (uint32_t)TH * j, C::BN / 16 * n - 1), s = (i * inv) >> 20, q = i - s * n;
       wv[j] = ws[min((n0 + 16 * s) >> 7, NB - 1) * KB + kb0 + q];
     }
+    bool out = false;
+#pragma unroll
+    for (int j = 0; j < XI; ++j) out |= far_scale(xv[j]);
+#pragma unroll
+    for (int j = 0; j < WI; ++j) out |= far_scale(wv[j]);
+    const bool any = __any(out);
+    if (lane == 0) fartab[group * C::WAVES + wave] = any;
 #pragma unroll
     for (int j = 0; j < XI; ++j) {  // threads past the end repeat the last entry
       const uint32_t i = min(tid + (uint32_t)TH * j, C::BM * n - 1), m = (i * inv) >> 20, q = i - m * n;
@@ -377,6 +415,7 @@ __global__ void __launch_bounds__(64 * WM * WN * GROUPS, GROUPS > 2 ? GROUPS : 2
   // row 16 i + r of a tile: chunks g and 4 + g
   const int frag0 = r * 128 + 16 * (g ^ (r >> 1));
   int stage = 0;
+  bool far = false;  // whether the tables hold scales whose product may leave f32's normal range (of all groups)
   auto step = [&](int kb, int q) __attribute__((always_inline)) {
     // this wave's part of step kb has arrived; the RING - 2 later ones may still be on their way
     __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0(C::ND * (RING - 2)));
@@ -385,6 +424,13 @@ __global__ void __launch_bounds__(64 * WM * WN * GROUPS, GROUPS > 2 ? GROUPS : 2
     const uint8_t* wr = lds + stage * C::STAGE + C::BM * 128 + wn * (16 * NS * 128);
     load(min(kb + RING - 1, KB - 1), stage == 0 ? RING - 1 : stage - 1);
     stage = stage == RING - 1 ? 0 : stage + 1;
+    if (q == 0) {
+      int any = 0;
+#pragma unroll
+      for (int w = 0; w < GROUPS * C::WAVES; ++w) any |= fartab[w];
+      far = __builtin_amdgcn_readfirstlane(any) != 0;
+      if (far) return;
+    }
     if (GROUPS > 1 && kb >= last) return;  // the last groups may have fewer steps; every barrier is met
     float sw[NS];
 #pragma unroll
@@ -427,13 +473,17 @@ __global__ void __launch_bounds__(64 * WM * WN * GROUPS, GROUPS > 2 ? GROUPS : 2
 #pragma unroll
       for (int s = 0; s < NS; ++s) asm volatile("" ::"v"(acc[i][s]));
   };
-  for (int k0 = 0; k0 < per_group; k0 += kTileTab) {
+  for (int k0 = 0; k0 < per_group && !far; k0 += kTileTab) {
     if (k0 > 0) asm volatile("s_barrier" ::: "memory");  // every wave is past the tables' last use
     fill_tables(first + k0);
     const int n = min(kTileTab, per_group - k0);
-    for (int q = 0; q < n; ++q) step(first + k0 + q, q);  // the step's barrier follows the table stores
+    for (int q = 0; q < n && !far; ++q) step(first + k0 + q, q);  // the step's barrier follows the table stores
   }
   __builtin_amdgcn_s_waitcnt(vmcnt_only(0));  // the last steps' DMA repeats step KB - 1: none outlives the workgroup
+  if (far) {
+    if (group == 0) far_tile<GROUPS, MS, NS, OutT>(a, b, m0 + wm * 16 * MS, n0 + wn * 16 * NS, per_group);
+    return;
+  }
   // The tile is turned in LDS: straight from the accumulators every four lanes
   // of a store would touch four rows of y (7 of the 22 us of a lone tile's
   // fixed cost); from LDS consecutive lanes store consecutive 16 bytes.

@@ -71,6 +71,38 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint3
 // 1 + e^-g = inf and a signed zero, as the divide does.
 __device__ __forceinline__ float silu_f32(float g) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
+// acc += p a b for a block's four sums p and its two scales.  f = a b is one
+// rounding and p f is added in one more; where f leaves f32's normal range
+// (an infinity would make a NaN of p = 0, a subnormal loses bits) though p a b
+// need not, the scales' powers of two are applied last instead, in one step.
+// A lane's result depends on its own p, a and b alone.
+typedef float block_sums __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void add_far_scaled(block_sums& acc, const block_sums& p, float a, float b) {
+  const float f = a * b;
+  const bool normal = __builtin_amdgcn_classf(f, 0x108);
+  const float m = __builtin_amdgcn_frexp_mantf(a) * __builtin_amdgcn_frexp_mantf(b);
+  const int e = __builtin_amdgcn_frexp_expf(a) + __builtin_amdgcn_frexp_expf(b);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float near = fmaf(p[q], f, acc[q]), far = acc[q] + ldexpf(p[q] * m, e);
+    acc[q] = normal ? near : far;
+  }
+}
+__device__ __forceinline__ void add_scaled(block_sums& acc, const block_sums& p, float a, float b) {
+  const float f = a * b;
+  if (__builtin_expect(__any(!__builtin_amdgcn_classf(f, 0x108)), 0)) {
+    add_far_scaled(acc, p, a, b);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[q] = fmaf(p[q], f, acc[q]);
+  }
+}
+// Whether a scale lies outside [2^-62, 2^62]: no product of two that do not (and are not 0) leaves the normal range.
+__device__ __forceinline__ bool far_scale(float s) {
+  const uint32_t u = __float_as_uint(s) & 0x7FFFFFFFu;
+  return u != 0 && u - ((127u - 62u) << 23) > (124u << 23);
+}
+
 // A float that no lane varies and no kernel of the launch writes, by a scalar
 // load: a vector load would be waited for with all the DMA issued before it.
 __device__ __forceinline__ float scalar_load(const float* p) {
