@@ -666,12 +666,9 @@ __device__ __forceinline__ void gu_stream(int rounds, int mine, int lo, int hi, 
             pu = w_mfma<FMT>(wu, q, x, pu);
           }
           if (FMT == FP4_FMT_FP8_BLOCK) {
-            const float f = xf[xt * steps + kb], fa = f * scalar_load(fg + kb), fb = f * scalar_load(fu + kb);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              ag[q] = fmaf(pg[q], fa, ag[q]);
-              au[q] = fmaf(pu[q], fb, au[q]);
-            }
+            const float f = xf[xt * steps + kb], sg = scalar_load(fg + kb), su = scalar_load(fu + kb);
+            add_scaled(ag, pg, f, sg);
+            add_scaled(au, pu, f, su);
           } else {
             ag = pg;
             au = pu;
