@@ -97,6 +97,11 @@ __device__ __forceinline__ void add_scaled(block_sums& acc, const block_sums& p,
     for (int q = 0; q < 4; ++q) acc[q] = fmaf(p[q], f, acc[q]);
   }
 }
+// v a b by the scales' mantissas first and their powers of two last: neither a b
+// nor v a leaves f32's range where v a b does not.
+__device__ __forceinline__ float scale_by(float v, float a, float b) {
+  return ldexpf(v * (__builtin_amdgcn_frexp_mantf(a) * __builtin_amdgcn_frexp_mantf(b)), __builtin_amdgcn_frexp_expf(a) + __builtin_amdgcn_frexp_expf(b));
+}
 // Whether a scale lies outside [2^-62, 2^62]: no product of two that do not (and are not 0) leaves the normal range.
 __device__ __forceinline__ bool far_scale(float s) {
   const uint32_t u = __float_as_uint(s) & 0x7FFFFFFFu;

@@ -71,8 +71,9 @@ constexpr int act_fmt(int mode) {
 struct DnPass {
   int32_t expert, n;
   uint16_t pair[kFewTokens];  // t * k + j | t << 9; those past n repeat the first
-  int32_t pad[6];
-  float factor[kFewTokens];   // routing weight times the expert's tensor scale
+  float scale;                // the expert's tensor scale
+  int32_t pad[5];
+  float factor[kFewTokens];   // routing weight
 };
 static_assert(sizeof(DnPass) == 128);
 
@@ -824,10 +825,11 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
         if (sl[t] == 0) continue;
         const int p = t * k + sl[t] - 1;
         pass->pair[q] = (uint16_t)(p | t << 9);
-        pass->factor[q] = wts[p] * f;
+        pass->factor[q] = wts[p];
         --n;
         if (++q == a.pass_pairs || n == 0) {
           pass->expert = list[i];
+          pass->scale = f;
           pass->n = q;
           for (; q < a.pass_pairs; ++q) pass->pair[q] = pass->pair[0];
           ++pass;
@@ -871,10 +873,13 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
         if (slot == 0) return;  // not a token of this expert
         const int64_t p = (int64_t)r * k + slot - 1;
         floatx4 h;
-        if constexpr (WF == FP4_FMT_NVFP4) {  // one after the other: their product may leave the f32 range
+        if constexpr (WF == FP4_FMT_NVFP4) {
           const float s = scale[ai], sx = xs[r];
-          ag = ag * s * sx;
-          au = au * s * sx;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            ag[q] = scale_by(ag[q], s, sx);
+            au[q] = scale_by(au[q], s, sx);
+          }
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) h[q] = silu_f32(ag[q]) * au[q];
@@ -953,10 +958,10 @@ __device__ __forceinline__ int pass_pair(const DnPass* p, int q) {
 // pair are the columns of the MFMA tile and stay in LDS.  The weights stream
 // through two slots, one being copied while the other is computed.  Nothing is
 // shared between waves, so none waits for another.  h_row(q) is where pair q's
-// h begins; its product times factor(q) goes to row out_row(q) of d.
+// h begins; its product times factor(q), wscale and ts goes to row out_row(q) of d.
 template <int FMT, int AF, int NT, typename HRow, typename Factor, typename OutRow>
 __device__ __forceinline__ void dn_run(const uint8_t* w, const uint8_t* ws, const float* wf, int64_t row0, int H, int K, int first, int steps, int m, int s0, int s1,
-                                       float ts, const DnPass* rec, int n, int PP, uint8_t* lds, float* d, HRow h_row,
+                                       float ts, float wscale, const DnPass* rec, int n, int PP, uint8_t* lds, float* d, HRow h_row,
                                        Factor factor, OutRow out_row) {
   using R = Rows<FMT>;
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
@@ -1156,7 +1161,7 @@ __device__ __forceinline__ void dn_run(const uint8_t* w, const uint8_t* ws, cons
       if (r < PP) {
         const float f = factor(r);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = v[q] * f * unscale;
+        for (int q = 0; q < 4; ++q) v[q] = scale_by(v[q] * f, wscale, NT == 2 ? unscale : ts);
         *reinterpret_cast<floatx4*>(out + (r * sl.hold + strip - base) * 16 + 4 * g) = v;
       }
       acc = floatx4{0.f, 0.f, 0.f, 0.f};
@@ -1217,9 +1222,9 @@ __global__ void __launch_bounds__(64 * kDnWaves, 2) few_down_kernel(FewArgs a) {
       const int n = (int)scalar_word(&rec->n);
       dn_run<WF, AF, NT>(
           a.w2, static_cast<const uint8_t*>(a.w2s), static_cast<const float*>(a.w2s), (int64_t)scalar_word(&rec->expert) * H, H, a.I, 0, steps, a.seg_steps, (int)s0, (int)s1,
-          ts, rec, n, PP, lds, a.d,
+          ts, __uint_as_float(scalar_word(&rec->scale)), rec, n, PP, lds, a.d,
           [&](int q) __attribute__((always_inline)) { return a.h + (int64_t)(PP == 1 ? pass_pair(rec, 0) : rec->pair[q] & 511) * a.I; },
-          [&](int q) __attribute__((always_inline)) { return ldp->factor[q] * ts; },
+          [&](int q) __attribute__((always_inline)) { return ldp->factor[q]; },
           [&](int q) __attribute__((always_inline)) { return pass_pair(rec, q); });
       it += s1 - s0;
     }
@@ -1229,7 +1234,7 @@ __global__ void __launch_bounds__(64 * kDnWaves, 2) few_down_kernel(FewArgs a) {
     for (uint32_t it = lo; it < hi;) {
       const uint32_t part = it / strips, s0 = it - part * strips, s1 = min((uint32_t)strips, s0 + hi - it);
       dn_run<FP4_FMT_MXFP8, FP4_FMT_MXFP8, 1>(
-          a.ws2, a.ws2s, nullptr, 0, H, S, (int)part, 1, 1, (int)s0, (int)s1, 1.0f, nullptr, T, T, smem + wave * sl.bytes, a.d,
+          a.ws2, a.ws2s, nullptr, 0, H, S, (int)part, 1, 1, (int)s0, (int)s1, 1.0f, 1.0f, nullptr, T, T, smem + wave * sl.bytes, a.d,
           [&](int q) __attribute__((always_inline)) { return a.sh + (int64_t)q * S; }, [&](int) __attribute__((always_inline)) { return gate; },
           [&](int q) __attribute__((always_inline)) { return (int)(P + part * T) + q; });
       it += s1 - s0;

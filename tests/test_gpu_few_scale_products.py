@@ -47,3 +47,18 @@ def test_layer_with_zero_sums_of_huge_scales():
     layer.w13_scale[:, :, 1] = 2.0 ** 100
     for a, b in zip(ref, _m().FewTokenLayer(layer, 4)(x, lg)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T", [2, 9])
+def test_nvfp4_layer_with_tiny_tensor_scales(T):
+    """NVFP4 / NVFP4 with w2's and h's tensor scales about 2^-75 each: their product, with the routing
+    weight, is a subnormal f32 of few bits, y is not (its block scales and codes bring 2^22)."""
+    print_case(f"few tensor scales T={T}")
+    layer = _layer("nvnv", 6, 256, 128, 2, seed=T)
+    x, lg = _inputs(T, 6, 256, seed=T)
+    for name, f in (("w13_scale_2", 2.0 ** -31), ("w2_scale_2", 2.0 ** -58)):
+        setattr(layer, name, getattr(layer, name) * f)
+    y, ids, _ = _m().FewTokenLayer(layer, T)(x, lg)
+    e_ids, _, e_y = _expected(layer, x, lg, None)
+    np.testing.assert_array_equal(host(ids), e_ids)
+    assert rel_fro(host(y).astype(np.float64) * 2.0 ** 100, e_y * 2.0 ** 100) <= 2e-3
