@@ -417,6 +417,38 @@ def moe_forward_noalloc(layer: MoELayer, x: torch.Tensor, topk_ids: torch.Tensor
     return y
 
 
+def _layer_fault(layer: MoELayer) -> Optional[str]:
+    """What the kernels could not read safely of the layer's tensors (None: nothing):
+    all lie on w13's device, contiguous, and are as large as the layer's sizes ask."""
+    E, H, I, S = layer.num_experts, layer.hidden, layer.inter, layer.shared_inter
+    u8, f32 = 1, torch.float32
+    if layer.w_fmt == "fp8_block":
+        rows = lambda n, k: (n * k, u8, (n // 128) * (k // 128), f32)
+    else:
+        rows = lambda n, k: (n * k // 2, u8, n * k // (16 if layer.w_fmt == "nvfp4" else 32), u8)
+    need = {}
+    for name, n, k in (("w13", E * 2 * I, H), ("w2", E * H, I)):
+        codes, ct, scales, st = rows(n, k)
+        need[name], need[name + "_scale"] = (codes, ct), (scales, st)
+        if layer.w_fmt == "nvfp4":
+            need[name + "_scale_2"] = (E, f32)
+    if layer.a_fmt == "nvfp4":
+        need["input_scale"] = need["inter_scale"] = (1, f32)
+    if S > 0:
+        need.update(ws13=(2 * S * H, u8), ws13_scale=(2 * S * H // 32, u8), ws2=(H * S, u8), ws2_scale=(H * S // 32, u8),
+                    shared_gate=(H, torch.bfloat16))
+    dev = layer.w13.device
+    for name, (n, kind) in need.items():
+        t = getattr(layer, name)
+        if t is None:  # the library says which it needs
+            continue
+        right = t.element_size() == 1 if kind == u8 else t.dtype == kind
+        if t.device != dev or not t.is_contiguous() or not right or t.numel() < n:
+            return (f"layer.{name}: {n} contiguous values of {'one byte' if kind == u8 else kind} on {dev} expected, got "
+                    f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return None if dev.type == "cuda" else f"device tensors expected, got {dev}"
+
+
 class FewTokenLayer:
     """A whole routed-expert layer for a few tokens (moe_fp4_forward_few): a
     layer, its argument record and a workspace for up to max_tokens tokens
@@ -431,14 +463,15 @@ class FewTokenLayer:
     captured graphs that may replay at once, need a FewTokenLayer each, which
     has to live as long as the graphs.  The layer's tensors are those at
     construction, kept here: what is set in the layer afterwards does not
-    matter."""
+    matter.  A layer whose tensors are not all contiguous, of its sizes and on
+    one GPU is refused by every call."""
 
     def __init__(self, layer: MoELayer, max_tokens: int, out_dtype: torch.dtype = torch.float32):
         if out_dtype not in (torch.float32, torch.bfloat16):
             raise TypeError(f"unsupported dtype {out_dtype}")
         layer = dataclasses.replace(layer)  # the struct's pointers are those of tensors that live as long as it
         self.layer, self.max_tokens, self.out_dtype = layer, max_tokens, out_dtype
-        self.device = layer.w13.device
+        self.device, self._fault = layer.w13.device, _layer_fault(layer)
         self._experts, self._top_k, self._hidden = layer.num_experts, layer.top_k, layer.hidden
         self._out_code = DT_F32 if out_dtype == torch.float32 else DT_BF16
         self._struct = layer.struct()
@@ -457,6 +490,8 @@ class FewTokenLayer:
                  y: Optional[torch.Tensor] = None, topk_ids: Optional[torch.Tensor] = None,
                  topk_weights: Optional[torch.Tensor] = None):
         dev, T, E, k, H = self.device, x.shape[0], self._experts, self._top_k, self._hidden
+        if self._fault:
+            raise ValueError(self._fault)
         if T > self.max_tokens:
             raise ValueError(f"{T} tokens, at most {self.max_tokens}")
         if y is None:
