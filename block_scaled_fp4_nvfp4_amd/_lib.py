@@ -479,6 +479,7 @@ class FewTokenLayer:
         need = ctypes.c_size_t()
         _check(lib().moe_fp4_few_workspace_size(self._layer_ref, max_tokens, ctypes.byref(need)))
         self.workspace = torch.empty(max(need.value, 1), dtype=torch.uint8, device=self.device)
+        self._home = _raw_stream(self.device.index) if self.device.type == "cuda" else None
 
     def _arg(self, name, t, dtype, rows, cols):
         if t.dtype != dtype or t.shape != (rows, cols) or t.device != self.device or not t.is_contiguous():
@@ -502,13 +503,16 @@ class FewTokenLayer:
             topk_weights = torch.empty((T, k), dtype=torch.float32, device=dev)
         if bias is not None and bias.shape != (E,):
             raise ValueError(f"bias: ({E},) expected, got {tuple(bias.shape)}")
+        stream = _raw_stream(dev.index)
+        if stream != self._home:  # once given up, the workspace waits for this stream before its memory is used again
+            self.workspace.record_stream(torch.cuda.current_stream(dev))
         _check(_on_device(dev.index, lib().moe_fp4_forward_few, self._layer_ref, self._arg("x", x, torch.bfloat16, T, H), T,
                           self._arg("logits", logits, torch.float32, T, E),
                           None if bias is None else self._arg("bias", bias[None], torch.float32, 1, E),
                           self._arg("y", y, self.out_dtype, T, H), self._out_code,
                           self._arg("topk_ids", topk_ids, torch.int32, T, k),
                           self._arg("topk_weights", topk_weights, torch.float32, T, k),
-                          self.workspace.data_ptr(), self.workspace.numel(), _raw_stream(dev.index)))
+                          self.workspace.data_ptr(), self.workspace.numel(), stream))
         return y, topk_ids, topk_weights
 
 
