@@ -202,7 +202,6 @@ __global__ void __launch_bounds__(64 * NW) fp8_skinny_kernel(MatmulArgs a) {
       dma_buffer(buf, (uint32_t)min(row, last) * (uint32_t)a.K + 16 * ((lane & 7) ^ (row >> 1)), 128 * (wave + NW * u), ring + 2048 * slot + 1024 * j);
     }
   };
-  const int items = mine * nu;
   int li = 0, lu = 0;  // the next item to load
   auto load_next = [&](int slot) __attribute__((always_inline)) {
     // past the end the last item is loaded again, so that every step issues two instructions
@@ -244,6 +243,8 @@ __global__ void __launch_bounds__(64 * NW) fp8_skinny_kernel(MatmulArgs a) {
         asm volatile("" ::: "memory");
         const uint8_t* w = ring + 2048 * slot;
         add_scaled(acc, block_product<F32SUM>(frag_of(ld16(w + frag0), ld16(w + (frag0 ^ 64))), xf[u]), sx[u], sw);
+        // pinned here: the next item's loads overwrite a slot only after its values have reached an MFMA
+        asm volatile("" ::"v"(acc));
         slot = slot == D - 1 ? 0 : slot + 1;
       }
     }

@@ -644,7 +644,8 @@ __device__ __forceinline__ void gu_stream(int rounds, int mine, int lo, int hi, 
       if (FMT == FP4_FMT_FP8_BLOCK) factors(j, fg, fu);
       for (int b = lo; b < hi; ++b) {
         const bool more = lj < mine;
-        if (more) load_next(slot ^ 1);  // read a piece ago: its values are in registers
+        __builtin_amdgcn_s_waitcnt(lgkmcnt0());  // the other slot's values are in registers
+        if (more) load_next(slot ^ 1);
         if (!more || (SR > 0 && !by4)) __builtin_amdgcn_s_waitcnt(0);
         else if (by16) __builtin_amdgcn_s_waitcnt(vmcnt_only(ND16));
         else __builtin_amdgcn_s_waitcnt(vmcnt_only(ND));
