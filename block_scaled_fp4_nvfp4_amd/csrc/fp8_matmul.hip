@@ -539,12 +539,15 @@ __global__ void __launch_bounds__(64 * WM * WN * GROUPS, GROUPS > 2 ? GROUPS : 2
   }
 }
 
+constexpr int64_t kMaxThreads = 0xFFFFFFFF;  // of a launch along x
+constexpr int64_t kMaxBatch = 65535;         // workgroups along z
+
 template <int WM, int WN, int MS, int NS, int RING, int GROUPS, typename OutT>
 static int launch_tile(const MatmulArgs& a, int64_t batch, hipStream_t st) {
   using C = TileCfg<WM, WN, MS, NS, RING, GROUPS>;
   const int64_t mt = (a.M + C::BM - 1) / C::BM, nt = (a.N + C::BN - 1) / C::BN;
   const int64_t grid = (mt * nt + 7) / 8 * 8;
-  if (grid > INT32_MAX / 8 || batch > 65535) return fail(FP4_ERR_UNSUPPORTED, "matmul: too many rows, outputs or matrices");
+  if (grid * (64 * C::WAVES * GROUPS) > kMaxThreads) return fail(FP4_ERR_UNSUPPORTED, "matmul: too many rows or outputs");
   hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, MS, NS, RING, GROUPS, OutT>), dim3((unsigned)grid, 1, (unsigned)batch), dim3(64 * C::WAVES * GROUPS), 0, st,
                      a, (int)mt, (int)nt);
   return check_launch("fp8_block_matmul");
@@ -553,7 +556,6 @@ static int launch_tile(const MatmulArgs& a, int64_t batch, hipStream_t st) {
 template <int U, int NW, int D, int XK, int P, typename OutT>
 static int launch_skinny(const MatmulArgs& a, int64_t batch, hipStream_t st) {
   const int64_t strips = (a.N + 15) / 16, wgs = std::max<int64_t>(1, 2 * device_cu_count() / batch);
-  if (batch > 65535) return fail(FP4_ERR_UNSUPPORTED, "matmul: too many matrices");
   hipLaunchKernelGGL((fp8_skinny_kernel<U, NW, D, XK, P, OutT>), dim3((unsigned)std::min(strips, wgs), 1, (unsigned)batch), dim3(64 * NW), 0, st, a);
   return check_launch("fp8_block_matmul");
 }
@@ -669,6 +671,7 @@ int fp8_block_matmul(const void* x, int x_dtype, const float* x_scales, const ui
   if ((uintptr_t)x % 16 || (uintptr_t)w % 16 || (uintptr_t)y % (y_dtype == FP4_DT_BF16 ? 2 : 4) ||
       (uintptr_t)x_scales % 4 || (uintptr_t)w_scales % 4)
     return fail(FP4_ERR_INVALID_ARG, "matmul: misaligned pointer");
+  if (batch > kMaxBatch) return fail(FP4_ERR_UNSUPPORTED, "matmul: more than %lld matrices", (long long)kMaxBatch);
   hipStream_t st = as_stream(stream);
   MatmulArgs a{static_cast<const uint8_t*>(x), x_scales, w, w_scales, y, m, n, (int)k};
   int xk = X_CODES;
@@ -681,7 +684,7 @@ int fp8_block_matmul(const void* x, int x_dtype, const float* x_scales, const ui
     uint8_t* codes = static_cast<uint8_t*>(workspace);
     float* scales = reinterpret_cast<float*>(codes + codes_bytes(batch, m, k));
     const int64_t blocks = batch * m * (k / 128), wgs = (blocks * 8 + 255) / 256;
-    if (wgs > INT32_MAX) return fail(FP4_ERR_UNSUPPORTED, "matmul: too many rows");
+    if (wgs * 256 > kMaxThreads) return fail(FP4_ERR_UNSUPPORTED, "matmul: too many rows");
     if (x_dtype == FP4_DT_BF16)
       hipLaunchKernelGGL(fp8_rows_kernel<X_BF16>, dim3((unsigned)wgs), dim3(256), 0, st, static_cast<const uint8_t*>(x), blocks, codes, scales);
     else
