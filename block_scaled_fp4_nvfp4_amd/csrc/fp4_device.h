@@ -208,13 +208,11 @@ __device__ __forceinline__ uint32_t e4m3_exact_quotient(float a, float sigma) {
   return e4m3_is_midpoint(q) ? e4m3_fix_midpoint(c, q, a, sigma) : c;
 }
 
-// Makes the FP8 conversions of this wave saturate at 448 (as the mode register
-// starts they turn 464 and more into NaN; a NaN stays one either way), the
-// overflow of fp16 ones at 65504 with them.  For kernels that call e4m3_codes, at
-// their start: a limit on every quotient instead cost 0.4 to 0.9 of 11.5 us at
-// 16 x 10240 x 2560.
-__device__ __forceinline__ void saturate_fp8() {
-  __builtin_amdgcn_s_setreg(1 | 23 << 6, 1);  // the mode register's FP16_OVFL bit
+// Makes the wave's FP8 conversions saturate at 448 (on) or turn 464 and more into
+// NaN (off, as a kernel starts); a NaN stays one either way.
+__device__ __forceinline__ void saturate_fp8(bool on) {
+  if (on) __builtin_amdgcn_s_setreg(1 | 23 << 6, 1);  // the mode register's FP16_OVFL bit
+  else __builtin_amdgcn_s_setreg(1 | 23 << 6, 0);
 }
 
 // N values (a multiple of 2) to E4M3 codes of v / sigma in d, bit for bit
@@ -224,12 +222,17 @@ __device__ __forceinline__ void saturate_fp8() {
 // does: ties, which bf16 values hit all the time, need no branch.  Both are
 // scaled by the power of two that brings sigma into [0.5, 1), so that the
 // remainder of every quotient above E4M3's smallest midpoint is exact.  A
-// sigma of a few units of 2^-149 lies up to a third below amax / 448: quotients
-// above 448 rely on saturate_fp8.
+// sigma of a few units of 2^-149 lies up to a third below amax / 448, so quotients
+// may pass 464: the conversions saturate (a limit on every quotient instead cost
+// 0.4 to 0.9 of 11.5 us at 16 x 10240 x 2560).  Only they do: an E4M3 MFMA run in
+// that mode loses the NaN of its operands.
 template <int N>
 __device__ __forceinline__ void e4m3_codes(const float (&v)[N], float sigma, uint32_t (&d)[(N + 3) / 4]) {
   const int e = -__builtin_amdgcn_frexp_expf(sigma);
-  const float s = ldexpf(sigma, e), inv = sigma > 0.0f ? 1.0f / s : 0.0f;
+  const float s = ldexpf(sigma, e);
+  float inv = sigma > 0.0f ? 1.0f / s : 0.0f;
+  saturate_fp8(true);
+  asm volatile("" : "+v"(inv));  // the conversions take it from here: after the switch
 #pragma unroll
   for (int w = 0; w < (N + 3) / 4; ++w) d[w] = 0;
 #pragma unroll
@@ -244,6 +247,9 @@ __device__ __forceinline__ void e4m3_codes(const float (&v)[N], float sigma, uin
     d[w >> 1] = (uint32_t)((w & 1) ? __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], (int)d[w >> 1], true)
                                    : __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], (int)d[w >> 1], false));
   }
+#pragma unroll
+  for (int w = 0; w < (N + 3) / 4; ++w) asm volatile("" : "+v"(d[w]));  // all converted: before the switch back
+  saturate_fp8(false);
 }
 
 }  // namespace fp4

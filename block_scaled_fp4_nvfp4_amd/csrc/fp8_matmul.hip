@@ -119,7 +119,6 @@ template <int XK>
 __global__ void __launch_bounds__(256) fp8_rows_kernel(const uint8_t* __restrict__ x, int64_t blocks, uint8_t* __restrict__ codes,
                                                        float* __restrict__ scales) {
   constexpr int XB = XK == X_BF16 ? 2 : 4;
-  saturate_fp8();
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if ((t >> 3) >= blocks) return;  // whole groups of 8 lanes
   float v[16];
@@ -184,7 +183,6 @@ __global__ void __launch_bounds__(64 * NW) fp8_skinny_kernel(MatmulArgs a) {
   constexpr int STAGED = XK == X_CODES ? 0 : 2048;  // a wave's staging of quantized x
   __shared__ __attribute__((aligned(16))) uint8_t lds[NW * (D * 2048 + STAGED) + 2 * NW * 1024];
   float* part = reinterpret_cast<float*>(lds + NW * (D * 2048 + STAGED));  // [2][NW][16 rows][16 outputs]
-  if constexpr (XK != X_CODES) saturate_fp8();
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, r = lane & 15;
   const int64_t b = blockIdx.z;
   const int KB = a.K >> 7, strips = (int)((a.N + 15) >> 4), first = blockIdx.x, step = gridDim.x;

@@ -697,7 +697,6 @@ __global__ void __launch_bounds__(64 * kGuWaves, 2) few_gateup_kernel(FewArgs a)
   __shared__ uint32_t s_amax;
   __shared__ int s_np;
   __shared__ unsigned long long touched[16];
-  if constexpr (AF == FP4_FMT_FP8_ROW) saturate_fp8();
   const int tid = threadIdx.x, th = blockDim.x, nw = th >> 6, lane = tid & 63, g = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int T = a.T, k = a.k, H = a.H, P = T * k, split = a.k_split, ks = wave % split, per = nw / split;
@@ -1193,7 +1192,6 @@ __device__ __forceinline__ void dn_run(const uint8_t* w, const uint8_t* ws, cons
 template <int MODE>
 __global__ void __launch_bounds__(64 * kDnWaves, 2) few_down_kernel(FewArgs a) {
   constexpr int WF = weight_fmt(MODE), AF = act_fmt(MODE), NT = dn_terms(MODE);
-  if constexpr (AF == FP4_FMT_FP8_ROW) saturate_fp8();
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int nw = blockDim.x >> 6, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int T = a.T, H = a.H, S = a.S, P = T * a.k, strips = H / 16;

@@ -51,3 +51,16 @@ def test_other_matrices_do_not_matter(m):
         w2[key][1] = w[key][1]
     w2["scales"][0] = float("inf")
     assert torch.equal(y[1], _m().fp8_matmul(x2, w2)[1])
+
+
+@pytest.mark.parametrize("m", [1, 4, 16, 17, 300])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_what_is_not_finite_shows_in_its_row(m, bad):
+    """Outside of what the operator asks of x, but never a finite result: the block's codes are NaN."""
+    print_case(f"matmul not finite m={m} {bad}")
+    for dtype in (torch.bfloat16, torch.float32):
+        x, w = _case(m, 1, m, 100, 384, dtype)
+        y = _m().fp8_matmul(x, w)
+        x[0, m - 1, 200] = bad
+        y2 = _m().fp8_matmul(x, w)
+        assert bool(torch.isnan(y2[0, m - 1]).all()) and torch.equal(y[:, :m - 1], y2[:, :m - 1])
