@@ -291,7 +291,9 @@ def fp8_matmul(x, w: dict, out_dtype: torch.dtype = torch.bfloat16, out: Optiona
     w: a record of quantize(w, "fp8_block"): codes [N, K] or [B, N, K], scales
     [ceil(N/128), K/128] (or [B, ...]); N need not be a multiple of 128.  A
     leading B = 1 of w may be left out or given either way.
-    Returns y [M, N] or [B, M, N] in out_dtype (bf16 or f32), in `out` if given.
+    Returns y [M, N] or [B, M, N] in out_dtype (bf16 or f32), in `out` if given
+    (not x's or w's memory).  f32 sums throughout with f32 results; with bf16
+    ones a 128-block's sum is the E4M3 MFMA's (see fp8_block_matmul).
     workspace: a uint8 device tensor of fp8_matmul_workspace_size bytes for
     bf16 / f32 x; allocated here when not given."""
     if isinstance(x, dict):
@@ -457,7 +459,9 @@ class FewTokenLayer:
     Calling it with x bf16 [T, H], router logits f32 [T, E] and an optional
     bias f32 [E] returns (y [T, H] in out_dtype, topk_ids int32 [T, k],
     topk_weights f32 [T, k]), in the given tensors where they are given.
-    Masked experts have logit -inf; slots left over get id -1, weight 0.
+    Masked experts have logit -inf; slots left over get id -1, weight 0.  Plain
+    activations from 8 tokens on (or with few weights) and MXFP8 ones at 16 are
+    faster through route and moe_forward.
 
     The workspace serves one call at a time: calls on several streams, or
     captured graphs that may replay at once, need a FewTokenLayer each, which

@@ -19,21 +19,30 @@
 // expert's tokens.
 //
 // Measured at 512 experts, hidden 2560, intermediate 640, top 10, in graph
-// replays (us; in brackets the same layer through the router and the sorted
-// forward): NVFP4 weights 1 token 27 [33], 4 tokens 45 [46], 16 tokens 110
-// [95]; MXFP4/MXFP8 1 token 26 [39], 4 tokens 42 [53], 16 tokens 100 [99];
-// NVFP4/NVFP4 with a shared expert of 1280, top 5, 16 tokens 86 [129]; block
-// FP8 with that shared expert, 7 tokens 93 [129].  Of the 27 us at one token
-// routing takes 4.5, the list of experts 1.3, gate_up 9, each gap between
-// kernels 1.5, the down products 7, the sum 2; of the 110 us at 16 tokens
-// routing and x~ 12, gate_up 56 (4.6 TB/s), the down products 34 (3.8 TB/s).
+// replays over 16 sets of logits (us; in brackets the same layer through the
+// router and the sorted forward): 1, 4, 8 and 16 tokens with NVFP4 weights 28
+// [33], 45 [46], 72 [64], 112 [95]; MXFP4 26 [33], 42 [46], 63 [62], 100 [91];
+// NVFP4/NVFP4 34 [72], 53 [86], 78 [115], 122 [190]; MXFP4/MXFP8 25 [38], 43
+// [53], 64 [70], 101 [100]; block FP8 31 [58], 58 [83], 93 [114], 151 [175]; with a
+// shared expert of 1280: NVFP4/NVFP4, top 5, 16 tokens 85 [130], block FP8, 7
+// tokens 92 [128].  NVFP4 with little to read: 8 experts of 256 x 128, one token 16
+// [14]; 64 experts, top 4, 16 tokens 53 [44].  So the other way is faster with plain
+// activations from 8 tokens on or few weights, and at 16 with MXFP8: every
+// workgroup routes every token here, and plain h costs two or three columns a
+// pair.  Of the time at one token of NVFP4 routing takes 4.5, the
+// list of experts 1.3, gate_up 9, each gap between kernels 1.5, the down products
+// 7, the sum 2; at 16 tokens routing and x~ 12, gate_up 56 (4.6 TB/s), the down
+// products 34 (3.8 TB/s).
 //
 // Exactness.  Weights and x~ are exact where they meet: in fp16 for NVFP4
 // weights (E2M1 codes times E4M3 scales, 6 significant bits) with x~ of NVFP4
 // or a plain x scaled to fp16's range, in bf16 for MXFP4 (E2M1 codes times
 // powers of two) and block FP8 (E4M3 codes alone; their scales multiply the f32
 // sum of each 128-block).  An h held in f32 (not quantized, or FP8 codes times
-// their scales) is split into terms whose sum is h.  Sums are f32.
+// their scales) is split into terms: in bf16 three, whose sum is h down to bf16's
+// smallest step, 2^-133 (all of an h of 2^-110 and more), for NVFP4 weights two in
+// fp16 (dn_terms).  Sums are f32; scales whose product may leave f32 are applied one
+// power of two at the end (scale_by, add_scaled).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -480,8 +489,8 @@ __device__ __forceinline__ float wave_amax(float m) {
 // xs[t] gets the factor of a token's products, xf those of its K steps (FP8
 // rows).  Plain x meets NVFP4 weights as fp16 scaled by the power of two that
 // brings the token's largest value to [2^14, 2^15): exact down to 2^-29 of
-// that value, and 2^-40 of it off below, far inside the f32 sums' own
-// rounding.
+// that value, and 2^-39 of it off below: inside the f32 sums' own rounding,
+// unless the weights of that largest value are zeros.
 template <int WF, int AF>
 __device__ __forceinline__ void prepare_x(const FewArgs& a, uint8_t* sx, float* xf, float* xs, float* tmp) {
   const int H = a.H, kp = (H + 127) / 128 * 128, T = a.T, nw = (int)blockDim.x >> 6;
@@ -1362,7 +1371,8 @@ static int launch_few(FewArgs a, const FewPlan& p, int y_dtype, hipStream_t st) 
   const int lds = gu_smem(a.T, a.E, a.k, a.H, MODE == FM_FP8, p.nw, ring, a.k_split > 1).total;
   const int per = p.nw / a.k_split, fit = kFewCus * std::max(1, std::min(2, kLds / (lds + 64)));
   int shared = 0;  // workgroups of the shared expert, by 1.5 times its share of the bytes: its waves stage all tokens' h
-             // for each K step (shares of 1 / 1.5 / 2: 16 tokens of NVFP4/NVFP4 87.9 / 85.8 / 87.3 us, 7 of block FP8 98 / 93 / 94)
+             // for each K step (shares of 1 / 1.5 / 2 in the header's graph replays: 16 tokens of NVFP4/NVFP4
+             // 87.9 / 85.8 / 87.3 us, 7 of block FP8 98 / 93 / 94)
   double share = 0;
   if (a.S > 0) {
     const double sb = 1.5 * 2.0 * a.S, rb = (double)std::min(a.E, a.T * a.k) * 2 * a.I * (MODE == FM_FP8 ? 1.0 : 0.55);

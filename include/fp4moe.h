@@ -370,11 +370,15 @@ int moe_fp4_forward_noalloc(const moe_fp4_layer* layer, const uint16_t* x, int64
  * moe_fp4_forward_few - the whole layer for a few tokens (1 to 16), from the
  * router's logits to y: moe_fp4_route and moe_fp4_forward in three launches,
  * for every format pair and the shared expert; the decode step of one or a few
- * sequences.  It is the faster way up to about 4 tokens with plain activations
- * and up to 16 with quantized ones (512 experts of hidden 2560, intermediate
- * 640, top 10, graph replays against moe_fp4_route + moe_fp4_forward: NVFP4
- * weights 1 token 27 against 33 us, 16 tokens 110 against 95; NVFP4/NVFP4 with
- * a shared expert, top 5, 16 tokens 86 against 129).
+ * sequences.  Which way is faster depends on the layer (512 experts of hidden
+ * 2560, intermediate 640, top 10, us in graph replays against moe_fp4_route +
+ * moe_fp4_forward): with plain activations this one up to about 4 tokens (NVFP4
+ * weights 1 token 28 against 33, 4 tokens 45 against 46, 8 tokens 72 against 64,
+ * 16 tokens 112 against 95), with MXFP8 ones up to about 8 (16 tokens 101 against
+ * 100), with NVFP4 and block-FP8 ones up to 16 (122 against 190, 151 against 175);
+ * with plain activations and little to read the other one (8 experts of 256 x 128,
+ * 1 token: 16 against 14; 64 experts, top 4, 16 tokens: 53 against 44).  The call
+ * never takes the other way by itself.
  *  x            bf16 [tokens, H], finite.
  *  logits, bias f32 [tokens, E] and [E] (bias may be NULL), selected from as by
  *               moe_fp4_route.  An expert whose logit + bias is -inf (or NaN)
@@ -390,12 +394,17 @@ int moe_fp4_forward_noalloc(const moe_fp4_layer* layer, const uint16_t* x, int64
  * included: S_x over all of x, masked tokens among it, and S_h over the
  * selected pairs' h.  The layer's tiled weight copies are not read.  Results
  * repeat bit for bit.
+ * Operands are exact and sums are f32, except: plain activations meet NVFP4
+ * weights in fp16 scaled by a power of two, x 2^-39 of its token's largest value
+ * off at most, h 2^-22 of itself and 2^-39 of its pair's largest value; MXFP4's
+ * plain h and block FP8's h lose what lies below 2^-133.
  * Errors: as moe_fp4_forward for the layer; more than 16 tokens or 1024
  * experts, a width above 65536, tokens whose x (2 bytes a value, with the
  * routing's tables) exceeds the LDS (16 tokens: hidden up to about 4000), an
  * inter whose h exceeds it (26000 or more, where it is not quantized), or gate_up
  * codes of an expert above 2 GiB -> FP4_ERR_UNSUPPORTED; misaligned pointer (x,
- * codes, gate: 16 bytes; NVFP4 scales: 2) -> FP4_ERR_INVALID_ARG.
+ * codes, gate: 16 bytes; NVFP4 scales: 2; block-FP8 scales: 4) ->
+ * FP4_ERR_INVALID_ARG.
  * tokens == 0 is a no-op.  Stream-ordered, asynchronous.
  */
 int moe_fp4_few_workspace_size(const moe_fp4_layer* layer, int64_t tokens, size_t* bytes);
@@ -417,17 +426,22 @@ int moe_fp4_forward_few(const moe_fp4_layer* layer, const uint16_t* x, int64_t t
  *               k/128], as fp4_quantize writes FP4_FMT_FP8_BLOCK.  n need not be
  *               a multiple of 128: the last scale row covers the rows left.
  *  y            [batch, m, n] bf16 or f32 (`y_dtype`), rounded once from f32 sums
- *               of the blocks.  bf16: the sum inside a 128-block is the E4M3
- *               MFMA's (about 1.6e-5 relative, far below bf16's rounding);
- *               f32: the codes go through the fp16 MFMA, exactly, with f32 sums.
+ *               of the blocks; no input's memory.  bf16: the sum inside a
+ *               128-block is the E4M3 MFMA's, off by less than 7 2^-14 of the sum
+ *               of the products' magnitudes (1.7e-5 of it on normal data), which
+ *               bf16's rounding covers unless the products cancel.  f32: the
+ *               codes go through the fp16 MFMA, exactly, with f32 sums; where
+ *               products cancel, ask for f32.
  *  workspace    fp8_block_matmul_workspace_size bytes of device memory, 16-byte
  *               aligned; NULL where that is 0 (E4M3 x, or m <= 16 with k <= 8192).
  *               Calls in flight at once, captured graphs among them, need one each.
  * Any m >= 0 and n >= 0; every buffer is contiguous.  The result does not
- * depend on other rows of x or on earlier calls, and repeats bit for bit.
+ * depend on other rows of x, other matrices of the batch or earlier calls, and
+ * repeats bit for bit.
  * Errors: k % 128, k == 0 -> FP4_ERR_SHAPE; unknown dtype, null or misaligned
- * pointer (x, w: 16 bytes) -> FP4_ERR_INVALID_ARG; a dimension beyond the grid's
- * or 2^31 -> FP4_ERR_UNSUPPORTED; FP4_ERR_WORKSPACE.  Stream-ordered, asynchronous.
+ * pointer (x, w: 16 bytes) -> FP4_ERR_INVALID_ARG; more than 65535 matrices, more
+ * rows or outputs than a launch has threads for, a dimension of 2^31, k above 2^22
+ * -> FP4_ERR_UNSUPPORTED; FP4_ERR_WORKSPACE.  Stream-ordered, asynchronous.
  */
 int fp8_block_matmul_workspace_size(int x_dtype, int64_t batch, int64_t m, int64_t n, int64_t k, size_t* bytes);
 int fp8_block_matmul(const void* x, int x_dtype, const float* x_scales, const uint8_t* w, const float* w_scales,
