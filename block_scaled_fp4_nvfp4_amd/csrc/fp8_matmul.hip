@@ -304,32 +304,52 @@ struct TileCfg {
 
 // One wave's 16 MS rows and 16 NS outputs from row m0 and output n0 on where
 // scales are so far from 1 that their products may leave f32's normal range:
-// from memory, one 16 x 16 tile after another, K's runs of `per_group` steps
-// each summed up by itself, as the tile kernel's groups do.  It starts over, so
-// that the tile kernel's registers need not hold both forms of a step.
+// from memory, 16 rows at a time, K's runs of `per_group` steps each summed up by
+// itself, as the tile kernel's groups do.  It starts over, so that the tile
+// kernel's registers need not hold both forms of a step (8192 x 2560 x 2560: 71 us,
+// 212 with one such row and one such tile of W, 608 where all of them are).
 template <int GROUPS, int MS, int NS, typename OutT>
 __device__ __forceinline__ void far_tile(const MatmulArgs& a, int64_t b, int64_t m0, int64_t n0, int per_group) {
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15, KB = a.K >> 7;
   const float* ws = a.ws + b * ((a.N + 127) >> 7) * KB;
+  // rows past the end of an operand repeat its last one; their results are not stored
+  const uint8_t* w[NS];
+  const float* sw[NS];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    const int64_t n = n0 + 16 * s;
+    w[s] = a.w + (b * a.N + min(n + r, a.N - 1)) * a.K + 16 * g;
+    sw[s] = ws + (min(n, a.N - 1) >> 7) * KB;
+  }
 #pragma unroll 1
-  for (int i = 0; i < MS * NS; ++i) {
-    const int64_t m = m0 + 16 * (i / NS) + r, n = n0 + 16 * (i % NS);
-    // rows past the end of an operand repeat its last one; their results are not stored
-    const int64_t xm = b * a.M + min(m, a.M - 1), wn = min(n + r, a.N - 1), wt = min(n, a.N - 1) >> 7;
-    const uint8_t *x = a.x + xm * a.K + 16 * g, *w = a.w + (b * a.N + wn) * a.K + 16 * g;
-    block_sums sum{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < MS; ++i) {
+    const int64_t m = m0 + 16 * i + r, xm = b * a.M + min(m, a.M - 1);
+    if (m0 + 16 * i >= a.M) break;
+    const uint8_t* x = a.x + xm * a.K + 16 * g;
+    const float* sx = a.xs + xm * KB;
+    block_sums sum[NS];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) sum[s] = block_sums{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     for (int h = 0; h < GROUPS; ++h) {
-      block_sums acc{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-      for (int kb = h * per_group; kb < min(KB, (h + 1) * per_group); ++kb)
-        add_far_scaled(acc, block_product<sizeof(OutT) == 4>(frag_of(ld16(w + 128 * kb), ld16(w + 128 * kb + 64)), frag_of(ld16(x + 128 * kb), ld16(x + 128 * kb + 64))),
-                       a.xs[xm * KB + kb], ws[wt * KB + kb]);
-      sum += acc;
+      block_sums acc[NS];
+#pragma unroll
+      for (int s = 0; s < NS; ++s) acc[s] = block_sums{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+      for (int kb = h * per_group; kb < min(KB, (h + 1) * per_group); ++kb) {
+        const intx8 xf = frag_of(ld16(x + 128 * kb), ld16(x + 128 * kb + 64));
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+          add_far_scaled(acc[s], block_product<sizeof(OutT) == 4>(frag_of(ld16(w[s] + 128 * kb), ld16(w[s] + 128 * kb + 64)), xf), sx[kb], sw[s][kb]);
+      }
+#pragma unroll
+      for (int s = 0; s < NS; ++s) sum[s] += acc[s];
     }
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (m < a.M && n + 4 * g + c < a.N) static_cast<OutT*>(a.y)[(b * a.M + m) * a.N + n + 4 * g + c] = out_of<OutT>(sum[c]);
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (const int64_t n = n0 + 16 * s + 4 * g + c; m < a.M && n < a.N) static_cast<OutT*>(a.y)[(b * a.M + m) * a.N + n] = out_of<OutT>(sum[s][c]);
   }
 }
 
@@ -379,7 +399,7 @@ __global__ void __launch_bounds__(64 * WM * WN * GROUPS, GROUPS > 2 ? GROUPS : 2
   };
   float* xtab = reinterpret_cast<float*>(lds + C::XTAB);
   float* wtab = reinterpret_cast<float*>(lds + C::WTAB);
-  int* fartab = reinterpret_cast<int*>(tile_lds + C::FARTAB);  // whether a wave put far scales into the tables
+  int* fartab = reinterpret_cast<int*>(tile_lds + C::FARTAB);  // which bounds a wave's scales in the tables leave
   // Scales of the K steps [kb0, kb0 + kTileTab): every thread's loads are
   // issued together, consecutive threads along a row's K steps.
   auto fill_tables = [&](int kb0) __attribute__((always_inline)) {
@@ -397,13 +417,15 @@ __global__ void __launch_bounds__(64 * WM * WN * GROUPS, GROUPS > 2 ? GROUPS : 2
       const uint32_t i = min(tid + (uint32_t)TH * j, C::BN / 16 * n - 1), s = (i * inv) >> 20, q = i - s * n;
       wv[j] = ws[min((n0 + 16 * s) >> 7, NB - 1) * KB + kb0 + q];
     }
-    bool out = false;
+    // no product leaves f32's normal range where x's scales lie in [2^-100, 2^120] and W's in [2^-24, 2^7] (as weights
+    // have them, so that a padding row of anything does not matter), nor where both lie in [2^-62, 2^62]
+    ScaleRange xr, wr;
 #pragma unroll
-    for (int j = 0; j < XI; ++j) out |= far_scale(xv[j]);
+    for (int j = 0; j < XI; ++j) xr.add(xv[j]);
 #pragma unroll
-    for (int j = 0; j < WI; ++j) out |= far_scale(wv[j]);
-    const bool any = __any(out);
-    if (lane == 0) fartab[group * C::WAVES + wave] = any;
+    for (int j = 0; j < WI; ++j) wr.add(wv[j]);
+    const int seen = (__any(xr.outside(-100, 120) || wr.outside(-24, 7)) ? 1 : 0) | (__any(xr.outside(-62, 62) || wr.outside(-62, 62)) ? 2 : 0);
+    if (lane == 0) fartab[group * C::WAVES + wave] = seen;
 #pragma unroll
     for (int j = 0; j < XI; ++j) {  // threads past the end repeat the last entry
       const uint32_t i = min(tid + (uint32_t)TH * j, C::BM * n - 1), m = (i * inv) >> 20, q = i - m * n;
@@ -438,7 +460,7 @@ __global__ void __launch_bounds__(64 * WM * WN * GROUPS, GROUPS > 2 ? GROUPS : 2
       int any = 0;
 #pragma unroll
       for (int w = 0; w < GROUPS * C::WAVES; ++w) any |= fartab[w];
-      far = __builtin_amdgcn_readfirstlane(any) != 0;
+      far = __builtin_amdgcn_readfirstlane(any) == 3;
       if (far) return;
     }
     if (GROUPS > 1 && kb >= last) return;  // the last groups may have fewer steps; every barrier is met

@@ -102,11 +102,18 @@ __device__ __forceinline__ void add_scaled(block_sums& acc, const block_sums& p,
 __device__ __forceinline__ float scale_by(float v, float a, float b) {
   return ldexpf(v * (__builtin_amdgcn_frexp_mantf(a) * __builtin_amdgcn_frexp_mantf(b)), __builtin_amdgcn_frexp_expf(a) + __builtin_amdgcn_frexp_expf(b));
 }
-// Whether a scale lies outside [2^-62, 2^62]: no product of two that do not (and are not 0) leaves the normal range.
-__device__ __forceinline__ bool far_scale(float s) {
-  const uint32_t u = __float_as_uint(s) & 0x7FFFFFFFu;
-  return u != 0 && u - ((127u - 62u) << 23) > (124u << 23);
-}
+// The range of scales, as bits: the least that is not 0 (less one) and the largest.
+// Negative and not finite ones count as very large.
+struct ScaleRange {
+  uint32_t least = 0xFFFFFFFFu, most = 0;
+  __device__ __forceinline__ void add(float s) {
+    least = min(least, __float_as_uint(s) - 1);
+    most = max(most, __float_as_uint(s));
+  }
+  __device__ __forceinline__ bool outside(int lo, int hi) const {  // of [2^lo, 2^hi]
+    return least < ((uint32_t)(127 + lo) << 23) - 1 || most > (uint32_t)(127 + hi) << 23;
+  }
+};
 
 // A float that no lane varies and no kernel of the launch writes, by a scalar
 // load: a vector load would be waited for with all the DMA issued before it.

@@ -81,3 +81,28 @@ def test_one_block_beyond_f32(m, n, k, at, out):
     near = [i for i in range(m) if i not in (1, m - 1)]
     if n > 128:
         assert torch.equal(y[0, near, 128:], ref[0, near, 128:])
+
+
+@pytest.mark.parametrize("m,n,k", [(40, 200, 128 * 26), (512, 2560, 384), (2100, 3001, 256), (4101, 8200, 256)])
+@pytest.mark.parametrize("sx,sw", [(2.0 ** -99, 2.0 ** -23), (2.0 ** -101, 2.0 ** -25), (2.0 ** -98, 2.0 ** -30), (2.0 ** -61, 2.0 ** -62),
+                                   (2.0 ** -64, 2.0 ** -64), (2.0 ** 119, 2.0 ** 6), (2.0 ** 120, 2.0 ** 8), (2.0 ** 61, 2.0 ** 61)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_scales_about_the_bounds_of_the_tables(m, n, k, sx, sw, out):
+    """On either side of what the tile kernel takes in its ordinary form: [2^-100, 2^120] with [2^-24, 2^7],
+    [2^-62, 2^62] with itself."""
+    test_products_beyond_f32(1, m, n, k, sx, sw, out)
+
+
+@pytest.mark.parametrize("m", [20, 300, 2100])
+def test_padding_rows_of_anything(m):
+    """Rows behind the last one in use that hold any bits: the others as without them."""
+    print_case(f"matmul padding m={m}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m)
+    n, k = 2560, 512
+    x = torch.randn(1, m, k, device="cuda", generator=g).to(torch.bfloat16)
+    w = _weight(g, 1, n, k)
+    x[:, m // 2:] = 0
+    ref = _m().fp8_matmul(x, w)
+    x[:, m // 2:] = torch.randint(-32768, 32768, (1, m - m // 2, k), device="cuda", generator=g, dtype=torch.int16).view(torch.bfloat16)
+    assert torch.equal(_m().fp8_matmul(x, w)[:, :m // 2], ref[:, :m // 2])
