@@ -460,8 +460,8 @@ class FewTokenLayer:
     bias f32 [E] returns (y [T, H] in out_dtype, topk_ids int32 [T, k],
     topk_weights f32 [T, k]), in the given tensors where they are given.
     Masked experts have logit -inf; slots left over get id -1, weight 0.  Plain
-    activations from 8 tokens on (or with few weights) and MXFP8 ones at 16 are
-    faster through route and moe_forward.
+    activations above about 8 tokens (or with few weights) are faster through
+    route and moe_forward.
 
     The workspace serves one call at a time: calls on several streams, or
     captured graphs that may replay at once, need a FewTokenLayer each, which

@@ -122,8 +122,8 @@ __device__ __forceinline__ void load_values(const uint8_t* p, float (&v)[V]) {
 
 // x [blocks, 128] to codes and one scale a block, 8 lanes of 16 values each
 // per block (fp4_quantize's row kernel, with 4 lanes and IEEE divisions, takes
-// 27 us for 8192 x 2560 bf16 and 5.5 us for 77 rows of f32 in a kernel trace;
-// this one 13.6, 4.7 TB/s, and 3.9).
+// 27 us for 8192 x 2560 bf16 and 5.1 us for 77 rows of f32 in a kernel trace;
+// this one 13.4, 4.7 TB/s, and 3.1).
 template <int XK>
 __global__ void __launch_bounds__(256) fp8_rows_kernel(const uint8_t* __restrict__ x, int64_t blocks, uint8_t* __restrict__ codes,
                                                        float* __restrict__ scales) {
@@ -631,7 +631,7 @@ struct TileModel {
 // 2560 x 8192 14.8, 22.7; 512 x 2560 x 2560 15.5, 11.4.  f32 results take the fp16 MFMA, whose
 // converted operands leave registers for 64 x 64 and 128 x 128 only.  The model has
 // no term for the bytes written: at K = 128 a tile takes up to twice what it says
-// (32 x (500 x 512 x 128): 5.2 modelled, 9.8 in a trace).
+// (32 x (500 x 512 x 128): 5.2 modelled, 9.2 in a trace).
 constexpr TileModel kTile64{64, 64, 4, 2.0, 0.34, 0.89}, kTile64Split{64, 64, 1, 4.4, 0.16, 0.26}, kTile128{128, 128, 2, 4.0, 0.60, 1.20}, kTile192{192, 256, 1, 4.4, 1.15, 1.58},
     kTile256{256, 256, 1, 5.0, 1.45, 2.05};
 

@@ -20,16 +20,16 @@
 //
 // Measured at 512 experts, hidden 2560, intermediate 640, top 10, in graph
 // replays over 16 sets of logits (us; in brackets the same layer through the
-// router and the sorted forward): 1, 4, 8 and 16 tokens with NVFP4 weights 28
-// [33], 45 [46], 72 [64], 112 [95]; MXFP4 26 [33], 42 [46], 63 [62], 100 [91];
-// NVFP4/NVFP4 34 [72], 53 [86], 78 [115], 122 [190]; MXFP4/MXFP8 25 [38], 43
-// [53], 64 [70], 101 [100]; block FP8 31 [58], 58 [83], 93 [114], 151 [175]; with a
-// shared expert of 1280: NVFP4/NVFP4, top 5, 16 tokens 85 [130], block FP8, 7
-// tokens 92 [128].  NVFP4 with little to read: 8 experts of 256 x 128, one token 16
-// [14]; 64 experts, top 4, 16 tokens 53 [44].  So the other way is faster with plain
-// activations from 8 tokens on or few weights, and at 16 with MXFP8: every
-// workgroup routes every token here, and plain h costs two or three columns a
-// pair.  Of the time at one token of NVFP4 routing takes 4.5, the
+// router and the sorted forward): 1, 4, 8 and 16 tokens with NVFP4 weights 27
+// [33], 45 [47], 70 [66], 111 [96]; MXFP4 25 [32], 41 [47], 62 [65], 100 [94];
+// NVFP4/NVFP4 33 [72], 53 [86], 78 [114], 122 [190]; MXFP4/MXFP8 25 [38], 42
+// [54], 64 [70], 101 [101]; block FP8 31 [58], 58 [85], 93 [115], 151 [175]; with a
+// shared expert of 1280: NVFP4/NVFP4, top 5, 16 tokens 85 [129], block FP8, 7
+// tokens 92 [126].  NVFP4 with little to read: 8 experts of 256 x 128, one token 16
+// [14]; 64 experts, top 4, 16 tokens 54 [44].  So with plain activations the other
+// way is faster above about 8 tokens or with few weights, with MXFP8 as fast at 16:
+// every workgroup routes every token here, and plain h costs two or three columns
+// a pair.  Of the time at one token of NVFP4 routing takes 4.5, the
 // list of experts 1.3, gate_up 9, each gap between kernels 1.5, the down products
 // 7, the sum 2; at 16 tokens routing and x~ 12, gate_up 56 (4.6 TB/s), the down
 // products 34 (3.8 TB/s).

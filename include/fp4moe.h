@@ -373,12 +373,12 @@ int moe_fp4_forward_noalloc(const moe_fp4_layer* layer, const uint16_t* x, int64
  * sequences.  Which way is faster depends on the layer (512 experts of hidden
  * 2560, intermediate 640, top 10, us in graph replays against moe_fp4_route +
  * moe_fp4_forward): with plain activations this one up to about 4 tokens (NVFP4
- * weights 1 token 28 against 33, 4 tokens 45 against 46, 8 tokens 72 against 64,
- * 16 tokens 112 against 95), with MXFP8 ones up to about 8 (16 tokens 101 against
- * 100), with NVFP4 and block-FP8 ones up to 16 (122 against 190, 151 against 175);
- * with plain activations and little to read the other one (8 experts of 256 x 128,
- * 1 token: 16 against 14; 64 experts, top 4, 16 tokens: 53 against 44).  The call
- * never takes the other way by itself.
+ * weights 1 token 27 against 33, 4 tokens 45 against 47, 8 tokens 70 against 66,
+ * 16 tokens 111 against 96), with MXFP8 ones up to about 8 (64 against 70; 16
+ * tokens 101 against 101), with NVFP4 and block-FP8 ones up to 16 (122 against 190,
+ * 151 against 175); with plain activations and little to read the other one (8
+ * experts of 256 x 128, 1 token: 16 against 14; 64 experts, top 4, 16 tokens: 54
+ * against 44).  The call never takes the other way by itself.
  *  x            bf16 [tokens, H], finite.
  *  logits, bias f32 [tokens, E] and [E] (bias may be NULL), selected from as by
  *               moe_fp4_route.  An expert whose logit + bias is -inf (or NaN)
