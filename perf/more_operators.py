@@ -1,0 +1,316 @@
+"""Four operators around a language-model head in 4 bits, in their plain form and as the framework's calls.
+
+matmul    y = x . W^T with W in NVFP4 (E2M1 codes, an E4M3 scale per 16 values, an f32 scale per tensor) or MXFP4 (E2M1
+          codes, a power-of-two scale per 32 values), x in bf16 or f32: projections and the head.
+grad      dx = dy . W, the gradient of that product with respect to x (the 4-bit weights are frozen).
+logprobs  from a row of logits, at a temperature: the log probability and the rank of a given token, the entropy, the
+          `top` most likely tokens with their log probabilities.
+lossgrad  the gradient of the log probabilities and the entropies with respect to the logits.
+
+All sizes are generic or those of the layers of this repository (hidden 2560, intermediate 640, 16 sequences, 8192
+prefill tokens).
+"""
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+BLOCK = {"nvfp4": 16, "mxfp4": 32}
+INF = float("inf")
+
+
+# ------------------------------------------------------------------ the cases
+
+def _mm(name, op, fmt, m, n, k, x="bf16", out="bf16", batch=1):
+    return {"name": name, "op": op, "fmt": fmt, "batch": batch, "m": m, "n": n, "k": k, "x": x, "out": out}
+
+
+def _lp(name, rows, vocab, x="bf16", top=0, temperature=1.0, masked=False, pad=0):
+    return {"name": name, "op": "logprobs", "rows": rows, "vocab": vocab, "x": x, "top": top, "temperature": temperature,
+            "masked": masked, "pad": pad}
+
+
+def _lg(name, rows, vocab, x="bf16", entropy=False, temperature=1.0, masked=False, pad=0):
+    return {"name": name, "op": "lossgrad", "rows": rows, "vocab": vocab, "x": x, "entropy": entropy,
+            "temperature": temperature, "masked": masked, "pad": pad}
+
+
+def listed():
+    return [
+        # a projection of one sequence's decode step: latency
+        _mm("mm_decode_1", "matmul", "nvfp4", 1, 2560, 2560),
+        # the head of 16 sequences' decode step, logits in f32: the weights' bytes
+        _mm("mm_head_16", "matmul", "mxfp4", 16, 131072, 2560, out="f32"),
+        # a short ragged prompt, f32 activations, widths that end inside every tile
+        _mm("mm_ragged_77", "matmul", "nvfp4", 77, 1001, 1296, x="f32"),
+        # prefill through a wide projection
+        _mm("mm_prefill", "matmul", "nvfp4", 8192, 10240, 2560),
+        # the gradient of a few tokens' adapters through a narrow projection, in f32
+        _mm("grad_few_16", "grad", "mxfp4", 16, 640, 2560, x="f32", out="f32"),
+        # a short ragged sequence, an odd output width
+        _mm("grad_ragged_300", "grad", "nvfp4", 300, 1001, 1296),
+        # a training batch through a wide projection
+        _mm("grad_batch", "grad", "nvfp4", 4096, 10240, 2560),
+        # one sampled token, five alternatives for the user: latency
+        _lp("lp_one", 1, 32000, top=5),
+        # 16 sequences under a grammar's mask (one has nothing left), f32 logits of a padded head
+        _lp("lp_masked_16", 16, 131000, x="f32", top=20, temperature=0.7, masked=True, pad=72),
+        # scoring a long prompt token by token
+        _lp("lp_score", 4096, 65536),
+        # policy gradient of a short ragged answer with its entropy bonus, f32
+        _lg("lg_ragged_300", 300, 50003, x="f32", entropy=True, temperature=0.8),
+        # distillation and fine-tuning: a batch's cross entropy
+        _lg("lg_batch", 4096, 65536),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(("matmul", "grad", "logprobs", "lossgrad"))
+    if op in ("matmul", "grad"):
+        fmt = rng.choice(("nvfp4", "mxfp4"))
+        batch = rng.choice((1, 1, 1, rng.randint(2, 16)))
+        k = BLOCK[fmt] * _log(rng, 1, 10240 // BLOCK[fmt])
+        n = max(1, min(_log(rng, 8, 131072), 131072 * 2560 // (batch * k)))
+        m = max(1, min(_log(rng, 1, 8192), 8192 * 10240 * 2560 // (2 * batch * n * k), (1 << 27) // (batch * max(n, k))))
+        return {"op": op, "fmt": fmt, "batch": batch, "m": m, "n": n, "k": k,
+                "x": rng.choice(("bf16", "bf16", "f32")), "out": rng.choice(("bf16", "bf16", "f32"))}
+    vocab = _log(rng, 100, 262144)
+    rows = max(1, min(_log(rng, 1, 8192), 4096 * 65536 // (2 * vocab)))
+    c = {"op": op, "rows": rows, "vocab": vocab, "x": rng.choice(("bf16", "f32")),
+         "temperature": rng.choice((1.0, 1.0, round(rng.uniform(0.5, 1.5), 2))), "masked": rng.random() < 0.3,
+         "pad": rng.choice((0, 0, rng.randint(1, 100)))}
+    if op == "logprobs":
+        return {**c, "top": rng.choice((0, 1, 5, 20, rng.randint(1, 64)))}
+    return {**c, "entropy": rng.random() < 0.5}
+
+
+# ------------------------------------------------------------------ work
+
+_WEIGHT_BYTES = {"nvfp4": 0.5 + 1 / 16, "mxfp4": 0.5 + 1 / 32}
+_BYTES = {"bf16": 2, "f32": 4}
+
+
+def work(case):
+    c = case
+    if c["op"] in ("matmul", "grad"):
+        b, m, n, k = c["batch"], c["m"], c["n"], c["k"]
+        i, o = (k, n) if c["op"] == "matmul" else (n, k)
+        return {"bytes": b * (m * i * _BYTES[c["x"]] + n * k * _WEIGHT_BYTES[c["fmt"]] + m * o * _BYTES[c["out"]]),
+                "flops": 2.0 * b * m * n * k}
+    size = c["rows"] * c["vocab"] * _BYTES[c["x"]]
+    if c["op"] == "logprobs":  # an exponential and two sums a value
+        return {"bytes": size + c["rows"] * (4 + 12 + 8 * c["top"]), "flops": 4.0 * c["rows"] * c["vocab"]}
+    return {"bytes": 2 * size + c["rows"] * 24, "flops": 4.0 * c["rows"] * c["vocab"]}
+
+
+# ------------------------------------------------------------------ inputs
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _randn(g, *shape):
+    return torch.randn(*shape, device="cuda", generator=g)
+
+
+def _weight(g, fmt, b, n, k):
+    """Codes of normal values (standard deviation 2.3 in units of a block's scale), scales around those of N(0, 0.02) weights."""
+    quantile = torch.special.ndtri((torch.arange(256, dtype=torch.float64) + 0.5) / 256) * 2.3
+    grid = torch.tensor(E2M1, dtype=torch.float64)
+    code = (quantile.abs()[:, None] - grid).abs().argmin(1) + 8 * (quantile < 0)
+    code = code.to(torch.uint8).cuda()
+    pick = lambda: code[torch.randint(0, 256, (b, n, k // 2), dtype=torch.int32, device="cuda", generator=g)]  # noqa: E731
+    w = {"codes": pick() | (pick() << 4), "tensor_scale": None}
+    if fmt == "nvfp4":
+        w["scales"] = torch.randint(0x72, 0x7F, (b, n, k // 16), dtype=torch.uint8, device="cuda", generator=g)
+        w["tensor_scale"] = (torch.rand(b, device="cuda", generator=g) * 0.4 + 0.8) * (0.11 / 2688)
+    else:
+        w["scales"] = torch.randint(119, 122, (b, n, k // 32), dtype=torch.uint8, device="cuda", generator=g)
+    return w
+
+
+def prepare(case, seed):
+    c, g = case, _gen(seed)
+    if c["op"] in ("matmul", "grad"):
+        b, m = c["batch"], c["m"]
+        x = _randn(g, b, m, c["k"] if c["op"] == "matmul" else c["n"]) * torch.exp(0.5 * _randn(g, b, m, 1))
+        return {"case": c, "x": x.to(DTYPES[c["x"]]), "w": _weight(g, c["fmt"], b, c["n"], c["k"])}
+    T, V = c["rows"], c["vocab"]
+    logits = (_randn(g, T, V + c["pad"]) * 2.5 * torch.exp(0.3 * _randn(g, T, 1))).to(DTYPES[c["x"]])[:, :V]
+    likely = logits.argmax(1)
+    some = torch.randint(0, V, (T,), device="cuda", generator=g)
+    if c["masked"]:  # what a grammar forbids, not the given tokens; the last of several rows has nothing left
+        for t in range(0, T, 512):  # in pieces: the random numbers of all rows at once would not fit three times
+            part = logits[t:t + 512]
+            part.masked_fill_(torch.rand(part.shape, device="cuda", generator=g) < 0.9, -INF)
+        logits[torch.arange(T, device="cuda"), some] = 1.0
+        logits[max(T - 1, 1):] = -INF
+    s = {"case": c, "logits": logits,
+         "targets": torch.where(torch.rand(T, device="cuda", generator=g) < (0.0 if c["masked"] else 0.6), likely, some).int()}
+    if c["op"] == "lossgrad":  # what the forward pass left: largest logit, sum of exponentials, entropy
+        z, _, total = _softmax(logits, c["temperature"])
+        e = torch.exp(z)
+        H = torch.log(total) - torch.where(e > 0, e * z, e).sum(1) / total
+        gone = total == 0
+        s["stats"] = torch.stack((logits.float().amax(1), total, torch.where(gone, torch.zeros_like(H), H)), 1)
+        s["d_logprobs"] = _randn(g, T) / T
+        s["d_entropy"] = torch.full((T,), 0.01 / T, device="cuda") if c["entropy"] else None
+    return s
+
+
+# ------------------------------------------------------------------ the operators in their plain form
+
+def _values(w, fmt):
+    """f32 values of 4-bit weights [b, n, k]."""
+    codes = w["codes"]
+    g = torch.tensor(E2M1 + tuple(-v for v in E2M1), dtype=torch.float32, device=codes.device)
+    byte = torch.arange(256, device=codes.device)
+    v = torch.stack((g[byte & 15], g[byte >> 4]), -1)[codes.int()].flatten(-2)
+    if fmt == "nvfp4":
+        s = w["scales"].view(torch.float8_e4m3fn).float() * w["tensor_scale"][:, None, None]
+    else:
+        s = torch.ldexp(torch.ones((), device=codes.device), w["scales"].int() - 127)
+    return (v.unflatten(-1, (-1, BLOCK[fmt])) * s[..., None]).flatten(-2)
+
+
+def _softmax(logits, temperature):
+    """(z, largest, sum e^z) of z = (l - largest) / temperature; -inf everywhere and 0 for a row of -inf."""
+    l = logits.float()
+    top = l.amax(1, keepdim=True)
+    z = (l - torch.where(top > -INF, top, torch.zeros_like(top))) / temperature
+    return z, top, torch.exp(z).sum(1)
+
+
+def _run_logprobs(s):
+    c, t = s["case"], s["targets"].long()
+    z, _, total = _softmax(s["logits"], c["temperature"])
+    T, V = z.shape
+    e = torch.exp(z)
+    logZ = torch.log(total)
+    live = total > 0
+    zero = torch.zeros_like(total)
+    H = torch.where(live, logZ - torch.where(e > 0, e * z, e).sum(1) / total, zero)
+    zt = z.gather(1, t[:, None])[:, 0]
+    lt = s["logits"].gather(1, t[:, None])
+    before = torch.arange(V, device=z.device)[None] < t[:, None]
+    rank = ((s["logits"] > lt) | ((s["logits"] == lt) & before)).sum(1).int()
+    lowest = torch.full_like(zt, -INF)
+    out = {"logprobs": torch.where(live, zt - logZ, lowest), "entropy": H, "ranks": rank}
+    if c["top"]:
+        k = min(c["top"], V)
+        l, ids = torch.sort(s["logits"], dim=1, descending=True, stable=True)
+        l, ids = l[:, :k], ids[:, :k]
+        lp = torch.where(live[:, None], z.gather(1, ids) - logZ[:, None], lowest[:, None])
+        ids = torch.where(l > -INF, ids, torch.full_like(ids, -1)).int()
+        more = c["top"] - k  # slots without a token
+        out["top_ids"] = torch.cat((ids, torch.full((T, more), -1, dtype=torch.int32, device=z.device)), 1)
+        out["top_logprobs"] = torch.cat((lp, torch.full((T, more), -INF, device=z.device)), 1)
+    return out
+
+
+def _run_lossgrad(s):
+    c, t = s["case"], s["targets"].long()
+    z, _, total = _softmax(s["logits"], c["temperature"])
+    live = (total > 0)[:, None]
+    p = torch.where(live, torch.exp(z) / total[:, None], torch.zeros_like(z))
+    d = -p * s["d_logprobs"][:, None]
+    if s["d_entropy"] is not None:
+        H = s["stats"][:, 2:3]
+        d = d - torch.where(p > 0, p * (z - torch.log(total)[:, None] + H), p) * s["d_entropy"][:, None]
+    hit = (torch.arange(z.shape[1], device=z.device)[None] == t[:, None]) & live
+    d = (d + torch.where(hit, s["d_logprobs"][:, None], torch.zeros_like(d))) / c["temperature"]
+    return d.to(s["logits"].dtype)
+
+
+def run(state):
+    s, c = state, state["case"]
+    if own:
+        import block_scaled_fp4_nvfp4_amd as fp
+        if c["op"] == "matmul":
+            return fp.fp4_matmul(s["x"], s["w"], c["fmt"], out_dtype=DTYPES[c["out"]])
+        if c["op"] == "grad":
+            return fp.fp4_matmul_grad(s["x"], s["w"], c["fmt"], out_dtype=DTYPES[c["out"]])
+        if c["op"] == "logprobs":
+            r = fp.token_logprobs(s["logits"], s["targets"], top=c["top"], temperature=c["temperature"])
+            return {name: r[name] for name in ("logprobs", "entropy", "ranks") + (("top_ids", "top_logprobs") if c["top"] else ())}
+        return fp.token_logprobs_grad(s["logits"], s["targets"], s["stats"], s["d_logprobs"], s["d_entropy"], temperature=c["temperature"])
+    if c["op"] == "matmul":
+        return torch.matmul(s["x"].float(), _values(s["w"], c["fmt"]).transpose(-1, -2).contiguous()).to(DTYPES[c["out"]])
+    if c["op"] == "grad":
+        return torch.matmul(s["x"].float(), _values(s["w"], c["fmt"])).to(DTYPES[c["out"]])
+    return _run_logprobs(s) if c["op"] == "logprobs" else _run_lossgrad(s)
+
+
+# ------------------------------------------------------------------ the definition in 64 bits
+
+def _w64(w, fmt, b):
+    """float64 values of one matrix of 4-bit weights."""
+    codes, scales = w["codes"][b], w["scales"][b]
+    nibble = torch.stack((codes % 16, codes // 16), -1).flatten(-2).int()
+    v = torch.tensor(E2M1, dtype=torch.float64, device=codes.device)[nibble % 8] * (1 - 2 * (nibble // 8))
+    if fmt == "nvfp4":
+        return v * (scales.view(torch.float8_e4m3fn).double() * w["tensor_scale"][b].double()).repeat_interleave(16, 1)
+    return v * (2.0 ** (scales.double() - 127)).repeat_interleave(32, 1)
+
+
+def _row64(row, t, c):
+    """One row's (logprob, entropy, rank, log probabilities, whether any token is left) in float64."""
+    l = row.double()
+    left = l > -INF
+    if not bool(left.any()):
+        return -INF, 0.0, int((torch.arange(len(l), device=l.device) < t).sum()), torch.full_like(l, -INF), False
+    z = l / c["temperature"]
+    lp = z - torch.logsumexp(z, 0)
+    p = torch.exp(lp)
+    H = -(p[left] * lp[left]).sum()
+    rank = (l > l[t]).sum() + (l[:t] == l[t]).sum()
+    return lp[t], H, int(rank), lp, True
+
+
+def exact(case, seed):
+    c, s = case, prepare(case, seed)
+    if c["op"] in ("matmul", "grad"):
+        out = []
+        for b in range(c["batch"]):
+            w = _w64(s["w"], c["fmt"], b)
+            out.append(s["x"][b].double() @ (w.t().contiguous() if c["op"] == "matmul" else w))
+        return torch.stack(out)
+    rows = [(s["logits"][i], int(t)) for i, t in enumerate(s["targets"].tolist())]
+    if c["op"] == "logprobs":
+        lps, Hs, ranks, ids, tops = [], [], [], [], []
+        for row, t in rows:
+            a, H, rank, lp, left = _row64(row, t, c)
+            lps.append(float(a)), Hs.append(float(H)), ranks.append(rank)
+            if c["top"]:
+                v = row.double()
+                k = min(c["top"], len(v))
+                cut = torch.topk(v, k).values[-1]
+                some = torch.nonzero((v >= cut) & (v > -INF))[:, 0].tolist()
+                val = v[some].tolist()
+                best = [some[i] for i in sorted(range(len(some)), key=lambda i: (-val[i], some[i]))[:k]]
+                ids.append(best + [-1] * (c["top"] - len(best)))
+                tops.append(lp[best].tolist() + [-INF] * (c["top"] - len(best)))
+        f = lambda v: torch.tensor(v, dtype=torch.float64)  # noqa: E731
+        out = {"logprobs": f(lps), "entropy": f(Hs), "ranks": torch.tensor(ranks, dtype=torch.int32)}
+        if c["top"]:
+            out["top_ids"], out["top_logprobs"] = torch.tensor(ids, dtype=torch.int32), f(tops)
+        return out
+    d = torch.zeros(c["rows"], c["vocab"], dtype=torch.float64, device="cuda")
+    for i, (row, t) in enumerate(rows):
+        _, H, _, lp, left = _row64(row, t, c)
+        if left:
+            p = torch.exp(lp)
+            d[i] = -float(s["d_logprobs"][i]) * p
+            d[i, t] += float(s["d_logprobs"][i])
+            if s["d_entropy"] is not None:
+                d[i] -= float(s["d_entropy"][i]) * torch.where(p > 0, p * (lp + H), p)
+    return d / c["temperature"]
