@@ -156,12 +156,9 @@ def prepare(case, seed):
         logits[max(T - 1, 1):] = -INF
     s = {"case": c, "logits": logits,
          "targets": torch.where(torch.rand(T, device="cuda", generator=g) < (0.0 if c["masked"] else 0.6), likely, some).int()}
-    if c["op"] == "lossgrad":  # what the forward pass left: largest logit, sum of exponentials, entropy
-        z, _, total = _softmax(logits, c["temperature"])
-        e = torch.exp(z)
-        H = torch.log(total) - torch.where(e > 0, e * z, e).sum(1) / total
-        gone = total == 0
-        s["stats"] = torch.stack((logits.float().amax(1), total, torch.where(gone, torch.zeros_like(H), H)), 1)
+    if c["op"] == "lossgrad":  # what the forward pass left: largest logit, sum of the other tokens' exponentials, entropy
+        z, rest, lnZ, H = _softmax(logits, c["temperature"])
+        s["stats"] = torch.stack((logits.float().amax(1), rest, H), 1)
         s["d_logprobs"] = _randn(g, T) / T
         s["d_entropy"] = torch.full((T,), 0.01 / T, device="cuda") if c["entropy"] else None
     return s
@@ -183,33 +180,35 @@ def _values(w, fmt):
 
 
 def _softmax(logits, temperature):
-    """(z, largest, sum e^z) of z = (l - largest) / temperature; -inf everywhere and 0 for a row of -inf."""
+    """Of z = (l - largest) / temperature: z, the sum of e^z without the largest logit's (small where a token is all but
+    certain, which 1 plus it would not show), ln of the whole sum, the entropy.  A row of -inf: -inf, -1, -inf, 0."""
     l = logits.float()
-    top = l.amax(1, keepdim=True)
+    top, at = l.max(1, keepdim=True)
+    live = top[:, 0] > -INF
     z = (l - torch.where(top > -INF, top, torch.zeros_like(top))) / temperature
-    return z, top, torch.exp(z).sum(1)
+    e = torch.exp(z)
+    rest = torch.where(live, e.scatter(1, at, 0.0).sum(1), -torch.ones_like(top[:, 0]))
+    lnZ = torch.log1p(rest)
+    H = torch.where(live, lnZ - torch.where(e > 0, e * z, e).sum(1) / (1 + rest), torch.zeros_like(lnZ))
+    return z, rest, lnZ, H
 
 
 def _run_logprobs(s):
     c, t = s["case"], s["targets"].long()
-    z, _, total = _softmax(s["logits"], c["temperature"])
+    z, _, lnZ, H = _softmax(s["logits"], c["temperature"])
     T, V = z.shape
-    e = torch.exp(z)
-    logZ = torch.log(total)
-    live = total > 0
-    zero = torch.zeros_like(total)
-    H = torch.where(live, logZ - torch.where(e > 0, e * z, e).sum(1) / total, zero)
+    live = lnZ > -INF
     zt = z.gather(1, t[:, None])[:, 0]
     lt = s["logits"].gather(1, t[:, None])
     before = torch.arange(V, device=z.device)[None] < t[:, None]
     rank = ((s["logits"] > lt) | ((s["logits"] == lt) & before)).sum(1).int()
     lowest = torch.full_like(zt, -INF)
-    out = {"logprobs": torch.where(live, zt - logZ, lowest), "entropy": H, "ranks": rank}
+    out = {"logprobs": torch.where(live, zt - lnZ, lowest), "entropy": H, "ranks": rank}
     if c["top"]:
         k = min(c["top"], V)
         l, ids = torch.sort(s["logits"], dim=1, descending=True, stable=True)
         l, ids = l[:, :k], ids[:, :k]
-        lp = torch.where(live[:, None], z.gather(1, ids) - logZ[:, None], lowest[:, None])
+        lp = torch.where(live[:, None], z.gather(1, ids) - lnZ[:, None], lowest[:, None])
         ids = torch.where(l > -INF, ids, torch.full_like(ids, -1)).int()
         more = c["top"] - k  # slots without a token
         out["top_ids"] = torch.cat((ids, torch.full((T, more), -1, dtype=torch.int32, device=z.device)), 1)
@@ -219,16 +218,15 @@ def _run_logprobs(s):
 
 def _run_lossgrad(s):
     c, t = s["case"], s["targets"].long()
-    z, _, total = _softmax(s["logits"], c["temperature"])
-    live = (total > 0)[:, None]
-    p = torch.where(live, torch.exp(z) / total[:, None], torch.zeros_like(z))
-    d = -p * s["d_logprobs"][:, None]
-    if s["d_entropy"] is not None:
-        H = s["stats"][:, 2:3]
-        d = d - torch.where(p > 0, p * (z - torch.log(total)[:, None] + H), p) * s["d_entropy"][:, None]
+    z, _, lnZ, _ = _softmax(s["logits"], c["temperature"])
+    live = (lnZ > -INF)[:, None]
+    lp = torch.where(live, z - lnZ[:, None], torch.full_like(z, -INF))
     hit = (torch.arange(z.shape[1], device=z.device)[None] == t[:, None]) & live
-    d = (d + torch.where(hit, s["d_logprobs"][:, None], torch.zeros_like(d))) / c["temperature"]
-    return d.to(s["logits"].dtype)
+    p = torch.exp(lp)
+    d = torch.where(hit, -torch.expm1(lp), -p) * s["d_logprobs"][:, None]  # [j = t] - p_j
+    if s["d_entropy"] is not None:
+        d = d - torch.where(p > 0, p * (lp + s["stats"][:, 2:3]), p) * s["d_entropy"][:, None]
+    return (d / c["temperature"]).to(s["logits"].dtype)
 
 
 def run(state):
