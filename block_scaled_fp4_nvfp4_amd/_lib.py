@@ -26,8 +26,9 @@ STATUS = {0: "FP4_OK", -1: "FP4_ERR_INVALID_ARG", -2: "FP4_ERR_SHAPE",
 EXPORTED = ["fp4_quantize", "fp4_quantize_hessian", "fp4_dequantize", "fp4_block_error", "moe_fp4_workspace_layout",
             "moe_fp4_workspace_size", "moe_fp4_forward", "moe_fp4_forward_profiled",
             "moe_fp4_route", "moe_fp4_tile_weights", "moe_fp4_forward_noalloc",
-            "moe_fp4_few_workspace_size", "moe_fp4_forward_few", "fp8_block_matmul_workspace_size", "fp8_block_matmul", "fp4_status_string",
-            "fp4_last_error"]
+            "moe_fp4_few_workspace_size", "moe_fp4_forward_few", "fp8_block_matmul_workspace_size", "fp8_block_matmul",
+            "fp4_matmul_workspace_size", "fp4_matmul", "fp4_matmul_grad_workspace_size", "fp4_matmul_grad",
+            "token_logprobs_workspace_size", "token_logprobs", "token_logprobs_grad", "fp4_status_string", "fp4_last_error"]
 NOALLOC_SCRATCH_BYTES = 64 << 20  # FP4_NOALLOC_SCRATCH_BYTES
 STAGES = ["permute", "x_quant", "gate_up", "h_quant", "down", "shared", "combine"]
 
@@ -104,6 +105,17 @@ def lib():
         L.fp8_block_matmul_workspace_size.restype = i32
         L.fp8_block_matmul.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, i64, vp, i32, vp, sz, vp]
         L.fp8_block_matmul.restype = i32
+        for name in ("fp4_matmul", "fp4_matmul_grad"):
+            f, size = getattr(L, name), getattr(L, name + "_workspace_size")
+            f.argtypes = [i32, vp, i32, vp, vp, vp, i64, i64, i64, i64, vp, i32, vp, sz, vp]
+            size.argtypes = [i32, i32, i64, i64, i64, i64, ctypes.POINTER(sz)]
+            f.restype = size.restype = i32
+        L.token_logprobs_workspace_size.argtypes = [i32, i64, i64, i32, ctypes.POINTER(sz)]
+        L.token_logprobs_workspace_size.restype = i32
+        L.token_logprobs.argtypes = [vp, i32, i64, i64, i64, vp, ctypes.c_float, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.token_logprobs.restype = i32
+        L.token_logprobs_grad.argtypes = [vp, i32, i64, i64, i64, vp, ctypes.c_float, vp, vp, vp, vp, i64, vp]
+        L.token_logprobs_grad.restype = i32
         L.fp4_status_string.argtypes = [i32]
         L.fp4_status_string.restype = ctypes.c_char_p
         L.fp4_last_error.argtypes = []
@@ -334,6 +346,174 @@ def fp8_matmul(x, w: dict, out_dtype: torch.dtype = torch.bfloat16, out: Optiona
                       _device_tensor(ws, dev, "W scales"), b, m, n, k, _device_tensor(out, dev, "out"), out_code,
                       None if workspace is None else _device_tensor(workspace, dev, "workspace"), ws_bytes,
                       _raw_stream(dev.index)))
+    return out
+
+
+_SIZES = {torch.bfloat16: DT_BF16, torch.float32: DT_F32}
+
+
+@functools.lru_cache(maxsize=4096)  # of the sizes alone
+def fp4_matmul_workspace_size(x_dtype: torch.dtype, batch: int, m: int, n: int, k: int, fmt: str, grad: bool = False) -> int:
+    """fp4_matmul_workspace_size, or fp4_matmul_grad_workspace_size with grad (x_dtype: dy's)."""
+    need = ctypes.c_size_t()
+    size = lib().fp4_matmul_grad_workspace_size if grad else lib().fp4_matmul_workspace_size
+    _check(size(FMT[fmt], _SIZES[x_dtype], batch, m, n, k, ctypes.byref(need)))
+    return need.value
+
+
+def _fp4_product(x, w, fmt, grad, out_dtype, out, workspace):
+    name = "dy" if grad else "x"
+    if fmt not in ("nvfp4", "mxfp4"):
+        raise ValueError(f"weights in nvfp4 or mxfp4 expected, got {fmt}")
+    codes, scales, ts = w["codes"], w["scales"], w.get("tensor_scale") if fmt == "nvfp4" else None
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or (fmt == "nvfp4" and (ts is None or ts.dtype != torch.float32)):
+        raise TypeError("w record of uint8 codes and scales (NVFP4: and a float32 tensor scale) expected")
+    code, out_code = _dtype_code(x), _SIZES.get(out_dtype)
+    if out_code is None:
+        raise TypeError(f"unsupported dtype {out_dtype}")
+    b, m, c = _dims(x)
+    wb, n, k = _dims(codes)
+    k *= 2
+    if wb != b or c != (n if grad else k):
+        raise ValueError(f"{name} {tuple(x.shape)} and W {tuple(codes.shape)} (two codes a byte) do not match")
+    block = 16 if fmt == "nvfp4" else 32
+    if scales.numel() != b * n * (k // block) or (ts is not None and ts.numel() != b):
+        raise ValueError("scales do not match their codes")
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError(f"device tensors expected, got {dev}")
+    shape = (m, k if grad else n) if x.dim() == 2 else (b, m, k if grad else n)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=dev)
+    elif out.dtype != out_dtype or tuple(out.shape) != shape:
+        raise ValueError(f"out {out.dtype} {tuple(out.shape)}, {out_dtype} {shape} expected")
+    if workspace is not None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    else:
+        ws_bytes = fp4_matmul_workspace_size(x.dtype, b, m, n, k, fmt, grad)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    call = lib().fp4_matmul_grad if grad else lib().fp4_matmul
+    _check(_on_device(dev.index, call, FMT[fmt], _device_tensor(x, dev, name), code, _device_tensor(codes, dev, "W"),
+                      _device_tensor(scales, dev, "W scales"), None if ts is None else _device_tensor(ts, dev, "W tensor scale"),
+                      b, m, n, k, _device_tensor(out, dev, "out"), out_code,
+                      None if workspace is None else _device_tensor(workspace, dev, "workspace"), ws_bytes, _raw_stream(dev.index)))
+    return out
+
+
+def fp4_matmul(x: torch.Tensor, w: dict, fmt: str, out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """fp4_matmul: y = x . W^T with 4-bit weights.
+
+    x: contiguous bf16 / f32 device tensor [M, K] or [B, M, K].
+    w: a record of quantize(w, fmt), fmt "nvfp4" or "mxfp4": codes [N, K/2] or
+    [B, N, K/2], scales [..., K/16] or [..., K/32] and for NVFP4 tensor_scale
+    [B].  A leading B = 1 of w may be left out or given either way.
+    Returns y [M, N] or [B, M, N] in out_dtype (bf16 or f32), in `out` if given
+    (not x's or w's memory), rounded once from f32 sums of exact operands.
+    workspace: a uint8 device tensor of fp4_matmul_workspace_size bytes;
+    allocated here when not given."""
+    return _fp4_product(x, w, fmt, False, out_dtype, out, workspace)
+
+
+def fp4_matmul_grad(dy: torch.Tensor, w: dict, fmt: str, out_dtype: torch.dtype = torch.bfloat16,
+                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """fp4_matmul_grad: dx = dy . W, the gradient of fp4_matmul(x, w, fmt) with
+    respect to x.  dy: contiguous bf16 / f32 device tensor [M, N] or [B, M, N]; w
+    as there; returns dx [M, K] or [B, M, K].  workspace:
+    fp4_matmul_workspace_size(..., grad=True) bytes."""
+    return _fp4_product(dy, w, fmt, True, out_dtype, out, workspace)
+
+
+@functools.lru_cache(maxsize=4096)
+def token_logprobs_workspace_size(dtype: torch.dtype, tokens: int, vocab: int, top: int = 0) -> int:
+    """token_logprobs_workspace_size."""
+    need = ctypes.c_size_t()
+    _check(lib().token_logprobs_workspace_size(_SIZES[dtype], tokens, vocab, top, ctypes.byref(need)))
+    return need.value
+
+
+def _logit_rows(t: torch.Tensor, name: str):
+    """(address, rows, vocabulary, row stride) of logits [T, V] whose rows are contiguous."""
+    if t.dim() != 2 or t.device.type != "cuda":
+        raise ValueError(f"{name}: device tensor [tokens, vocab] expected, got {tuple(t.shape)} on {t.device}")
+    T, V = t.shape
+    if V > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: contiguous rows expected, got strides {t.stride()}")
+    stride = t.stride(0) if T > 1 else V
+    if stride < V:
+        raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
+    return t.data_ptr(), T, V, stride
+
+
+def _per_token(t: Optional[torch.Tensor], dtype, T: int, dev, name: str):
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} of {t.dtype}, {dtype} expected")
+    if t.numel() != T:
+        raise ValueError(f"{name} {tuple(t.shape)} for {T} tokens")
+    return _device_tensor(t, dev, name)
+
+
+def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor], top: int = 0, temperature: float = 1.0,
+                   workspace: Optional[torch.Tensor] = None) -> dict:
+    """token_logprobs: what is read from a head's logits.
+
+    logits: bf16 / f32 device tensor [T, V]; rows may lie at any stride (a
+    padded head's logits[:, :V]).  targets: int32 [T], the given tokens (any
+    value outside [0, V): none), or None.
+    Returns a dict of f32 logprobs [T] and int32 ranks [T] (with targets), f32
+    entropy [T] (a view of stats), f32 stats [T, 3] for token_logprobs_grad
+    and, with top > 0, int32 top_ids and f32 top_logprobs [T, top]: the most
+    likely tokens, ties to the lower id; slots left over -1 and -inf.
+    workspace: a uint8 device tensor of token_logprobs_workspace_size bytes;
+    allocated here when not given."""
+    ptr, T, V, stride = _logit_rows(logits, "logits")
+    code, dev = _dtype_code(logits), logits.device
+    tp = _per_token(targets, torch.int32, T, dev, "targets")
+    f32 = functools.partial(torch.empty, dtype=torch.float32, device=dev)
+    stats = f32(T, 3)
+    r = {"entropy": stats[:, 2], "stats": stats}
+    lp = ranks = ids = tops = None
+    if targets is not None:
+        lp, ranks = f32(T), torch.empty(T, dtype=torch.int32, device=dev)
+        r["logprobs"], r["ranks"] = lp, ranks
+    if top > 0:
+        ids, tops = torch.empty(T, top, dtype=torch.int32, device=dev), f32(T, top)
+        r["top_ids"], r["top_logprobs"] = ids, tops
+    if workspace is not None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    else:
+        ws_bytes = token_logprobs_workspace_size(logits.dtype, T, V, top)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    _check(_on_device(dev.index, lib().token_logprobs, ptr, code, T, V, stride, tp, temperature, top, _ptr(lp), _ptr(ranks),
+                      _ptr(ids), _ptr(tops), _ptr(stats), None if workspace is None else _device_tensor(workspace, dev, "workspace"),
+                      ws_bytes, _raw_stream(dev.index)))
+    return r
+
+
+def token_logprobs_grad(logits: torch.Tensor, targets: Optional[torch.Tensor], stats: torch.Tensor,
+                        d_logprobs: Optional[torch.Tensor], d_entropy: Optional[torch.Tensor] = None, temperature: float = 1.0,
+                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """token_logprobs_grad: the gradient of sum(d_logprobs * logprobs +
+    d_entropy * entropy) with respect to the logits.  logits, targets and
+    temperature as in token_logprobs, stats from it; d_logprobs, d_entropy f32
+    [T] or None.  Returns d_logits [T, V] of the logits' type, in `out` if given
+    (rows at any stride; logits itself is allowed)."""
+    ptr, T, V, stride = _logit_rows(logits, "logits")
+    code, dev = _dtype_code(logits), logits.device
+    if out is None:
+        out = torch.empty(T, V, dtype=logits.dtype, device=dev)
+    elif out.dtype != logits.dtype or tuple(out.shape) != (T, V) or out.device != dev:
+        raise ValueError(f"out {out.dtype} {tuple(out.shape)} on {out.device}, {logits.dtype} {(T, V)} on {dev} expected")
+    optr, _, _, ostride = _logit_rows(out, "out")
+    if tuple(stats.shape) != (T, 3) or stats.dtype != torch.float32:
+        raise ValueError(f"stats {stats.dtype} {tuple(stats.shape)}, float32 {(T, 3)} expected")
+    _check(_on_device(dev.index, lib().token_logprobs_grad, ptr, code, T, V, stride, _per_token(targets, torch.int32, T, dev, "targets"),
+                      temperature, _device_tensor(stats, dev, "stats"), _per_token(d_logprobs, torch.float32, T, dev, "d_logprobs"),
+                      _per_token(d_entropy, torch.float32, T, dev, "d_entropy"), optr, ostride, _raw_stream(dev.index)))
     return out
 
 

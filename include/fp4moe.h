@@ -448,6 +448,102 @@ int fp8_block_matmul(const void* x, int x_dtype, const float* x_scales, const ui
                      int64_t batch, int64_t m, int64_t n, int64_t k, void* y, int y_dtype, void* workspace,
                      size_t workspace_bytes, void* stream);
 
+/*
+ * fp4_matmul - y[b] = x[b] . W[b]^T for `batch` independent products with 4-bit
+ * weights, the dense layer or the head beside a routed-expert layer:
+ *   y[m][n] = S sum_k x[m][k] g[n][k] s[n][k/B]
+ * g the E2M1 values, s the block scales and S the tensor scale (NVFP4: B = 16;
+ * MXFP4: B = 32 and no S).
+ *  w_fmt        FP4_FMT_NVFP4 or FP4_FMT_MXFP4.
+ *  x            bf16 or f32 [batch, m, k], `x_dtype`, finite.
+ *  w, w_scales, tensor_scale  codes [batch, n, k/2], scales [batch, n, k/B] and f32
+ *               [batch] (NVFP4), as fp4_quantize writes them.
+ *  y            [batch, m, n] bf16 or f32 (`y_dtype`), rounded once from f32 sums; no
+ *               input's memory.
+ *  workspace    fp4_matmul_workspace_size bytes of device memory, 16-byte aligned,
+ *               written before it is read in every call; NULL where that is 0.
+ *               Calls in flight at once, captured graphs among them, need one each.
+ * Operands are exact (bf16 x and decoded weights as they are, f32 x as three bf16
+ * terms, which lose what lies below 2^-133) and sums are f32, of products with S's
+ * power of two in them: nothing overflows or vanishes that does not in the result.  Weights beyond f32's range
+ * (MXFP4 scales of 2^126 and more) are infinite, as fp4_dequantize has them.  Every
+ * buffer is contiguous; any m >= 0 and n >= 0.  A result does not depend on other
+ * rows of x or other matrices' values, and repeats bit for bit.
+ * Errors: k % B, k == 0 -> FP4_ERR_SHAPE; unknown format or dtype, null or
+ * misaligned pointer (x: 16 bytes for bf16 with k % 64 == 0, else its type's; w: 8)
+ * -> FP4_ERR_INVALID_ARG; formats other than NVFP4 and MXFP4, more than 65535
+ * matrices, a dimension of 2^31, k above 2^22, more rows or outputs than a launch
+ * has threads for -> FP4_ERR_UNSUPPORTED; FP4_ERR_WORKSPACE.  Stream-ordered,
+ * asynchronous.
+ */
+int fp4_matmul_workspace_size(int w_fmt, int x_dtype, int64_t batch, int64_t m, int64_t n, int64_t k, size_t* bytes);
+int fp4_matmul(int w_fmt, const void* x, int x_dtype, const uint8_t* w, const void* w_scales, const float* tensor_scale,
+               int64_t batch, int64_t m, int64_t n, int64_t k, void* y, int y_dtype, void* workspace,
+               size_t workspace_bytes, void* stream);
+
+/*
+ * fp4_matmul_grad - the gradient of fp4_matmul with respect to x,
+ *   dx[m][k] = S sum_n dy[m][n] g[n][k] s[n][k/B],
+ * for the training of what lies below a frozen 4-bit layer (the weights, being
+ * codes, have no gradient).  dy bf16 or f32 [batch, m, n], dx bf16 or f32 [batch,
+ * m, k]; all else as fp4_matmul, n taking k's place in what it says of lengths and
+ * alignment of x: n == 0 -> FP4_ERR_SHAPE, n above 2^22 -> FP4_ERR_UNSUPPORTED, dy
+ * aligned to 16 bytes for bf16 with n % 64 == 0, else to its type.
+ */
+int fp4_matmul_grad_workspace_size(int w_fmt, int dy_dtype, int64_t batch, int64_t m, int64_t n, int64_t k, size_t* bytes);
+int fp4_matmul_grad(int w_fmt, const void* dy, int dy_dtype, const uint8_t* w, const void* w_scales,
+                    const float* tensor_scale, int64_t batch, int64_t m, int64_t n, int64_t k, void* dx, int dx_dtype,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * token_logprobs - what is read from a head's logits: of each of `tokens` rows l of
+ * `vocab` logits, with M = max l, z = (l - M) / temperature and Z = sum e^z,
+ *   logprobs[t]    z_target - ln Z, the log probability of the row's given token;
+ *   ranks[t]       how many logits come before the target's: larger ones, and equal
+ *                  ones of lower ids;
+ *   top_ids, top_logprobs [tokens, top]  the `top` first tokens in that order with their
+ *                  log probabilities;
+ *   stats[t]       f32 [tokens, 3]: M, Z - 1 (the sum without the largest logit's 1: it
+ *                  keeps its bits where a token is all but certain) and the entropy
+ *                  H = ln Z - sum z e^z / Z.
+ *  logits       bf16 or f32 (`dtype`), row t at logits + t * stride (in values).
+ *  targets      int32 [tokens]; one outside [0, vocab) is no token: logprob 0, rank
+ *               -1.  NULL if neither logprobs nor ranks is asked for.
+ *  temperature  positive and finite.
+ *  logprobs, ranks, stats  out, each optional (may be NULL); top_ids, top_logprobs out,
+ *               needed if top > 0 (top <= 64, which may exceed vocab).
+ *  workspace    as fp4_matmul's, of token_logprobs_workspace_size bytes.
+ * A logit of -inf is a masked token: it has probability 0 and is never among the
+ * alternatives; slots left over get id -1 and -inf.  A row with every token masked
+ * has logprob -inf and stats (-inf, -1, 0).  NaN or +inf in a row makes its logprobs,
+ * Z and H NaN; a NaN is never an alternative and comes before nothing.  Sums are f32.
+ * Results repeat bit for bit and do not depend on other rows.
+ * Errors: vocab < 1, stride < vocab -> FP4_ERR_SHAPE; unknown dtype, top, temperature,
+ * null or misaligned pointer (its type's) -> FP4_ERR_INVALID_ARG; 2^30 logits a row,
+ * 2^31 rows, more logits than 2^46 -> FP4_ERR_UNSUPPORTED; FP4_ERR_WORKSPACE.  tokens == 0 is a
+ * no-op.  Stream-ordered, asynchronous.
+ */
+int token_logprobs_workspace_size(int dtype, int64_t tokens, int64_t vocab, int top, size_t* bytes);
+int token_logprobs(const void* logits, int dtype, int64_t tokens, int64_t vocab, int64_t stride, const int32_t* targets,
+                   float temperature, int top, float* logprobs, int32_t* ranks, int32_t* top_ids, float* top_logprobs,
+                   float* stats, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * token_logprobs_grad - the gradient of sum_t (d_logprobs[t] logprobs[t] +
+ * d_entropy[t] H[t]) with respect to the logits, p_j = e^z_j / Z:
+ *   d_logits[j] = (d_logprobs ([j = target] - p_j) - d_entropy p_j (ln p_j + H)) / temperature
+ *  stats        of token_logprobs on the same logits and temperature.
+ *  d_logprobs, d_entropy  f32 [tokens], each optional (NULL: zeros); targets may be
+ *               NULL without d_logprobs.
+ *  d_logits     out, logits' type, row t at d_logits + t * d_stride; may be logits itself
+ *               (with d_stride == stride), no other overlap.
+ * Masked tokens other than the target, rows with every token masked and, of
+ * d_logprobs, rows whose target is no token get gradient 0.  Errors as token_logprobs.
+ */
+int token_logprobs_grad(const void* logits, int dtype, int64_t tokens, int64_t vocab, int64_t stride,
+                        const int32_t* targets, float temperature, const float* stats, const float* d_logprobs,
+                        const float* d_entropy, void* d_logits, int64_t d_stride, void* stream);
+
 const char* fp4_status_string(int status);
 const char* fp4_last_error(void);
 
