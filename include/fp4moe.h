@@ -520,8 +520,8 @@ int fp4_matmul_grad(int w_fmt, const void* dy, int dy_dtype, const uint8_t* w, c
  * Results repeat bit for bit and do not depend on other rows.
  * Errors: vocab < 1, stride < vocab -> FP4_ERR_SHAPE; unknown dtype, top, temperature,
  * null or misaligned pointer (its type's) -> FP4_ERR_INVALID_ARG; 2^30 logits a row,
- * 2^31 rows, more logits than 2^46 -> FP4_ERR_UNSUPPORTED; FP4_ERR_WORKSPACE.  tokens == 0 is a
- * no-op.  Stream-ordered, asynchronous.
+ * 2^24 rows, more logits than 2^46 -> FP4_ERR_UNSUPPORTED; FP4_ERR_WORKSPACE.
+ * tokens == 0 is a no-op.  Stream-ordered, asynchronous.
  */
 int token_logprobs_workspace_size(int dtype, int64_t tokens, int64_t vocab, int top, size_t* bytes);
 int token_logprobs(const void* logits, int dtype, int64_t tokens, int64_t vocab, int64_t stride, const int32_t* targets,
