@@ -21,6 +21,7 @@ namespace fp4 {
 
 constexpr int kTopMost = 64;    // one lane of a wave each
 constexpr int kSplitsMost = 64;  // parts of a row, one lane each when they meet
+constexpr int kFewInserts = 6;   // alternatives that are inserted one by one; more are sorted and merged
 constexpr float kLog2E = 1.44269504f, kLn2 = 0.693147181f;
 
 struct LogprobArgs {
@@ -83,20 +84,43 @@ __device__ __forceinline__ int from_lane_before(int v) { return __builtin_amdgcn
 // The best alternatives so far, lane j the j-th, largest first, ties by id; empty
 // ones are (-inf, none).
 constexpr int kNone = 0x7FFFFFFF;
+__device__ __forceinline__ bool before(float a, int ia, float b, int ib) { return a > b || (a == b && ia < ib); }
+
 struct TopList {
   float v = -__builtin_huge_valf();
   int id = kNone;
-  __device__ __forceinline__ void insert(float cv, int cid) {  // cv, cid: the same for every lane
+  // One step of a sorting network: of each two lanes `d` apart the one with `first` gets the element that comes before.
+  __device__ __forceinline__ void exchange(int d, bool first) {
+    const float ov = __shfl_xor(v, d);
+    const int oid = __shfl_xor(id, d);
+    if (before(v, id, ov, oid) != first) v = ov, id = oid;
+  }
+  __device__ __forceinline__ void sort() {
     const int lane = threadIdx.x & 63;
-    const bool stays = v > cv || (v == cv && id < cid);
-    const int at = __popcll(__ballot(stays));
+#pragma unroll
+    for (int n = 2; n <= 64; n *= 2)
+#pragma unroll
+      for (int d = n / 2; d > 0; d /= 2) exchange(d, ((lane & d) == 0) == ((lane & n) == 0));
+  }
+  // The first 64 of both lists: of the j-th here and the j-th last there the better, which
+  // rise and fall once, so that the network's last six steps sort them.
+  __device__ __forceinline__ void merge(float ov, int oid) {
+    const int lane = threadIdx.x & 63;
+    ov = __shfl_xor(ov, 63);
+    oid = __shfl_xor(oid, 63);
+    if (before(ov, oid, v, id)) v = ov, id = oid;
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) exchange(d, (lane & d) == 0);
+  }
+  __device__ __forceinline__ void insert(float cv, int cid) {  // cv, cid: the same for every lane
+    const int lane = threadIdx.x & 63, at = __popcll(__ballot(before(v, id, cv, cid)));
     const int pv = from_lane_before(__float_as_int(v)), pid = from_lane_before(id);
     if (lane > at) v = __int_as_float(pv), id = pid;
     if (lane == at) v = cv, id = cid;
   }
 };
 
-// One of the lanes with the largest v: the one with the lowest id among equals.
+// Of the lanes with the largest v the one with the lowest id.
 __device__ __forceinline__ int lane_of_max(float v, int id, float most) {
   uint64_t which = __ballot(v == most);
   if (__popcll(which) > 1) {
@@ -108,26 +132,16 @@ __device__ __forceinline__ int lane_of_max(float v, int id, float most) {
   return (int)__ffsll((unsigned long long)which) - 1;
 }
 
-// `lists` sorted lists (v, id) of `top` each, `stride` apart, into one, by one wave: a lane holds a list's head.
-__device__ __forceinline__ TopList merge_lists(const float* v, const int* id, int lists, int stride, int top) {
+// The lists of a workgroup's WAVES waves (a power of two) into wave 0's, pair by pair.
+template <int WAVES>
+__device__ __forceinline__ void merge_waves(TopList& best, int wave, float (&v)[WAVES][kTopMost], int (&id)[WAVES][kTopMost]) {
   const int lane = threadIdx.x & 63;
-  TopList out;
-  int p = 0;
-  float hv = lane < lists ? v[lane * stride] : -__builtin_huge_valf();
-  int hid = lane < lists ? id[lane * stride] : kNone;
-  for (int j = 0; j < top; ++j) {
-    const float most = wave_max(hv);
-    if (!(most > -__builtin_huge_valf())) break;
-    const int from = lane_of_max(hv, hid, most);
-    const int bid = __builtin_amdgcn_readlane(hid, from);
-    if (lane == j) out.v = most, out.id = bid;
-    if (lane == from) {
-      ++p;
-      hv = p < top ? v[lane * stride + p] : -__builtin_huge_valf();
-      hid = p < top ? id[lane * stride + p] : kNone;
-    }
+#pragma unroll
+  for (int d = 1; d < WAVES; d *= 2) {
+    if ((wave & (2 * d - 1)) == d) v[wave][lane] = best.v, id[wave][lane] = best.id;
+    __syncthreads();
+    if ((wave & (2 * d - 1)) == 0) best.merge(v[wave + d][lane], id[wave + d][lane]);
   }
-  return out;
 }
 
 // A row's results from its sums and alternatives, by one wave.
@@ -158,8 +172,8 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& a, int64_t row, co
 // t = (l - m) c, 2^t, the two sums and the count of logits before the target, 10
 // operations a bf16 value; a round that reaches it (few do) brings the sums to the
 // new one and counts the exponentials that are 1.  Alternatives: a round with
-// nothing above the wave's last one costs a comparison; else its largest values are
-// taken out of it one by one.
+// nothing above the wave's last one costs a comparison; else the lanes' largest values
+// are taken out and inserted, or where they are many sorted and merged into the list.
 template <typename T>
 __global__ void __launch_bounds__(256) logprobs_kernel(LogprobArgs a) {
   constexpr int PV = 16 / (int)sizeof(T), NV = 2 * PV;  // values of a piece, of a lane's round
@@ -186,7 +200,8 @@ __global__ void __launch_bounds__(256) logprobs_kernel(LogprobArgs a) {
   Sums s = no_sums();
   float R = 0.0f, E = 0.0f, gate = ninf;  // a lane's sums; logits below `gate` have 2^t < 1
   TopList best;
-  float least = ninf;                     // the last alternative's logit
+  float least = ninf;                     // the last alternative
+  int least_id = kNone;
   u32x4 raw[2];
   auto load = [&](int p0) __attribute__((always_inline)) {
 #pragma unroll
@@ -270,16 +285,29 @@ __global__ void __launch_bounds__(256) logprobs_kernel(LogprobArgs a) {
       for (int i = 0; i < NV; ++i) s.rank += __popcll(__ballot(v[i] >= bar));
     }
     if (a.top > 0) {
-      while (__any(lm > least)) {
-        const float most = wave_max(lm);
-        int k = NV;  // the first of this lane's values that is the largest
+      while (__any(lm >= least && lm > ninf)) {
+        int k = NV;  // the first of this lane's values that is its largest
 #pragma unroll
-        for (int i = NV - 1; i >= 0; --i) k = v[i] == most ? i : k;
-        const int id = k < NV ? (p0 + 64 * (k / PV) + lane) * PV - skip + k % PV : kNone;
-        const int from = lane_of_max(lm, id, most);
-        best.insert(most, __builtin_amdgcn_readlane(id, from));
+        for (int i = NV - 1; i >= 0; --i) k = v[i] == lm ? i : k;
+        const int id = (p0 + 64 * (k / PV) + lane) * PV - skip + k % PV;
+        const bool better = lm > ninf && before(lm, id, least, least_id);
+        const uint64_t which = __ballot(better);
+        if (which == 0) break;
+        bool gone = better;
+        if (__popcll(which) > kFewInserts) {  // every such lane's largest at once
+          TopList some;
+          if (better) some.v = lm, some.id = id;
+          some.sort();
+          best.merge(some.v, some.id);
+        } else {
+          const float most = wave_max(better ? lm : ninf);
+          const int from = lane_of_max(better ? lm : ninf, id, most);
+          best.insert(most, __builtin_amdgcn_readlane(id, from));
+          gone = lane == from;
+        }
         least = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(best.v), a.top - 1));
-        if (lane == from) {
+        least_id = __builtin_amdgcn_readlane(best.id, a.top - 1);
+        if (gone) {
           lm = ninf;
 #pragma unroll
           for (int i = 0; i < NV; ++i) {
@@ -298,16 +326,14 @@ __global__ void __launch_bounds__(256) logprobs_kernel(LogprobArgs a) {
   s.R = R;
   s.E = E;
   if (lane == 0) sums_of[wave] = s;
-  list_v[wave][lane] = best.v;
-  list_id[wave][lane] = best.id;
-  __syncthreads();
+  if (a.top > 0) merge_waves<4>(best, wave, list_v, list_id);
+  else __syncthreads();
   if (wave != 0) return;
   s = sums_of[0];
 #pragma unroll
   for (int w = 1; w < 4; ++w) join(s, sums_of[w], c);
   // what the first piece holds before the row counted as masked logits of lower ids
   if (split == 0 && lt == ninf) s.rank -= skip;
-  if (a.top > 0) best = merge_lists(&list_v[0][0], &list_id[0][0], 4, kTopMost, a.top);
   if (a.splits == 1) {
     finish_row(a, row, s, best, given, lt);
     return;
@@ -320,22 +346,36 @@ __global__ void __launch_bounds__(256) logprobs_kernel(LogprobArgs a) {
   }
 }
 
-// The parts of a row by one wave.
+// The parts of a row: eight waves merge their alternatives, a wave taking every
+// eighth part's, and one joins their sums.
 template <typename T>
-__global__ void __launch_bounds__(64) logprobs_join_kernel(LogprobArgs a) {
-  __shared__ float list_v[kSplitsMost * kTopMost];
-  __shared__ int list_id[kSplitsMost * kTopMost];
+__global__ void __launch_bounds__(512) logprobs_join_kernel(LogprobArgs a) {
+  constexpr int WAVES = 8, EACH = kSplitsMost / WAVES;
+  __shared__ float list_v[WAVES][kTopMost];
+  __shared__ int list_id[WAVES][kTopMost];
   const int64_t row = blockIdx.x;
-  const int lane = threadIdx.x, size = 8 + 2 * a.top;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), size = 8 + 2 * a.top;
   const float* parts = a.parts + row * a.splits * size;
   const float c = a.inv_t * kLog2E;
   Sums s = no_sums();
-  if (lane < a.splits) s = *reinterpret_cast<const Sums*>(parts + lane * size);
-  for (int i = lane; i < a.splits * a.top; i += 64) {
-    const float* p = parts + i / a.top * size + 8 + i % a.top;
-    list_v[i] = p[0];
-    list_id[i] = __float_as_int(p[a.top]);
+  if (wave == 0 && lane < a.splits) s = *reinterpret_cast<const Sums*>(parts + lane * size);
+  TopList best;
+  if (a.top > 0) {
+    TopList of[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
+      if (wave + WAVES * i < a.splits && lane < a.top) {
+        const float* p = parts + (wave + WAVES * i) * size + 8 + lane;
+        of[i].v = p[0];
+        of[i].id = __float_as_int(p[a.top]);
+      }
+    best = of[0];
+#pragma unroll
+    for (int i = 1; i < EACH; ++i)
+      if (wave + WAVES * i < a.splits) best.merge(of[i].v, of[i].id);
+    merge_waves<WAVES>(best, wave, list_v, list_id);
   }
+  if (wave != 0) return;
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {  // lane i takes lane i + o, in a fixed order
     Sums b;
@@ -351,9 +391,6 @@ __global__ void __launch_bounds__(64) logprobs_join_kernel(LogprobArgs a) {
   s.E = __shfl(s.E, 0);
   s.ones = __shfl(s.ones, 0);
   s.rank = __shfl(s.rank, 0);
-  __syncthreads();
-  TopList best;
-  if (a.top > 0) best = merge_lists(list_v, list_id, a.splits, a.top, a.top);
   const int32_t t = a.targets ? a.targets[row] : -1;
   const bool given = t >= 0 && t < a.V;
   const float lt = given ? logit(static_cast<const T*>(a.logits) + row * a.stride, t) : 0.0f;
@@ -507,8 +544,8 @@ int token_logprobs(const void* logits, int dtype, int64_t tokens, int64_t vocab,
   else hipLaunchKernelGGL(logprobs_kernel<uint16_t>, grid, dim3(256), 0, st, a);
   FP4_CHECK(check_launch("token_logprobs"));
   if (splits == 1) return FP4_OK;
-  if (dtype == FP4_DT_F32) hipLaunchKernelGGL(logprobs_join_kernel<float>, dim3((unsigned)tokens), dim3(64), 0, st, a);
-  else hipLaunchKernelGGL(logprobs_join_kernel<uint16_t>, dim3((unsigned)tokens), dim3(64), 0, st, a);
+  if (dtype == FP4_DT_F32) hipLaunchKernelGGL(logprobs_join_kernel<float>, dim3((unsigned)tokens), dim3(512), 0, st, a);
+  else hipLaunchKernelGGL(logprobs_join_kernel<uint16_t>, dim3((unsigned)tokens), dim3(512), 0, st, a);
   return check_launch("token_logprobs");
 }
 
