@@ -15,6 +15,8 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "fp4_device.h"
 #include "host_common.h"
@@ -66,7 +68,7 @@ __global__ void __launch_bounds__(256) fp4_rows_kernel(const T* __restrict__ x, 
       for (int t = 0; t < 3; ++t) {
         const uint32_t top = __float_as_uint(v) & 0xFFFF0000u;
         d[t][j >> 1] |= (j & 1) ? top : top >> 16;
-        v = __builtin_amdgcn_classf(v, 0x207) ? 0.0f : v - __uint_as_float(top);  // infinities and NaN leave nothing
+        v -= __uint_as_float(top);
       }
     }
   }
@@ -74,26 +76,23 @@ __global__ void __launch_bounds__(256) fp4_rows_kernel(const T* __restrict__ x, 
   for (int t = 0; t < TERMS; ++t) st16(out + t * rows * ld + row * ld + c, u32x4{d[t][0], d[t][1], d[t][2], d[t][3]});
 }
 
-// 16 codes of a row (two dwords) and their block's scale byte to 16 bf16 values.
-// `pow2`: the power of two of the tensor scale (NVFP4).
+// The float that a block's scale byte stands for as decode2 takes it: MXFP4's
+// conversion reads the exponent byte alone (0 is 2^-127, 255 NaN); `pow2` is the power
+// of two of the NVFP4 tensor scale.
 template <int FMT>
-__device__ __forceinline__ void decode16(uint32_t a, uint32_t b, uint32_t scale, float pow2, uint32_t (&out)[8]) {
+__device__ __forceinline__ float block_scale(uint32_t byte, float pow2) {
+  if constexpr (FMT == FP4_FMT_MXFP4) return __uint_as_float(byte << 23);
+  else return __builtin_amdgcn_cvt_f32_fp8((int)byte, 0) * pow2;
+}
+// The codes of byte I of a dword, scaled, as two bf16 values, exactly.
+template <int FMT, int I>
+__device__ __forceinline__ uint32_t decode2(uint32_t codes, float scale) {
   if constexpr (FMT == FP4_FMT_MXFP4) {
-    const float s = __uint_as_float(scale << 23);  // the conversion reads the exponent byte: 0 is 2^-127, 255 NaN
-#define FP4_CVT(d, i) __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, i))
-    out[0] = FP4_CVT(a, 0); out[1] = FP4_CVT(a, 1); out[2] = FP4_CVT(a, 2); out[3] = FP4_CVT(a, 3);
-    out[4] = FP4_CVT(b, 0); out[5] = FP4_CVT(b, 1); out[6] = FP4_CVT(b, 2); out[7] = FP4_CVT(b, 3);
-#undef FP4_CVT
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, I));
   } else {
-    const float s = __builtin_amdgcn_cvt_f32_fp8((int)scale, 0) * pow2;
-    float v[16];
-    e2m1x8_to_f32x8(a, *reinterpret_cast<float(*)[8]>(v));
-    e2m1x8_to_f32x8(b, *reinterpret_cast<float(*)[8]>(v + 8));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bf16x2_t p{(__bf16)(v[2 * i] * s), (__bf16)(v[2 * i + 1] * s)};  // exact
-      out[i] = __builtin_bit_cast(uint32_t, p);
-    }
+    const f32x2_t v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, I);
+    const bf16x2_t p{(__bf16)(v.x * scale), (__bf16)(v.y * scale)};
+    return __builtin_bit_cast(uint32_t, p);
   }
 }
 
@@ -107,6 +106,290 @@ __device__ __forceinline__ void split_scale(float S, float& pow2, float& mant) {
 }
 
 __device__ __forceinline__ bf16x8_t as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8_t, v); }
+
+// ------------------------------------------------------------ few rows
+
+constexpr int kFewK = 256;   // a wave's step: 128 bytes of codes of each of 16 rows of W
+constexpr int kRing = 4;     // steps on their way to a wave
+constexpr int kSlot = 2304;  // bytes of a step: 2 KB of codes, scales
+constexpr int kDirectRows = 4;
+// Waves that multiply: seven and the adding one have 256 registers each, eight and it 168.
+constexpr int few_waves(int ms, int u, int terms) { return ms * u * terms > 2 ? 7 : 8; }
+constexpr int few_per_simd(int ms, int u, int terms) { return ms * u * terms == 2 ? 4 : ms * u * terms == 1 ? 6 : ms * u * terms == 3 ? 3 : 2; }
+
+struct Fp4FewArgs {
+  const void* x;       // [batch][M][K]
+  const uint8_t* w;    // [batch][N][K / 2]
+  const uint8_t* ws;
+  const float* ts;
+  void* y;             // [batch][M][N]
+  int64_t M, N;
+  int K, y_f32;
+};
+
+// Eight values of x as TERMS bf16 fragments (f32: three, whose sum they are; see fp4_rows_kernel), zeros where not `ok`.
+template <int TERMS>
+struct XPiece {
+  u32x4 v[TERMS == 3 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* x, int64_t at) {
+    if constexpr (TERMS == 1) {
+      v[0] = ld16(static_cast<const uint16_t*>(x) + at);
+    } else {
+      v[0] = ld16(static_cast<const float*>(x) + at);
+      v[1] = ld16(static_cast<const float*>(x) + at + 4);
+    }
+  }
+  __device__ __forceinline__ void arrived() {
+#pragma unroll
+    for (int i = 0; i < (TERMS == 3 ? 2 : 1); ++i) asm volatile("" : "+v"(v[i]));
+  }
+  __device__ __forceinline__ void terms(bool ok, bf16x8_t (&f)[TERMS]) const {
+    if constexpr (TERMS == 1) {
+      f[0] = as_bf16x8(ok ? v[0] : u32x4{0, 0, 0, 0});
+    } else {
+      u32x4 d[3];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        float a = ok ? __uint_as_float(v[p >> 1][2 * (p & 1)]) : 0.0f, b = ok ? __uint_as_float(v[p >> 1][2 * (p & 1) + 1]) : 0.0f;
+#pragma unroll
+        for (int t = 0; t < 3; ++t) {
+          const uint32_t ta = __float_as_uint(a) & 0xFFFF0000u, tb = __float_as_uint(b) & 0xFFFF0000u;
+          d[t][p] = __builtin_amdgcn_perm(tb, ta, 0x07060302);  // the upper halves
+          a -= __uint_as_float(ta);
+          b -= __uint_as_float(tb);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 3; ++t) f[t] = as_bf16x8(d[t]);
+    }
+  }
+};
+
+// 16 MS rows of x: a workgroup walks over strips of 16 outputs; wave w takes the steps
+// w, w + waves, ... of K (U at most) of every strip.  Its share of x is loaded once
+// and stays in registers as MFMA fragments; its share of W streams through a ring of
+// steps in LDS that belongs to the wave alone (DMA), is decoded in registers and goes
+// into the MFMAs as their A operand.  A strip's partial sums meet in LDS.  Where rows
+// of codes or scales are not whole pieces of DMA (DMA false), they are loaded
+// straight into registers, without a step ahead.  Bound by W's bytes, or by latency
+// where they are few.
+template <int FMT, int TERMS, int MS, int U, bool DMA>
+__global__ void __launch_bounds__(64 * (few_waves(MS, U, TERMS) + 1), few_per_simd(MS, U, TERMS)) fp4_few_kernel(Fp4FewArgs a) {
+  constexpr int SLOT = kSlot, RING = DMA ? kRing * SLOT : 8192, BLOCKS = FMT == FP4_FMT_NVFP4 ? 16 : 8;  // scales of a row and step
+  extern __shared__ __attribute__((aligned(16))) uint8_t few_lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = (blockDim.x >> 6) - 1, g = lane >> 4, r = lane & 15;
+  uint8_t* ring = few_lds + waves * (2 * MS * 1024) + wave * RING;  // W's steps; before them 8 KB of x
+  const int64_t b = blockIdx.z, m0 = (int64_t)blockIdx.y * (16 * MS);
+  const int KS = (a.K + kFewK - 1) / kFewK, strips = (int)((a.N + 15) >> 4), first = blockIdx.x, stride = gridDim.x;
+  const int nu = max(0, (KS - wave + waves - 1) / waves), mine = (strips - first + stride - 1) / stride;
+  const uint32_t wrow = (uint32_t)a.K / 2, srow = (uint32_t)a.K / (kFewK / BLOCKS);
+  const uint8_t* wbase = a.w + b * a.N * wrow;
+  const uint8_t* sbase = a.ws + b * a.N * srow;
+  float pow2 = 1.0f, mant = 1.0f;
+  if constexpr (FMT == FP4_FMT_NVFP4) split_scale(a.ts[b], pow2, mant);
+  if (wave == waves) {  // the last wave adds up the others' sums of a strip while they are at the next one
+    const bool vec = a.N % 4 == 0 && (uintptr_t)a.y % 16 == 0;
+    const int m = lane >> 2, n = 4 * (lane & 3);
+    for (int i = 0; i < mine; ++i) {
+      asm volatile("s_barrier" ::: "memory");
+      const float* part = reinterpret_cast<const float*>(few_lds) + (i & 1) * waves * (MS * 256);
+      const int64_t n0 = (int64_t)(first + i * stride) * 16 + n;
+#pragma unroll
+      for (int s = 0; s < MS; ++s) {
+        floatx4 v{0.f, 0.f, 0.f, 0.f};
+        for (int w = 0; w < waves; ++w) v += *reinterpret_cast<const floatx4*>(part + (w * MS + s) * 256 + m * 16 + 4 * ((n >> 2) ^ ((m >> 1) & 3)));
+        v *= mant;
+        const int64_t row = m0 + 16 * s + m, at = (b * a.M + row) * a.N + n0;
+        if (row >= a.M) continue;
+        const bf16x2_t lo{(__bf16)v[0], (__bf16)v[1]}, hi{(__bf16)v[2], (__bf16)v[3]};
+        const u32x2 h{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+        if (vec && n0 < a.N) {
+          if (a.y_f32) *reinterpret_cast<floatx4*>(static_cast<float*>(a.y) + at) = v;
+          else *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + at) = h;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (n0 + c < a.N) {
+              if (a.y_f32) static_cast<float*>(a.y)[at + c] = v[c];
+              else static_cast<uint16_t*>(a.y)[at + c] = (uint16_t)(h[c >> 1] >> (16 * (c & 1)));
+            }
+        }
+      }
+    }
+    return;
+  }
+
+  // DMA of strip i's step u into a slot: row j of the strip at 128 j, its 16-byte chunks swizzled by the row so that
+  // 16 rows' reads of a chunk touch all banks; then 16 rows of scales.  A lane's offsets are the same in every strip:
+  // rows past the last one are left out by the buffer's bounds (their results are not stored), and what lies past the
+  // end of a row is not used.
+  constexpr int DW = BLOCKS / 4;  // dwords of scales of a row
+  uint32_t at_code[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int row = 8 * j + (lane >> 3);
+    at_code[j] = row * wrow + 16 * ((lane & 7) ^ ((row >> 1) & 7));
+  }
+  const uint32_t at_scale = ((lane / DW) & 15) * srow + 4 * (lane % DW);
+  int li = 0, lu = 0;  // the next step to load
+  auto load_next = [&](int slot) __attribute__((always_inline)) {
+    // past the end the last strip is loaded again, so that every step issues three instructions
+    const int64_t n0 = (int64_t)(first + min(li, mine - 1) * stride) * 16;
+    const int kb = wave + waves * lu, rows = (int)min((int64_t)16, a.N - n0);
+    const auto codes = buffer_of(wbase + n0 * wrow, rows * wrow);
+    const auto scales = buffer_of(sbase + n0 * srow, rows * srow);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) dma_buffer(codes, at_code[j], 128 * kb, ring + SLOT * slot + 1024 * j);
+    dma_buffer4(scales, at_scale, BLOCKS * kb, ring + SLOT * slot + 2048);
+    if (++lu == nu) { lu = 0; ++li; }
+  };
+  bf16x8_t xf[U][2][4][MS][TERMS];
+  if (nu > 0) {
+    // 16 rows of x at a time, 512 bytes of each, come in by DMA (the ring is not in use yet): fragments straight from
+    // memory would touch a row in every lane.  For a few rows those are fewer, and the same for many lanes.
+    constexpr int XB = TERMS == 3 ? 4 : 2, PARTS = TERMS == 3 ? 2 : 1;
+    const bool direct = a.M <= kDirectRows;
+    if (DMA && direct) {
+#pragma unroll
+      for (int d = 0; d < kRing; ++d) load_next(d);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int s = 0; s < MS; ++s) {
+        const int64_t m = b * a.M + min(m0 + 16 * s, a.M - 1);  // blocks past the end: the last row, not stored
+        const int last = (int)max((int64_t)0, min((int64_t)15, a.M - 1 - m0 - 16 * s));
+        const int k0 = kFewK * (wave + waves * u);
+        XPiece<TERMS> piece[2][4];
+        if (direct) {
+          const int64_t row = (m + min(r, last)) * a.K;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int k = k0 + 128 * h + 32 * g + 8 * q;
+              piece[h][q].load(a.x, row + (k < a.K ? k : 0));
+            }
+        } else {
+          const uint32_t bytes = (uint32_t)a.K * XB;
+          const auto rows = buffer_of(static_cast<const uint8_t*>(a.x) + m * bytes, (uint32_t)(last + 1) * bytes);
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) {
+            const int at = k0 * XB + 512 * p;  // of the row's bytes
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int row = 2 * j + (lane >> 5), from = at + 16 * ((lane & 31) ^ row);
+              dma_buffer(rows, (uint32_t)min(row, last) * bytes + ((uint32_t)from < bytes ? from : 0), 0, ring + 1024 * j);
+            }
+            __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if (TERMS == 3 && h != p) continue;
+                const int n = TERMS == 3 ? 8 * g + 2 * q : 16 * h + 4 * g + q;
+                piece[h][q].v[0] = ld16(ring + r * 512 + 16 * (n ^ r));
+                if constexpr (TERMS == 3) piece[h][q].v[1] = ld16(ring + r * 512 + 16 * ((n + 1) ^ r));
+              }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                if (TERMS == 1 || h == p) piece[h][q].arrived();
+            __builtin_amdgcn_s_waitcnt(lgkmcnt0());  // read: the place may be filled again
+            asm volatile("" ::: "memory");
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) piece[h][q].terms(k0 + 128 * h + 32 * g + 8 * q < a.K, xf[u][h][q][s]);
+      }
+    if (DMA && !direct) {
+#pragma unroll
+      for (int d = 0; d < kRing; ++d) load_next(d);
+    }
+  }
+  int slot = 0;
+  for (int i = 0; i < mine; ++i) {
+    const int64_t n0 = (int64_t)(first + i * stride) * 16;
+    constexpr int CH = MS * TERMS >= 2 ? 2 : 4;  // independent sums: an MFMA waits for the one before in its own
+    floatx4 acc[CH][MS];
+#pragma unroll
+    for (int h = 0; h < CH; ++h)
+#pragma unroll
+      for (int s = 0; s < MS; ++s) acc[h][s] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (u < nu) {
+        const int kb = wave + waves * u;
+        u32x4 code[2];
+        uint32_t scale[2];  // NVFP4: the chunk's two blocks' bytes
+        if constexpr (DMA) {
+          __builtin_amdgcn_s_waitcnt(vmcnt_only(3 * (kRing - 1)));  // this step has arrived; the later ones may be on their way
+          asm volatile("" ::: "memory");
+          const uint8_t* from = ring + SLOT * slot;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int chunk = 4 * h + g;
+            code[h] = ld16(from + r * 128 + 16 * (chunk ^ (r >> 1)));
+            if constexpr (FMT == FP4_FMT_NVFP4) scale[h] = *reinterpret_cast<const uint16_t*>(from + 2048 + r * BLOCKS + 2 * chunk);
+            else scale[h] = from[2048 + r * BLOCKS + chunk];
+            asm volatile("" : "+v"(code[h]), "+v"(scale[h]));
+          }
+          __builtin_amdgcn_s_waitcnt(lgkmcnt0());  // read: the slot may be filled again
+          asm volatile("" ::: "memory");
+          load_next(slot);
+          slot = slot == kRing - 1 ? 0 : slot + 1;
+        } else {
+          const int64_t n = min(n0 + r, a.N - 1);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int k = kFewK * kb + 32 * (4 * h + g), k1 = k < a.K ? k : 0, k2 = k + 16 < a.K ? k + 16 : 0;
+            const uint8_t *c = wbase + n * wrow, *sc = sbase + n * srow;
+            const u32x2 lo = *reinterpret_cast<const u32x2*>(c + k1 / 2), hi = *reinterpret_cast<const u32x2*>(c + k2 / 2);
+            code[h] = u32x4{lo.x, lo.y, k + 16 < a.K ? hi.x : 0, k + 16 < a.K ? hi.y : 0};
+            if constexpr (FMT == FP4_FMT_NVFP4) scale[h] = sc[k1 / 16] | (k + 16 < a.K ? (uint32_t)sc[k2 / 16] << 8 : 0);
+            else scale[h] = sc[k1 / 32];
+          }
+        }
+        if (kFewK * (kb + 1) > a.K) {  // what is past the end of the rows counts 0
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (kFewK * kb + 32 * (4 * h + g) >= a.K) {
+              code[h] = u32x4{0, 0, 0, 0};
+              scale[h] = 0;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float s = block_scale<FMT>(FMT == FP4_FMT_NVFP4 ? (scale[h] >> (8 * (q >> 1))) & 0xFF : scale[h], pow2);
+            const uint32_t d = code[h][q];
+            const bf16x8_t wf = as_bf16x8(u32x4{decode2<FMT, 0>(d, s), decode2<FMT, 1>(d, s), decode2<FMT, 2>(d, s), decode2<FMT, 3>(d, s)});
+#pragma unroll
+            for (int t = 0; t < TERMS; ++t)
+#pragma unroll
+              for (int m = 0; m < MS; ++m) acc[q % CH][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[u][h][q][m][t], acc[q % CH][m], 0, 0, 0);
+          }
+      }
+    }
+    // [half][wave][16 MS rows][16 outputs], 16-byte pieces swizzled by the row; a half is written again two strips
+    // later, when the adding wave has met the barrier after reading it
+    float* part = reinterpret_cast<float*>(few_lds) + (i & 1) * waves * (MS * 256);
+#pragma unroll
+    for (int s = 0; s < MS; ++s) {
+      floatx4 v = acc[0][s] + acc[1][s];
+      if constexpr (CH == 4) v += acc[2][s] + acc[3][s];
+      *reinterpret_cast<floatx4*>(part + (wave * MS + s) * 256 + r * 16 + 4 * (g ^ ((r >> 1) & 3))) = v;
+    }
+    __builtin_amdgcn_s_waitcnt(lgkmcnt0());
+    asm volatile("s_barrier" ::: "memory");
+  }
+  if constexpr (DMA) __builtin_amdgcn_s_waitcnt(vmcnt_only(0));  // no DMA outlives the workgroup
+}
 
 // ------------------------------------------------------------ tiles
 
@@ -125,13 +408,15 @@ struct Fp4Tile {
   static constexpr int WB = GRAD ? 64 * WROW : BO * 128;
   static constexpr int CPT = BO * 4 / TH;                          // blocks of 16 codes a thread decodes a step
   static constexpr int XD = BM / 8 / WAVES;                        // DMA instructions of a wave a step
-  static constexpr int LDS = 2 * (XB + WB);
-  static_assert(CPT >= 1 && (BO * 4) % TH == 0 && (BM / 8) % WAVES == 0, "whole chunks");
+  static constexpr int YROW = BO * 2 + 16;                         // bytes of a row of bf16 results on their way out
+  static constexpr int LDS = 2 * (XB + WB) > BM * YROW ? 2 * (XB + WB) : BM * YROW;
+  static_assert(CPT == 1 || CPT == 2 || CPT == 4, "a thread's codes");
+  static_assert((BO * 4) % TH == 0 && (BM / 8) % WAVES == 0, "whole chunks");
   static_assert(LDS <= 160 * 1024, "LDS");
 };
 
-template <int FMT, bool GRAD, int WM, int WN, int MS, int NS>
-__global__ void __launch_bounds__(64 * WM * WN, 2) fp4_tile_kernel(Fp4MatmulArgs a, int mt, int ot) {
+template <int FMT, bool GRAD, int TERMS, int WM, int WN, int MS, int NS>
+__global__ void __launch_bounds__(64 * WM * WN, MS * NS > 32 ? 1 : 2) fp4_tile_kernel(Fp4MatmulArgs a, int mt, int ot) {
   using C = Fp4Tile<WM, WN, MS, NS, GRAD>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[C::LDS];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, r = lane & 15;
@@ -142,15 +427,13 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp4_tile_kernel(Fp4MatmulArgs
   if (t >= tiles) return;
   const int grp = t / (8 * ot), in = t - grp * 8 * ot, rows = min(8, mt - grp * 8);
   const int64_t m0 = (int64_t)(grp * 8 + in % rows) * C::BM, o0 = (int64_t)(in / rows) * C::BO, b = blockIdx.z;
-  const int64_t wrow = a.K / 2, srow = a.K / (FMT == FP4_FMT_NVFP4 ? 16 : 32);
-  const uint8_t* w = a.w + b * a.N * wrow;
-  const uint8_t* ws = a.ws + b * a.N * srow;
+  const uint8_t* w = a.w + b * a.N * (a.K / 2);
+  const uint8_t* ws = a.ws + b * a.N * (a.K / (FMT == FP4_FMT_NVFP4 ? 16 : 32));
   float pow2 = 1.0f, mant = 1.0f;
   if constexpr (FMT == FP4_FMT_NVFP4) split_scale(a.ts[b], pow2, mant);
 
   // x rows past the end repeat the last one; their results are not stored
   const int mlast = (int)min((int64_t)C::BM - 1, a.M - 1 - m0);
-  const int nsteps = a.steps * a.terms;
   uint32_t xoff[C::XD];
 #pragma unroll
   for (int j = 0; j < C::XD; ++j) {
@@ -164,39 +447,41 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp4_tile_kernel(Fp4MatmulArgs
     for (int j = 0; j < C::XD; ++j) dma_buffer(buf, xoff[j], 128 * step, lds + half * C::XB + (wave * C::XD + j) * 1024);
   };
   // this thread's blocks of 16 codes: consecutive ones of one row of the weight tile
-  constexpr int PER_ROW = GRAD ? C::BO / 16 : 4;
-  const int trow = tid * C::CPT / PER_ROW, tblk = tid * C::CPT % PER_ROW;
-  uint32_t code[C::CPT][2], scale[C::CPT];
-  auto load_w = [&](int step) __attribute__((always_inline)) {
-    const int64_t n = GRAD ? (int64_t)step * kBK + trow : o0 + trow;
-    const bool inside = n < a.N;
-    const int64_t nn = min(n, a.N - 1);
+  constexpr int PER_ROW = GRAD ? C::BO / 16 : 4, CPT = C::CPT;
+  const int trow = tid * CPT / PER_ROW, tblk = tid * CPT % PER_ROW;
+  // two steps' codes and scales as they were loaded: decoded a step after they arrive
+  u32x2 code[2][CPT];
+  uint32_t scale[2][CPT];
+  bool ok[2][CPT];
+  const uint32_t wrow = (uint32_t)(a.K / 2), srow = (uint32_t)(a.K / (FMT == FP4_FMT_NVFP4 ? 16 : 32));  // bytes of a row
+  const uint8_t* wbase = w + (GRAD ? o0 / 2 : o0 * wrow);
+  const uint8_t* sbase = ws + (GRAD ? o0 / (FMT == FP4_FMT_NVFP4 ? 16 : 32) : o0 * srow);
+  auto load_w = [&](int step, int set) __attribute__((always_inline)) {
+    // rows and blocks past the end: others of the same step are loaded instead, and not used
+    const int64_t first_row = GRAD ? (int64_t)step * kBK : o0, first_blk = GRAD ? o0 / 16 : (int64_t)step * 4;
+    const int rows_left = (int)min((int64_t)(GRAD ? kBK : C::BO), a.N - first_row), blks_left = (int)min((int64_t)PER_ROW, a.K / 16 - first_blk);
+    const uint8_t* wp = wbase + (GRAD ? first_row * wrow : (int64_t)step * 32);
+    const uint8_t* sp = sbase + (GRAD ? first_row * srow : (int64_t)step * (FMT == FP4_FMT_NVFP4 ? 4 : 2));
+    const uint32_t row = min(trow, rows_left - 1);
 #pragma unroll
-    for (int c = 0; c < C::CPT; ++c) {
-      const int64_t blk = (GRAD ? o0 / 16 : (int64_t)step * 4) + tblk + c;
-      const bool ok = inside && blk * 16 < a.K;
-      const int64_t bb = ok ? blk : 0;
-      const u32x2 v = *reinterpret_cast<const u32x2*>(w + nn * wrow + bb * 8);
-      const uint32_t s = ws[nn * srow + (FMT == FP4_FMT_NVFP4 ? bb : bb >> 1)];
-      // what is past the end counts 0 (an infinity or NaN there would reach sums whose x is 0)
-      code[c][0] = ok ? v.x : 0;
-      code[c][1] = ok ? v.y : 0;
-      scale[c] = ok ? s : 0;
+    for (int c = 0; c < CPT; ++c) {
+      ok[set][c] = trow < rows_left && tblk + c < blks_left;
+      const uint32_t at = tblk + c < blks_left ? tblk + c : 0;
+      code[set][c] = *reinterpret_cast<const u32x2*>(wp + (row * wrow + at * 8));
+      scale[set][c] = sp[row * srow + (FMT == FP4_FMT_NVFP4 ? at : at >> 1)];
     }
   };
   uint8_t* wlds = lds + 2 * C::XB;
-  auto decode_w = [&](int half) __attribute__((always_inline)) {
-#pragma unroll
-    for (int c = 0; c < C::CPT; ++c) {
-      uint32_t v[8];
-      decode16<FMT>(code[c][0], code[c][1], scale[c], pow2, v);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int piece = 2 * (tblk + c) + h;
-        uint8_t* to = wlds + half * C::WB + trow * C::WROW + 16 * (GRAD ? piece : piece ^ ((trow >> 1) & 7));
-        st16(to, u32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]});
-      }
-    }
+  // The `part`-th of 2 CPT parts of the decoding: 8 codes, one 16-byte piece of the tile.
+  float sc = 0.0f;
+  auto decode_w = [&](int set, int part, int half) __attribute__((always_inline)) {
+    const int c = part >> 1, h = part & 1;
+    // what is past the end counts 0 (an infinity or NaN there would reach sums whose x is 0)
+    if (h == 0) sc = block_scale<FMT>(ok[set][c] ? scale[set][c] : 0, pow2);
+    const uint32_t d = ok[set][c] ? code[set][c][h] : 0;
+    const int piece = 2 * (tblk + c) + h;
+    uint8_t* to = wlds + half * C::WB + trow * C::WROW + 16 * (GRAD ? piece : piece ^ ((trow >> 1) & 7));
+    st16(to, u32x4{decode2<FMT, 0>(d, sc), decode2<FMT, 1>(d, sc), decode2<FMT, 2>(d, sc), decode2<FMT, 3>(d, sc)});
   };
   auto read_w = [&](int half, int s, int j) __attribute__((always_inline)) {
     const uint8_t* from = wlds + half * C::WB;
@@ -218,72 +503,197 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp4_tile_kernel(Fp4MatmulArgs
   for (int i = 0; i < MS; ++i)
 #pragma unroll
     for (int s = 0; s < NS; ++s) acc[i][s] = floatx4{0.f, 0.f, 0.f, 0.f};
+  const int frag = r * 128 + 16 * (g ^ ((r >> 1) & 7));  // rows 16 apart lie alike
+  // One step: its products of term `term` of x, and on the way the next step's x and weights.  P: the step's parity.
+  auto body = [&](int step, auto P_, auto TERM_) __attribute__((always_inline)) {
+    constexpr int P = decltype(P_)::value, TERM = decltype(TERM_)::value, HALF = (P + TERM) & 1;
+    // This step's x has arrived and its weights are written.
+    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0(0));
+    asm volatile("s_barrier" ::: "memory");
+    // (the last step asks for itself again)
+    load_x(min(TERM + 1 == TERMS ? step + 1 : step, a.steps - 1), TERM + 1 == TERMS ? 0 : TERM + 1, HALF ^ 1);
+    if (TERM == 0) load_w(min(step + 2, a.steps - 1), P);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    const uint8_t* xr = lds + HALF * C::XB + wm * (16 * MS * 128);
+    bf16x8_t wf[2][NS], xf[3];
+    auto read_x = [&](int i) __attribute__((always_inline)) { xf[i % 3] = as_bf16x8(ld16(xr + 2048 * (i % MS) + (frag ^ (64 * (i / MS))))); };
+#pragma unroll
+    for (int s = 0; s < NS; ++s) wf[0][s] = read_w(P, s, 0);
+    read_x(0);
+    read_x(1);
+    // The order is pinned: fragments are read two groups of MFMAs ahead, and the next
+    // step's weights decoded between the MFMAs.
+#pragma unroll
+    for (int i = 0; i < 2 * MS; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (i + 2 < 2 * MS) read_x(i + 2);
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+        if (i == (s * MS) / NS) wf[1][s] = read_w(P, s, 1);
+      if (TERM == 0) {
+#pragma unroll
+        for (int part = 0; part < 2 * CPT; ++part)
+          if (i == (part * 2 * MS) / (2 * CPT)) decode_w(P ^ 1, part, P ^ 1);
+      }
+#pragma unroll
+      for (int s = 0; s < NS; ++s) acc[i % MS][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[i / MS][s], xf[i % 3], acc[i % MS][s], 0, 0, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto step_of = [&](int step, auto P_) __attribute__((always_inline)) {
+    body(step, P_, std::integral_constant<int, 0>());
+    if constexpr (TERMS == 3) {
+      body(step, P_, std::integral_constant<int, 1>());
+      body(step, P_, std::integral_constant<int, 2>());
+    }
+  };
+  load_w(0, 0);
   load_x(0, 0, 0);
-  load_w(0);
-  decode_w(0);
-  load_w(min(1, a.steps - 1));
-  int step = 0, term = 0;
-  for (int i = 0; i < nsteps; ++i) {
-    __builtin_amdgcn_s_waitcnt(0);  // this step's x has arrived and its weights are written
-    __syncthreads();
-    const int next_term = term + 1 == a.terms ? 0 : term + 1, next_step = next_term ? step : step + 1;
-    if (i + 1 < nsteps) load_x(next_step, next_term, (i + 1) & 1);
-    if (term == 0) {
-      decode_w((step + 1) & 1);
-      load_w(min(step + 2, a.steps - 1));
-    }
-    const uint8_t* xr = lds + (i & 1) * C::XB;
+  load_w(min(1, a.steps - 1), 1);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      bf16x8_t wf[NS];
-#pragma unroll
-      for (int s = 0; s < NS; ++s) wf[s] = read_w(step & 1, s, j);
-#pragma unroll
-      for (int q = 0; q < MS; ++q) {
-        const int row = wm * 16 * MS + 16 * q + r;
-        const bf16x8_t xf = as_bf16x8(ld16(xr + row * 128 + 16 * ((4 * j + g) ^ ((row >> 1) & 7))));
-#pragma unroll
-        for (int s = 0; s < NS; ++s) acc[q][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[s], xf, acc[q][s], 0, 0, 0);
-      }
-    }
-    term = next_term;
-    step = next_step;
+  for (int part = 0; part < 2 * CPT; ++part) decode_w(0, part, 0);
+  for (int step = 0; step < a.steps; step += 2) {
+    step_of(step, std::integral_constant<int, 0>());
+    if (step + 1 < a.steps) step_of(step + 1, std::integral_constant<int, 1>());
   }
+  __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0(0));  // no DMA outlives the workgroup
+  if (a.y_f32) {
+    float* y = static_cast<float*>(a.y) + (b * a.M + m0) * a.O + o0;
+    const bool vec = a.O % 4 == 0 && (uintptr_t)a.y % 16 == 0;
 #pragma unroll
-  for (int q = 0; q < MS; ++q) {
-    const int64_t m = m0 + wm * 16 * MS + 16 * q + r;
-    if (m >= a.M) continue;
+    for (int q = 0; q < MS; ++q) {
+      const int m = wm * 16 * MS + 16 * q + r;
+      if (m > mlast) continue;
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
+      for (int s = 0; s < NS; ++s) {
+        const int o = wn * 16 * NS + 16 * s + 4 * g;
+        const floatx4 v = acc[q][s] * mant;
+        if (vec) {
+          if (o0 + o < a.O) *reinterpret_cast<floatx4*>(y + m * a.O + o) = v;
+        } else {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int64_t o = o0 + wn * 16 * NS + 16 * s + 4 * g + c;
-        if (o >= a.O) continue;
-        const float v = acc[q][s][c] * mant;
-        const int64_t at = (b * a.M + m) * a.O + o;
-        if (a.y_f32) static_cast<float*>(a.y)[at] = v;
-        else static_cast<uint16_t*>(a.y)[at] = __builtin_bit_cast(uint16_t, (__bf16)v);
+          for (int c = 0; c < 4; ++c)
+            if (o0 + o + c < a.O) y[m * a.O + o + c] = v[c];
+        }
       }
+    }
+    return;
+  }
+  // bf16 results are turned in LDS, so that consecutive lanes store consecutive 16 bytes of a row
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < MS; ++q)
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const bf16x2_t lo{(__bf16)(acc[q][s][0] * mant), (__bf16)(acc[q][s][1] * mant)}, hi{(__bf16)(acc[q][s][2] * mant), (__bf16)(acc[q][s][3] * mant)};
+      *reinterpret_cast<u32x2*>(lds + (wm * 16 * MS + 16 * q + r) * C::YROW + (wn * 16 * NS + 16 * s + 4 * g) * 2) =
+          u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+    }
+  __syncthreads();
+  uint16_t* y = static_cast<uint16_t*>(a.y) + (b * a.M + m0) * a.O + o0;
+  const bool vec = a.O % 8 == 0 && (uintptr_t)a.y % 16 == 0;
+  constexpr int PIECES = C::BO / 8;
+#pragma unroll 4
+  for (int q = tid; q < C::BM * PIECES; q += C::TH) {
+    const int m = q / PIECES, o = q % PIECES * 8;
+    if (m > mlast || o0 + o >= a.O) continue;
+    const u32x4 v = ld16(lds + m * C::YROW + o * 2);
+    if (vec) {
+      st16(y + m * a.O + o, v);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (o0 + o + c < a.O) y[m * a.O + o + c] = (uint16_t)(v[c >> 1] >> (16 * (c & 1)));
+    }
   }
 }
 
 constexpr int64_t kMost = 0xFFFFFFFF;  // threads of a launch along x
 constexpr int64_t kMostMatrices = 65535;
 
-template <int FMT, bool GRAD>
-static int launch_fp4(const Fp4MatmulArgs& a, int64_t batch, hipStream_t st) {
-  using C = Fp4Tile<2, 2, 2, 2, GRAD>;
+template <int FMT, bool GRAD, int TERMS, int WM, int WN, int MS, int NS>
+static int launch_tile(const Fp4MatmulArgs& a, int64_t batch, hipStream_t st) {
+  using C = Fp4Tile<WM, WN, MS, NS, GRAD>;
   const int64_t mt = (a.M + C::BM - 1) / C::BM, ot = (a.O + C::BO - 1) / C::BO, grid = (mt * ot + 7) / 8 * 8;
   if (grid * C::TH > kMost) return fail(FP4_ERR_UNSUPPORTED, "fp4_matmul: too many rows or outputs");
-  hipLaunchKernelGGL((fp4_tile_kernel<FMT, GRAD, 2, 2, 2, 2>), dim3((unsigned)grid, 1, (unsigned)batch), dim3(C::TH), 0, st, a, (int)mt, (int)ot);
+  hipLaunchKernelGGL((fp4_tile_kernel<FMT, GRAD, TERMS, WM, WN, MS, NS>), dim3((unsigned)grid, 1, (unsigned)batch), dim3(C::TH), 0, st, a, (int)mt, (int)ot);
   return check_launch("fp4_matmul");
+}
+
+// The few-rows kernel's waves and steps a wave for K (0 waves: K is too long).
+struct FewShape {
+  int waves, steps;
+};
+static FewShape few_shape(int64_t k, int terms, int ms) {
+  const int64_t ks = (k + kFewK - 1) / kFewK, most = terms == 3 ? 2 : 4 / ms;  // x of a wave: 128 registers, f32 192
+  for (int u = 1; u <= most; u *= 2)
+    if ((ks + u - 1) / u <= few_waves(ms, u, terms)) return {(int)((ks + u - 1) / u), u};
+  return {0, 0};
+}
+
+template <int FMT, int TERMS, int MS, int U, bool DMA>
+static int launch_few(const Fp4FewArgs& a, int64_t batch, int waves, hipStream_t st) {
+  static std::atomic<uint64_t> raised{0};
+  const int lds = waves * (2 * MS * 1024 + (DMA ? kRing * kSlot : 8192));
+  void (*kernel)(Fp4FewArgs) = &fp4_few_kernel<FMT, TERMS, MS, U, DMA>;
+  FP4_CHECK(raise_dyn_lds(reinterpret_cast<const void*>(kernel), 160 * 1024, raised));
+  const int64_t strips = (a.N + 15) / 16, blocks = (a.M + 16 * MS - 1) / (16 * MS);
+  // as many workgroups as stay on the card together, then the strips evenly
+  const int64_t room = std::max<int64_t>(1, std::min<int64_t>(160 * 1024 / lds, 4 * few_per_simd(MS, U, TERMS) / (waves + 1))) * device_cu_count();
+  const int64_t each = std::max<int64_t>(1, (strips * blocks * batch + room - 1) / room), wgs = (strips + each - 1) / each;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)wgs, (unsigned)blocks, (unsigned)batch), dim3(64 * (waves + 1)), lds, st, a);
+  return check_launch("fp4_matmul");
+}
+
+template <int FMT, int TERMS, int MS, int U>
+static int launch_few_dma(const Fp4FewArgs& a, int64_t batch, int waves, hipStream_t st) {
+  // whole pieces of DMA: 16 bytes of codes and 4 of scales
+  const bool whole = a.K % (FMT == FP4_FMT_NVFP4 ? 64 : 128) == 0 && (uintptr_t)a.w % 16 == 0 && (uintptr_t)a.ws % 4 == 0;
+  return whole ? launch_few<FMT, TERMS, MS, U, true>(a, batch, waves, st) : launch_few<FMT, TERMS, MS, U, false>(a, batch, waves, st);
+}
+
+template <int FMT>
+static int launch_few_rows(const Fp4FewArgs& a, int64_t batch, int terms, int ms, hipStream_t st) {
+  const FewShape f = few_shape(a.K, terms, ms);
+  if (terms == 3) return f.steps == 1 ? launch_few_dma<FMT, 3, 1, 1>(a, batch, f.waves, st) : launch_few_dma<FMT, 3, 1, 2>(a, batch, f.waves, st);
+  if (ms == 1) {
+    if (f.steps == 1) return launch_few_dma<FMT, 1, 1, 1>(a, batch, f.waves, st);
+    if (f.steps == 2) return launch_few_dma<FMT, 1, 1, 2>(a, batch, f.waves, st);
+    return launch_few_dma<FMT, 1, 1, 4>(a, batch, f.waves, st);
+  }
+  if (ms == 2) {
+    if (f.steps == 1) return launch_few_dma<FMT, 1, 2, 1>(a, batch, f.waves, st);
+    return launch_few_dma<FMT, 1, 2, 2>(a, batch, f.waves, st);
+  }
+  return launch_few_dma<FMT, 1, 4, 1>(a, batch, f.waves, st);
+}
+
+#ifndef FP4_CFG
+#define FP4_CFG 2, 2, 2, 2
+#endif
+template <int FMT, bool GRAD>
+static int launch_fp4(const Fp4MatmulArgs& a, int64_t batch, hipStream_t st) {
+  return a.terms == 1 ? launch_tile<FMT, GRAD, 1, FP4_CFG>(a, batch, st) : launch_tile<FMT, GRAD, 3, FP4_CFG>(a, batch, st);
 }
 
 // ------------------------------------------------------------ the calls
 
+// The few-rows kernel's blocks of 16 rows for a product, 0 where tiles are to take it.
+static int few_blocks(int64_t m, int64_t n, int64_t k, int terms) {
+#ifdef FP4_FEWM
+  if (m > FP4_FEWM) return 0;
+#endif
+  if (m > (terms == 3 ? 128 : 64)) return 0;
+  for (int ms = terms == 3 || m <= 16 ? 1 : m <= 32 ? 2 : 4; ms > 0; ms /= 2)
+    if (few_shape(k, terms, ms).waves) return ms;
+  return 0;
+}
+
 struct Fp4Plan {
   int64_t sum, out, ld, terms;  // length of the sum, outputs, row stride and terms of x as the kernels read it
   bool rows;                    // x is copied (split, padded) first
+  int few;                      // the few-rows kernel's blocks of 16 rows, or 0
   size_t bytes;
 };
 
@@ -298,14 +708,15 @@ static int plan_fp4(int w_fmt, int x_dtype, bool grad, int64_t batch, int64_t m,
   if (batch >= most || m >= most || n >= most || k >= most) return fail(FP4_ERR_UNSUPPORTED, "fp4_matmul: a dimension of 2^31 or more");
   p.sum = grad ? n : k;
   p.out = grad ? k : n;
-  if (p.sum > (int64_t)1 << 22) return fail(FP4_ERR_UNSUPPORTED, "fp4_matmul: sums of more than 2^22 products");  // 32-bit offsets inside a tile
+  if (p.sum > (int64_t)1 << 22 || k > (int64_t)1 << 26) return fail(FP4_ERR_UNSUPPORTED, "fp4_matmul: sums of more than 2^22 products or k above 2^26");  // 32-bit offsets inside a tile
   if (batch > kMostMatrices) return fail(FP4_ERR_UNSUPPORTED, "fp4_matmul: more than %lld matrices", (long long)kMostMatrices);
   const double elems = 0x1p46;
   if ((double)batch * m * k > elems || (double)batch * n * k > elems || (double)batch * m * n > elems)
     return fail(FP4_ERR_UNSUPPORTED, "fp4_matmul: an operand of more than 2^46 values");
   p.ld = (p.sum + kBK - 1) / kBK * kBK;
   p.terms = x_dtype == FP4_DT_F32 ? 3 : 1;
-  p.rows = p.terms > 1 || p.ld != p.sum;
+  p.few = grad ? 0 : few_blocks(m, n, k, (int)p.terms);
+  p.rows = !p.few && (p.terms > 1 || p.ld != p.sum);
   p.bytes = p.rows ? (size_t)(2 * p.terms) * (size_t)(batch * m * p.ld) : 0;
   if (p.rows && batch * m * (p.ld / 8) > kMost) return fail(FP4_ERR_UNSUPPORTED, "fp4_matmul: too many rows");
   return FP4_OK;
@@ -319,7 +730,7 @@ static int run_fp4(int w_fmt, const void* x, int x_dtype, bool grad, const uint8
   if (batch == 0 || m == 0 || p.out == 0) return FP4_OK;
   if (p.sum == 0) return fail(FP4_ERR_SHAPE, "fp4_matmul: sums of no products");
   if (!x || !w || !w_scales || !y || (w_fmt == FP4_FMT_NVFP4 && !tensor_scale)) return fail(FP4_ERR_INVALID_ARG, "fp4_matmul: null pointer");
-  if ((uintptr_t)x % (p.rows ? x_dtype == FP4_DT_F32 ? 4 : 2 : 16) || (uintptr_t)w % 8 || (uintptr_t)tensor_scale % 4 ||
+  if ((uintptr_t)x % (grad && p.rows ? x_dtype == FP4_DT_F32 ? 4 : 2 : 16) || (uintptr_t)w % 8 || (uintptr_t)tensor_scale % 4 ||
       (uintptr_t)y % (y_dtype == FP4_DT_F32 ? 4 : 2))
     return fail(FP4_ERR_INVALID_ARG, "fp4_matmul: misaligned pointer");
   if (p.bytes) {
@@ -327,6 +738,10 @@ static int run_fp4(int w_fmt, const void* x, int x_dtype, bool grad, const uint8
     if ((uintptr_t)workspace % 16) return fail(FP4_ERR_INVALID_ARG, "fp4_matmul: misaligned workspace");
   }
   hipStream_t st = as_stream(stream);
+  if (p.few) {
+    const Fp4FewArgs a{x, w, static_cast<const uint8_t*>(w_scales), tensor_scale, y, m, n, (int)k, y_dtype == FP4_DT_F32};
+    return w_fmt == FP4_FMT_NVFP4 ? launch_few_rows<FP4_FMT_NVFP4>(a, batch, (int)p.terms, p.few, st) : launch_few_rows<FP4_FMT_MXFP4>(a, batch, (int)p.terms, p.few, st);
+  }
   if (p.rows) {
     const int64_t rows = batch * m;
     uint16_t* to = static_cast<uint16_t*>(workspace);

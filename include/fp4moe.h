@@ -470,8 +470,7 @@ int fp8_block_matmul(const void* x, int x_dtype, const float* x_scales, const ui
  * buffer is contiguous; any m >= 0 and n >= 0.  A result does not depend on other
  * rows of x or other matrices' values, and repeats bit for bit.
  * Errors: k % B, k == 0 -> FP4_ERR_SHAPE; unknown format or dtype, null or
- * misaligned pointer (x: 16 bytes for bf16 with k % 64 == 0, else its type's; w: 8)
- * -> FP4_ERR_INVALID_ARG; formats other than NVFP4 and MXFP4, more than 65535
+ * misaligned pointer (x: 16 bytes; w: 8) -> FP4_ERR_INVALID_ARG; formats other than NVFP4 and MXFP4, more than 65535
  * matrices, a dimension of 2^31, k above 2^22, more rows or outputs than a launch
  * has threads for -> FP4_ERR_UNSUPPORTED; FP4_ERR_WORKSPACE.  Stream-ordered,
  * asynchronous.
@@ -486,8 +485,8 @@ int fp4_matmul(int w_fmt, const void* x, int x_dtype, const uint8_t* w, const vo
  *   dx[m][k] = S sum_n dy[m][n] g[n][k] s[n][k/B],
  * for the training of what lies below a frozen 4-bit layer (the weights, being
  * codes, have no gradient).  dy bf16 or f32 [batch, m, n], dx bf16 or f32 [batch,
- * m, k]; all else as fp4_matmul, n taking k's place in what it says of lengths and
- * alignment of x: n == 0 -> FP4_ERR_SHAPE, n above 2^22 -> FP4_ERR_UNSUPPORTED, dy
+ * m, k]; all else as fp4_matmul, n taking k's place in what it says of lengths:
+ * n == 0 -> FP4_ERR_SHAPE, n above 2^22 or k above 2^26 -> FP4_ERR_UNSUPPORTED, dy
  * aligned to 16 bytes for bf16 with n % 64 == 0, else to its type.
  */
 int fp4_matmul_grad_workspace_size(int w_fmt, int dy_dtype, int64_t batch, int64_t m, int64_t n, int64_t k, size_t* bytes);
