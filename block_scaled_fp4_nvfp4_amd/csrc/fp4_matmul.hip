@@ -16,6 +16,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "fp4_device.h"
@@ -39,6 +40,8 @@ struct Fp4MatmulArgs {
   int64_t ld, term;    // x's row and term strides
   int64_t M, N, K, O;  // O: outputs (N, or K for the gradient)
   int steps, terms, y_f32;
+  int each;            // steps of a workgroup
+  float* parts;        // [splits][batch][M][O], where several workgroups share a tile's steps
 };
 
 // ------------------------------------------------------------ operands
@@ -393,6 +396,40 @@ __global__ void __launch_bounds__(64 * (few_waves(MS, U, TERMS) + 1), few_per_si
 
 // ------------------------------------------------------------ tiles
 
+// NS fragments of 16 columns by 32 rows from a tile that lies row by row (ROW bytes each): the transposing reads, in one
+// block with their wait, because the compiler lets such a read wait for all DMA that is on its way.
+template <int NS, int ROW>
+__device__ __forceinline__ void read_turned(const uint8_t* p, bf16x8_t (&f)[NS]) {
+  const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)p;
+  u32x2 v[2 * NS];
+  if constexpr (NS == 2) {
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %4\n"
+        "ds_read_b64_tr_b16 %1, %4 offset:%5\n"
+        "ds_read_b64_tr_b16 %2, %4 offset:32\n"
+        "ds_read_b64_tr_b16 %3, %4 offset:%6\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+        : "v"(at), "n"(4 * ROW), "n"(4 * ROW + 32));
+  } else {
+    static_assert(NS == 4, "two or four fragments");
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %8\n"
+        "ds_read_b64_tr_b16 %1, %8 offset:%9\n"
+        "ds_read_b64_tr_b16 %2, %8 offset:32\n"
+        "ds_read_b64_tr_b16 %3, %8 offset:%10\n"
+        "ds_read_b64_tr_b16 %4, %8 offset:64\n"
+        "ds_read_b64_tr_b16 %5, %8 offset:%11\n"
+        "ds_read_b64_tr_b16 %6, %8 offset:96\n"
+        "ds_read_b64_tr_b16 %7, %8 offset:%12\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7])
+        : "v"(at), "n"(4 * ROW), "n"(4 * ROW + 32), "n"(4 * ROW + 64), "n"(4 * ROW + 96));
+  }
+#pragma unroll
+  for (int s = 0; s < NS; ++s) f[s] = as_bf16x8(u32x4{v[2 * s].x, v[2 * s].y, v[2 * s + 1].x, v[2 * s + 1].y});
+}
+
 // Tile of BM rows by BO outputs per workgroup of WM x WN waves, each owning 16 MS
 // rows and 16 NS outputs.  Steps of 64 products: x's part comes by DMA, the
 // weights' codes through registers, decoded on their way to LDS, both into the
@@ -400,24 +437,25 @@ __global__ void __launch_bounds__(64 * (few_waves(MS, U, TERMS) + 1), few_per_si
 // the MFMA, so that a lane's four sums are four consecutive outputs of one row.
 // The gradient sums over W's rows: its tile lies in LDS as W does and is turned by
 // the transposing reads.
-template <int WM, int WN, int MS, int NS, bool GRAD>
+template <int R, int WM, int WN, int MS, int NS, bool GRAD>
 struct Fp4Tile {
   static constexpr int WAVES = WM * WN, TH = 64 * WAVES, BM = 16 * MS * WM, BO = 16 * NS * WN;
   static constexpr int XB = BM * 128;                              // bytes of x a step
   static constexpr int WROW = GRAD ? BO * 2 + 32 : 128;            // bytes of a row of the weight tile
   static constexpr int WB = GRAD ? 64 * WROW : BO * 128;
   static constexpr int CPT = BO * 4 / TH;                          // blocks of 16 codes a thread decodes a step
-  static constexpr int XD = BM / 8 / WAVES;                        // DMA instructions of a wave a step
+  static constexpr int XD = BM / 8 < WAVES ? 1 : BM / 8 / WAVES;   // DMA instructions of a wave a step
   static constexpr int YROW = BO * 2 + 16;                         // bytes of a row of bf16 results on their way out
-  static constexpr int LDS = 2 * (XB + WB) > BM * YROW ? 2 * (XB + WB) : BM * YROW;
+  static constexpr int LDS = R * XB + 2 * WB > BM * YROW ? R * XB + 2 * WB : BM * YROW;
   static_assert(CPT == 1 || CPT == 2 || CPT == 4, "a thread's codes");
-  static_assert((BO * 4) % TH == 0 && (BM / 8) % WAVES == 0, "whole chunks");
+  static_assert((BO * 4) % TH == 0 && ((BM / 8) % WAVES == 0 || WAVES % (BM / 8) == 0), "whole chunks");
+  static_assert(R == 2 || R == 4, "the steps that the loop has written out");
   static_assert(LDS <= 160 * 1024, "LDS");
 };
 
-template <int FMT, bool GRAD, int TERMS, int WM, int WN, int MS, int NS>
-__global__ void __launch_bounds__(64 * WM * WN, MS * NS > 32 ? 1 : 2) fp4_tile_kernel(Fp4MatmulArgs a, int mt, int ot) {
-  using C = Fp4Tile<WM, WN, MS, NS, GRAD>;
+template <int FMT, bool GRAD, int TERMS, int R, int WM, int WN, int MS, int NS>
+__global__ void __launch_bounds__(64 * WM * WN, 2) fp4_tile_kernel(Fp4MatmulArgs a, int mt, int ot) {
+  using C = Fp4Tile<R, WM, WN, MS, NS, GRAD>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[C::LDS];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, r = lane & 15;
   const int wm = wave / WN, wn = wave % WN;
@@ -437,22 +475,23 @@ __global__ void __launch_bounds__(64 * WM * WN, MS * NS > 32 ? 1 : 2) fp4_tile_k
   uint32_t xoff[C::XD];
 #pragma unroll
   for (int j = 0; j < C::XD; ++j) {
-    const int row = wave * 8 * C::XD + 8 * j + (lane >> 3);
+    const int row = 8 * ((wave * C::XD + j) % (C::BM / 8)) + (lane >> 3);
     xoff[j] = (uint32_t)min(row, mlast) * (uint32_t)(a.ld * 2) + 16 * ((lane & 7) ^ ((row >> 1) & 7));
   }
   const uint16_t* xbase = a.x + (b * a.M + m0) * a.ld;
-  auto load_x = [&](int step, int term, int half) __attribute__((always_inline)) {
+  const int first = blockIdx.y * a.each, last = min(a.steps, first + a.each) - 1;  // this workgroup's steps
+  auto load_x = [&](int step, int term, int slot) __attribute__((always_inline)) {
     const auto buf = buffer_of(xbase + term * a.term, (uint32_t)(mlast + 1) * (uint32_t)(a.ld * 2));
 #pragma unroll
-    for (int j = 0; j < C::XD; ++j) dma_buffer(buf, xoff[j], 128 * step, lds + half * C::XB + (wave * C::XD + j) * 1024);
+    for (int j = 0; j < C::XD; ++j) dma_buffer(buf, xoff[j], 128 * step, lds + slot * C::XB + ((wave * C::XD + j) % (C::BM / 8)) * 1024);
   };
   // this thread's blocks of 16 codes: consecutive ones of one row of the weight tile
   constexpr int PER_ROW = GRAD ? C::BO / 16 : 4, CPT = C::CPT;
   const int trow = tid * CPT / PER_ROW, tblk = tid * CPT % PER_ROW;
-  // two steps' codes and scales as they were loaded: decoded a step after they arrive
-  u32x2 code[2][CPT];
-  uint32_t scale[2][CPT];
-  bool ok[2][CPT];
+  // R steps' codes and scales as they were loaded
+  u32x2 code[R][CPT];
+  uint32_t scale[R][CPT];
+  uint32_t ok[R][CPT];  // all bits of what is inside
   const uint32_t wrow = (uint32_t)(a.K / 2), srow = (uint32_t)(a.K / (FMT == FP4_FMT_NVFP4 ? 16 : 32));  // bytes of a row
   const uint8_t* wbase = w + (GRAD ? o0 / 2 : o0 * wrow);
   const uint8_t* sbase = ws + (GRAD ? o0 / (FMT == FP4_FMT_NVFP4 ? 16 : 32) : o0 * srow);
@@ -465,37 +504,36 @@ __global__ void __launch_bounds__(64 * WM * WN, MS * NS > 32 ? 1 : 2) fp4_tile_k
     const uint32_t row = min(trow, rows_left - 1);
 #pragma unroll
     for (int c = 0; c < CPT; ++c) {
-      ok[set][c] = trow < rows_left && tblk + c < blks_left;
+      ok[set][c] = trow < rows_left && tblk + c < blks_left ? 0xFFFFFFFFu : 0;
       const uint32_t at = tblk + c < blks_left ? tblk + c : 0;
       code[set][c] = *reinterpret_cast<const u32x2*>(wp + (row * wrow + at * 8));
       scale[set][c] = sp[row * srow + (FMT == FP4_FMT_NVFP4 ? at : at >> 1)];
     }
   };
-  uint8_t* wlds = lds + 2 * C::XB;
+  uint8_t* wlds = lds + R * C::XB;
   // The `part`-th of 2 CPT parts of the decoding: 8 codes, one 16-byte piece of the tile.
   float sc = 0.0f;
   auto decode_w = [&](int set, int part, int half) __attribute__((always_inline)) {
     const int c = part >> 1, h = part & 1;
     // what is past the end counts 0 (an infinity or NaN there would reach sums whose x is 0)
-    if (h == 0) sc = block_scale<FMT>(ok[set][c] ? scale[set][c] : 0, pow2);
-    const uint32_t d = ok[set][c] ? code[set][c][h] : 0;
+    if (h == 0) sc = block_scale<FMT>(scale[set][c] & ok[set][c], pow2);
+    const uint32_t d = code[set][c][h] & ok[set][c];
     const int piece = 2 * (tblk + c) + h;
     uint8_t* to = wlds + half * C::WB + trow * C::WROW + 16 * (GRAD ? piece : piece ^ ((trow >> 1) & 7));
     st16(to, u32x4{decode2<FMT, 0>(d, sc), decode2<FMT, 1>(d, sc), decode2<FMT, 2>(d, sc), decode2<FMT, 3>(d, sc)});
   };
-  auto read_w = [&](int half, int s, int j) __attribute__((always_inline)) {
+  // The weights' fragments of half a step.
+  auto read_w = [&](int half, int j, bf16x8_t (&wf)[NS]) __attribute__((always_inline)) {
     const uint8_t* from = wlds + half * C::WB;
     if constexpr (GRAD) {
       // lane (g, r) names 4 values of row 32 j + 8 g + r / 4 and gets column r of the rows 32 j + 8 g .. + 3 (then + 4 .. + 7)
-      const uint8_t* p = from + (32 * j + 8 * g + (r >> 2)) * C::WROW + (wn * 16 * NS + 16 * s + 4 * (r & 3)) * 2;
-      typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
-      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * C::WROW));
-      const u32x2 l = __builtin_bit_cast(u32x2, lo), h = __builtin_bit_cast(u32x2, hi);
-      return as_bf16x8(u32x4{l.x, l.y, h.x, h.y});
+      read_turned<NS, C::WROW>(from + (32 * j + 8 * g + (r >> 2)) * C::WROW + (wn * 16 * NS + 4 * (r & 3)) * 2, wf);
     } else {
-      const int row = wn * 16 * NS + 16 * s + r;
-      return as_bf16x8(ld16(from + row * 128 + 16 * ((4 * j + g) ^ ((row >> 1) & 7))));
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const int row = wn * 16 * NS + 16 * s + r;
+        wf[s] = as_bf16x8(ld16(from + row * 128 + 16 * ((4 * j + g) ^ ((row >> 1) & 7))));
+      }
     }
   };
   floatx4 acc[MS][NS];
@@ -504,22 +542,30 @@ __global__ void __launch_bounds__(64 * WM * WN, MS * NS > 32 ? 1 : 2) fp4_tile_k
 #pragma unroll
     for (int s = 0; s < NS; ++s) acc[i][s] = floatx4{0.f, 0.f, 0.f, 0.f};
   const int frag = r * 128 + 16 * (g ^ ((r >> 1) & 7));  // rows 16 apart lie alike
-  // One step: its products of term `term` of x, and on the way the next step's x and weights.  P: the step's parity.
+  int slot = 0;                                   // of this term's x
+  int lstep = first, lterm = 0, lslot = 0;        // the next x to load
+  auto load_next_x = [&]() __attribute__((always_inline)) {
+    load_x(min(lstep, last), lterm, lslot);  // past the end the last step again
+    lslot = lslot == R - 1 ? 0 : lslot + 1;
+    if (++lterm == TERMS) { lterm = 0; ++lstep; }
+  };
+  // One step's products of one term of x, and on the way later steps' x and weights.  P: the set of the step's codes.
   auto body = [&](int step, auto P_, auto TERM_) __attribute__((always_inline)) {
-    constexpr int P = decltype(P_)::value, TERM = decltype(TERM_)::value, HALF = (P + TERM) & 1;
-    // This step's x has arrived and its weights are written.
-    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0(0));
+    constexpr int P = decltype(P_)::value, TERM = decltype(TERM_)::value, NEXT = (P + 1) % R;
+    const int half = (step - first) & 1;
+    // This term's x has arrived and its weights are written; what was asked for after that x may still be on its
+    // way: its DMA, and of a step's codes and scales two loads at least, however the compiler merges them (none is
+    // dropped, since all are used at the end, and none passes a barrier).
+    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0((R - 2) * (C::XD + (TERMS == 1 ? 2 : 0))));
     asm volatile("s_barrier" ::: "memory");
-    // (the last step asks for itself again)
-    load_x(min(TERM + 1 == TERMS ? step + 1 : step, a.steps - 1), TERM + 1 == TERMS ? 0 : TERM + 1, HALF ^ 1);
-    if (TERM == 0) load_w(min(step + 2, a.steps - 1), P);
+    if (TERM == 0) load_w(min(step + R, last), P);
+    load_next_x();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    const uint8_t* xr = lds + HALF * C::XB + wm * (16 * MS * 128);
+    const uint8_t* xr = lds + slot * C::XB + wm * (16 * MS * 128);
     bf16x8_t wf[2][NS], xf[3];
     auto read_x = [&](int i) __attribute__((always_inline)) { xf[i % 3] = as_bf16x8(ld16(xr + 2048 * (i % MS) + (frag ^ (64 * (i / MS))))); };
-#pragma unroll
-    for (int s = 0; s < NS; ++s) wf[0][s] = read_w(P, s, 0);
+    read_w(half, 0, wf[0]);
     read_x(0);
     read_x(1);
     // The order is pinned: fragments are read two groups of MFMAs ahead, and the next
@@ -528,18 +574,17 @@ __global__ void __launch_bounds__(64 * WM * WN, MS * NS > 32 ? 1 : 2) fp4_tile_k
     for (int i = 0; i < 2 * MS; ++i) {
       __builtin_amdgcn_sched_barrier(0);
       if (i + 2 < 2 * MS) read_x(i + 2);
-#pragma unroll
-      for (int s = 0; s < NS; ++s)
-        if (i == (s * MS) / NS) wf[1][s] = read_w(P, s, 1);
+      if (i == MS - 1) read_w(half, 1, wf[1]);
       if (TERM == 0) {
 #pragma unroll
         for (int part = 0; part < 2 * CPT; ++part)
-          if (i == (part * 2 * MS) / (2 * CPT)) decode_w(P ^ 1, part, P ^ 1);
+          if (i == (part * 2 * MS) / (2 * CPT)) decode_w(NEXT, part, half ^ 1);
       }
 #pragma unroll
       for (int s = 0; s < NS; ++s) acc[i % MS][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[i / MS][s], xf[i % 3], acc[i % MS][s], 0, 0, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
+    slot = slot == R - 1 ? 0 : slot + 1;
   };
   auto step_of = [&](int step, auto P_) __attribute__((always_inline)) {
     body(step, P_, std::integral_constant<int, 0>());
@@ -548,19 +593,36 @@ __global__ void __launch_bounds__(64 * WM * WN, MS * NS > 32 ? 1 : 2) fp4_tile_k
       body(step, P_, std::integral_constant<int, 2>());
     }
   };
-  load_w(0, 0);
-  load_x(0, 0, 0);
-  load_w(min(1, a.steps - 1), 1);
+  load_w(first, 0);
+#pragma unroll
+  for (int i = 0; i < R - 1; ++i) {  // in groups as the steps', which the waits count on
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    load_w(min(first + 1 + i, last), i + 1);
+    load_next_x();
+  }
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int part = 0; part < 2 * CPT; ++part) decode_w(0, part, 0);
-  for (int step = 0; step < a.steps; step += 2) {
+  for (int step = first; step <= last; step += R) {
     step_of(step, std::integral_constant<int, 0>());
-    if (step + 1 < a.steps) step_of(step + 1, std::integral_constant<int, 1>());
+    if (step + 1 <= last) step_of(step + 1, std::integral_constant<int, 1>());
+    if constexpr (R >= 4) {
+      if (step + 2 <= last) step_of(step + 2, std::integral_constant<int, 2>());
+      if (step + 3 <= last) step_of(step + 3, std::integral_constant<int, 3>());
+    }
   }
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) asm volatile("" ::"v"(code[i][c]), "v"(scale[i][c]));
   __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0(0));  // no DMA outlives the workgroup
-  if (a.y_f32) {
-    float* y = static_cast<float*>(a.y) + (b * a.M + m0) * a.O + o0;
-    const bool vec = a.O % 4 == 0 && (uintptr_t)a.y % 16 == 0;
+  if (a.y_f32 || a.parts) {
+    const bool part = a.parts != nullptr;  // sums of some of the steps: joined, and scaled, by fp4_join_kernel
+    if (part) mant = 1.0f;
+    float* y = (part ? a.parts + (int64_t)blockIdx.y * gridDim.z * a.M * a.O : static_cast<float*>(a.y)) + (b * a.M + m0) * a.O + o0;
+    const bool vec = a.O % 4 == 0 && (part || (uintptr_t)a.y % 16 == 0);
 #pragma unroll
     for (int q = 0; q < MS; ++q) {
       const int m = wm * 16 * MS + 16 * q + r;
@@ -609,16 +671,67 @@ __global__ void __launch_bounds__(64 * WM * WN, MS * NS > 32 ? 1 : 2) fp4_tile_k
   }
 }
 
+// y = S sum of the parts, in their order.
+__global__ void __launch_bounds__(256) fp4_join_kernel(const float* __restrict__ parts, int splits, int64_t per, int64_t batch, const float* __restrict__ ts,
+                                                       void* __restrict__ y, int y_f32) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, total = per * batch;
+  if (i >= total) return;
+  float pow2 = 1.0f, mant[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+  if (ts)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) split_scale(ts[min(i + c, total - 1) / per], pow2, mant[c]);
+  const bool vec = total % 4 == 0;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < splits; ++s) {
+    const float* p = parts + s * total + i;
+    if (vec) {
+      const floatx4 q = *reinterpret_cast<const floatx4*>(p);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] += q[c];
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] += i + c < total ? p[c] : 0.0f;
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) v[c] *= mant[c];
+  if (y_f32) {
+    float* o = static_cast<float*>(y) + i;
+    if (vec && (uintptr_t)y % 16 == 0) {
+      *reinterpret_cast<floatx4*>(o) = floatx4{v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (i + c < total) o[c] = v[c];
+    }
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(y) + i;
+    const bf16x2_t lo{(__bf16)v[0], (__bf16)v[1]}, hi{(__bf16)v[2], (__bf16)v[3]};
+    const u32x2 h{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+    if (vec && (uintptr_t)y % 8 == 0) {
+      *reinterpret_cast<u32x2*>(o) = h;
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (i + c < total) o[c] = (uint16_t)(h[c >> 1] >> (16 * (c & 1)));
+    }
+  }
+}
+
 constexpr int64_t kMost = 0xFFFFFFFF;  // threads of a launch along x
 constexpr int64_t kMostMatrices = 65535;
 
-template <int FMT, bool GRAD, int TERMS, int WM, int WN, int MS, int NS>
-static int launch_tile(const Fp4MatmulArgs& a, int64_t batch, hipStream_t st) {
-  using C = Fp4Tile<WM, WN, MS, NS, GRAD>;
+template <int FMT, bool GRAD, int TERMS, int R, int WM, int WN, int MS, int NS>
+static int launch_tile(const Fp4MatmulArgs& a, int64_t batch, int splits, hipStream_t st) {
+  using C = Fp4Tile<R, WM, WN, MS, NS, GRAD>;
   const int64_t mt = (a.M + C::BM - 1) / C::BM, ot = (a.O + C::BO - 1) / C::BO, grid = (mt * ot + 7) / 8 * 8;
   if (grid * C::TH > kMost) return fail(FP4_ERR_UNSUPPORTED, "fp4_matmul: too many rows or outputs");
-  hipLaunchKernelGGL((fp4_tile_kernel<FMT, GRAD, TERMS, WM, WN, MS, NS>), dim3((unsigned)grid, 1, (unsigned)batch), dim3(C::TH), 0, st, a, (int)mt, (int)ot);
-  return check_launch("fp4_matmul");
+  hipLaunchKernelGGL((fp4_tile_kernel<FMT, GRAD, TERMS, R, WM, WN, MS, NS>), dim3((unsigned)grid, (unsigned)splits, (unsigned)batch), dim3(C::TH), 0, st, a, (int)mt, (int)ot);
+  FP4_CHECK(check_launch("fp4_matmul"));
+  if (splits == 1) return FP4_OK;
+  const int64_t wgs = (a.M * a.O * batch + 1023) / 1024;
+  hipLaunchKernelGGL(fp4_join_kernel, dim3((unsigned)wgs), dim3(256), 0, st, a.parts, splits, a.M * a.O, batch, FMT == FP4_FMT_NVFP4 ? a.ts : nullptr, a.y, a.y_f32);
+  return check_launch("fp4_join");
 }
 
 // The few-rows kernel's waves and steps a wave for K (0 waves: K is too long).
@@ -669,12 +782,20 @@ static int launch_few_rows(const Fp4FewArgs& a, int64_t batch, int terms, int ms
   return launch_few_dma<FMT, 1, 4, 1>(a, batch, f.waves, st);
 }
 
-#ifndef FP4_CFG
-#define FP4_CFG 2, 2, 2, 2
-#endif
+// The tiles there are: rows, outputs.
+enum Fp4TileKind { TILE_16 = 0, TILE_32, TILE_64, TILE_128, TILE_256 };
+
+template <int FMT, bool GRAD, int TERMS>
+static int launch_tiles(const Fp4MatmulArgs& a, int64_t batch, int kind, int splits, hipStream_t st) {
+  if (kind == TILE_16) return launch_tile<FMT, GRAD, TERMS, 4, 1, 4, 1, 2>(a, batch, splits, st);
+  if (kind == TILE_32) return launch_tile<FMT, GRAD, TERMS, 4, 1, 4, 2, 2>(a, batch, splits, st);
+  if (kind == TILE_64) return launch_tile<FMT, GRAD, TERMS, 4, 2, 2, 2, 2>(a, batch, splits, st);
+  if (kind == TILE_128) return launch_tile<FMT, GRAD, TERMS, 2, 2, 2, 4, 4>(a, batch, splits, st);
+  return launch_tile<FMT, GRAD, TERMS, 2, 2, 4, 8, 4>(a, batch, splits, st);
+}
 template <int FMT, bool GRAD>
-static int launch_fp4(const Fp4MatmulArgs& a, int64_t batch, hipStream_t st) {
-  return a.terms == 1 ? launch_tile<FMT, GRAD, 1, FP4_CFG>(a, batch, st) : launch_tile<FMT, GRAD, 3, FP4_CFG>(a, batch, st);
+static int launch_fp4(const Fp4MatmulArgs& a, int64_t batch, int kind, int splits, hipStream_t st) {
+  return a.terms == 1 ? launch_tiles<FMT, GRAD, 1>(a, batch, kind, splits, st) : launch_tiles<FMT, GRAD, 3>(a, batch, kind, splits, st);
 }
 
 // ------------------------------------------------------------ the calls
@@ -694,8 +815,48 @@ struct Fp4Plan {
   int64_t sum, out, ld, terms;  // length of the sum, outputs, row stride and terms of x as the kernels read it
   bool rows;                    // x is copied (split, padded) first
   int few;                      // the few-rows kernel's blocks of 16 rows, or 0
-  size_t bytes;
+  int kind, splits, each;       // the tile, workgroups that share one, their steps
+  size_t row_bytes, bytes;      // of the workspace: x's rows, all
 };
+
+// One tile's modelled time: rounds of as many as the card holds at once at full load, and a last round between a lone
+// tile's time and a full round's (microseconds a step of 64 products).
+struct Fp4TileModel {
+  int bm, bo, slots;
+  double fixed, lone, loaded;
+};
+// This card's, fitted at 40 and 160 steps.  Measured (us, graph replays) in this order, without splits: dx of 16 x 10240 ->
+// 2560 80, 86, 77, 137, 276; y of 300 x 2560 -> 2560 36, 25, 18, 38, 76; of 1024 x 2560 -> 2560 85, 54, 33, 38, 77;
+// 8192 x 2560 -> 10240 - , - , 764, 586, 435.
+constexpr Fp4TileModel kTiles[] = {{16, 128, 768, 3.0, 0.50, 1.25}, {32, 128, 768, 3.0, 0.54, 1.40}, {64, 64, 768, 3.0, 0.37, 0.72},
+                                   {128, 128, 512, 3.0, 0.85, 1.45}, {256, 256, 256, 4.0, 1.75, 2.15}};
+
+// The tile and the number of workgroups that share one's steps whose modelled time is the least.  Parts of a tile are
+// written, read and joined by a launch of its own: 4.5 us, and their bytes at 5 TB/s (4096 x 10240 -> 2560: 278 us in
+// whole tiles, 251 in thirds; 16 x 10240 -> 2560 80 and, in eighths, 20).
+static void choose_tile(int64_t m, int64_t out, int64_t steps, int64_t batch, int terms, Fp4Plan& p) {
+  double best = 0;
+  p.kind = TILE_64;
+  p.splits = 1;
+  for (int kind = TILE_16; kind <= TILE_256; ++kind) {
+    const Fp4TileModel& t = kTiles[kind];
+    const double tiles = (double)((m + t.bm - 1) / t.bm) * (double)((out + t.bo - 1) / t.bo) * (double)batch, terms_cost = terms == 3 ? 2.3 : 1.0;
+    for (int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (s > 1 && (steps < 2 * s || tiles * s > 8192)) break;
+      const double n = (double)((steps + s - 1) / s) * terms_cost, one = t.fixed + t.lone * n, full = t.fixed + t.loaded * n;
+      const double rounds = std::floor(tiles * s / t.slots), rest = tiles * s - rounds * t.slots;
+      double time = rounds * full + (rest > 0 ? one + (full - one) * rest / t.slots : 0.0);
+      if (s > 1) time += 4.5 + 8.0 * s * (double)batch * (double)m * (double)out / 5e6;
+      if (best == 0 || time < best) {
+        best = time;
+        p.kind = kind;
+        p.splits = s;
+      }
+    }
+  }
+  p.each = (int)((steps + p.splits - 1) / p.splits);
+  p.splits = p.each > 0 ? (int)((steps + p.each - 1) / p.each) : 1;
+}
 
 static int plan_fp4(int w_fmt, int x_dtype, bool grad, int64_t batch, int64_t m, int64_t n, int64_t k, Fp4Plan& p) {
   if (w_fmt < FP4_FMT_NVFP4 || w_fmt > FP4_FMT_NONE) return fail(FP4_ERR_INVALID_ARG, "fp4_matmul: unknown w_fmt %d", w_fmt);
@@ -717,7 +878,10 @@ static int plan_fp4(int w_fmt, int x_dtype, bool grad, int64_t batch, int64_t m,
   p.terms = x_dtype == FP4_DT_F32 ? 3 : 1;
   p.few = grad ? 0 : few_blocks(m, n, k, (int)p.terms);
   p.rows = !p.few && (p.terms > 1 || p.ld != p.sum);
-  p.bytes = p.rows ? (size_t)(2 * p.terms) * (size_t)(batch * m * p.ld) : 0;
+  p.kind = p.splits = p.each = 0;
+  if (!p.few) choose_tile(m, p.out, p.ld / kBK, batch, (int)p.terms, p);
+  p.row_bytes = p.rows ? ((size_t)(2 * p.terms) * (size_t)(batch * m * p.ld) + 255) / 256 * 256 : 0;
+  p.bytes = p.row_bytes + (p.splits > 1 ? sizeof(float) * (size_t)p.splits * (size_t)(batch * m * p.out) : 0);
   if (p.rows && batch * m * (p.ld / 8) > kMost) return fail(FP4_ERR_UNSUPPORTED, "fp4_matmul: too many rows");
   return FP4_OK;
 }
@@ -752,9 +916,10 @@ static int run_fp4(int w_fmt, const void* x, int x_dtype, bool grad, const uint8
     x = to;
   }
   const Fp4MatmulArgs a{static_cast<const uint16_t*>(x), w, static_cast<const uint8_t*>(w_scales), tensor_scale, y, p.ld, batch * m * p.ld,
-                        m, n, k, p.out, (int)(p.ld / kBK), (int)p.terms, y_dtype == FP4_DT_F32};
-  if (w_fmt == FP4_FMT_NVFP4) return grad ? launch_fp4<FP4_FMT_NVFP4, true>(a, batch, st) : launch_fp4<FP4_FMT_NVFP4, false>(a, batch, st);
-  return grad ? launch_fp4<FP4_FMT_MXFP4, true>(a, batch, st) : launch_fp4<FP4_FMT_MXFP4, false>(a, batch, st);
+                        m, n, k, p.out, (int)(p.ld / kBK), (int)p.terms, y_dtype == FP4_DT_F32, p.each,
+                        p.splits > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.row_bytes) : nullptr};
+  if (w_fmt == FP4_FMT_NVFP4) return grad ? launch_fp4<FP4_FMT_NVFP4, true>(a, batch, p.kind, p.splits, st) : launch_fp4<FP4_FMT_NVFP4, false>(a, batch, p.kind, p.splits, st);
+  return grad ? launch_fp4<FP4_FMT_MXFP4, true>(a, batch, p.kind, p.splits, st) : launch_fp4<FP4_FMT_MXFP4, false>(a, batch, p.kind, p.splits, st);
 }
 
 }  // namespace fp4
