@@ -21,6 +21,7 @@ namespace fp4 {
 
 constexpr int kTopMost = 64;    // one lane of a wave each
 constexpr int kSplitsMost = 64;  // parts of a row, one lane each when they meet
+constexpr int kFound = 1024;     // logits of a workgroup that may reach the floor before they are taken out wave by wave
 constexpr int kFewInserts = 6;   // alternatives that are inserted one by one; more are sorted and merged
 constexpr float kLog2E = 1.44269504f, kLn2 = 0.693147181f;
 
@@ -64,6 +65,41 @@ __device__ __forceinline__ void join(Sums& a, const Sums& b, float c) {
   a.m = m;
 }
 
+// The sums of the first N lanes (a power of two), for every lane: lane i takes lane i + N / 2 and so on, in a fixed order.
+template <int N>
+__device__ __forceinline__ void join_lanes(Sums& s, float c) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) {
+    const Sums b{__shfl_down(s.m, o), __shfl_down(s.R, o), __shfl_down(s.E, o), __shfl_down(s.ones, o), __shfl_down(s.rank, o)};
+    if (lane < o) join(s, b, c);
+  }
+  s = Sums{__shfl(s.m, 0), __shfl(s.R, 0), __shfl(s.E, 0), __shfl(s.ones, 0), __shfl(s.rank, 0)};
+}
+
+// The value of the lane whose number differs in the bits D: within rows of 16 lanes by DPP, across them by the row and
+// half swaps of gfx950 (a shuffle through LDS takes a wave about three times as long).
+template <int D>
+__device__ __forceinline__ int lane_xor(int v) {
+  if constexpr (D == 1) return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);         // quads 1 0 3 2
+  else if constexpr (D == 2) return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);    // quads 2 3 0 1
+  else if constexpr (D == 4) return __builtin_amdgcn_mov_dpp(__builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true), 0x1B, 0xF, 0xF, true);  // eights turned round, quads too
+  else if constexpr (D == 8) return __builtin_amdgcn_mov_dpp(v, 0x128, 0xF, 0xF, true);   // rows turned by 8
+  else if constexpr (D == 15) return __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true);  // rows turned round
+  else if constexpr (D == 16) {  // the odd rows of one copy change places with the even rows of the other
+    const auto p = __builtin_amdgcn_permlane16_swap((unsigned)v, (unsigned)v, false, false);
+    return (threadIdx.x & 16) ? (int)p[0] : (int)p[1];
+  } else if constexpr (D == 32) {
+    const auto p = __builtin_amdgcn_permlane32_swap((unsigned)v, (unsigned)v, false, false);
+    return (threadIdx.x & 32) ? (int)p[0] : (int)p[1];
+  } else {
+    static_assert(D == 63, "a power of two, 15 or 63");
+    return lane_xor<32>(lane_xor<16>(lane_xor<15>(v)));
+  }
+}
+template <int D>
+__device__ __forceinline__ float lane_xor(float v) { return __int_as_float(lane_xor<D>(__float_as_int(v))); }
+
 template <int CTRL>
 __device__ __forceinline__ float dpp_max(float v) {
   const int o = __builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), CTRL, 0xF, 0xF, false);
@@ -89,28 +125,28 @@ __device__ __forceinline__ bool before(float a, int ia, float b, int ib) { retur
 struct TopList {
   float v = -__builtin_huge_valf();
   int id = kNone;
-  // One step of a sorting network: of each two lanes `d` apart the one with `first` gets the element that comes before.
-  __device__ __forceinline__ void exchange(int d, bool first) {
-    const float ov = __shfl_xor(v, d);
-    const int oid = __shfl_xor(id, d);
+  // One step of a sorting network: of each two lanes D apart the one with `first` gets the element that comes before.
+  template <int D>
+  __device__ __forceinline__ void exchange(bool first) {
+    const float ov = lane_xor<D>(v);
+    const int oid = lane_xor<D>(id);
     if (before(v, id, ov, oid) != first) v = ov, id = oid;
   }
-  __device__ __forceinline__ void sort() {
+  template <int N, int D>
+  __device__ __forceinline__ void sort_steps() {
     const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int n = 2; n <= 64; n *= 2)
-#pragma unroll
-      for (int d = n / 2; d > 0; d /= 2) exchange(d, ((lane & d) == 0) == ((lane & n) == 0));
+    exchange<D>(((lane & D) == 0) == ((lane & N) == 0));
+    if constexpr (D > 1) sort_steps<N, D / 2>();
+    else if constexpr (N < 64) sort_steps<2 * N, N>();
   }
+  __device__ __forceinline__ void sort() { sort_steps<2, 1>(); }
   // The first 64 of both lists: of the j-th here and the j-th last there the better, which
   // rise and fall once, so that the network's last six steps sort them.
   __device__ __forceinline__ void merge(float ov, int oid) {
-    const int lane = threadIdx.x & 63;
-    ov = __shfl_xor(ov, 63);
-    oid = __shfl_xor(oid, 63);
+    ov = lane_xor<63>(ov);
+    oid = lane_xor<63>(oid);
     if (before(ov, oid, v, id)) v = ov, id = oid;
-#pragma unroll
-    for (int d = 32; d > 0; d /= 2) exchange(d, (lane & d) == 0);
+    sort_steps<64, 32>();
   }
   __device__ __forceinline__ void insert(float cv, int cid) {  // cv, cid: the same for every lane
     const int lane = threadIdx.x & 63, at = __popcll(__ballot(before(v, id, cv, cid)));
@@ -120,13 +156,29 @@ struct TopList {
   }
 };
 
+// The wave's values, largest first (a sorting network; no NaN).
+template <int N, int D>
+__device__ __forceinline__ float sorted_steps(float v) {
+  const int lane = threadIdx.x & 63;
+  const float o = lane_xor<D>(v);
+  v = ((lane & D) == 0) == ((lane & N) == 0) ? fmaxf(v, o) : fminf(v, o);
+  if constexpr (D > 1) return sorted_steps<N, D / 2>(v);
+  else if constexpr (N < 64) return sorted_steps<2 * N, N>(v);
+  else return v;
+}
+__device__ __forceinline__ float sorted(float v) { return sorted_steps<2, 1>(v); }
+
 // Of the lanes with the largest v the one with the lowest id.
 __device__ __forceinline__ int lane_of_max(float v, int id, float most) {
   uint64_t which = __ballot(v == most);
   if (__popcll(which) > 1) {
     int low = v == most ? id : kNone;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) low = min(low, __shfl_xor(low, o));
+    low = min(low, lane_xor<1>(low));
+    low = min(low, lane_xor<2>(low));
+    low = min(low, lane_xor<4>(low));
+    low = min(low, lane_xor<8>(low));
+    low = min(low, lane_xor<16>(low));
+    low = min(low, lane_xor<32>(low));
     which = __ballot(v == most && id == low);
   }
   return (int)__ffsll((unsigned long long)which) - 1;
@@ -166,7 +218,7 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& a, int64_t row, co
   }
 }
 
-// The part `split` of a row by a workgroup of four waves.  A wave takes 2 x 64
+// The part `split` of a row by a workgroup of WAVES waves.  A wave takes 2 x 64
 // pieces of 16 bytes at a time, loaded one round ahead.  Its running maximum is one
 // for all lanes, and a round whose logits all lie below it needs nothing but
 // t = (l - m) c, 2^t, the two sums and the count of logits before the target, 10
@@ -174,12 +226,16 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& a, int64_t row, co
 // new one and counts the exponentials that are 1.  Alternatives: a round with
 // nothing above the wave's last one costs a comparison; else the lanes' largest values
 // are taken out and inserted, or where they are many sorted and merged into the list.
-template <typename T>
-__global__ void __launch_bounds__(256) logprobs_kernel(LogprobArgs a) {
+//
+// HELD rounds at most (0: any number): all are loaded at once and stay in registers, so that the workgroup knows its largest
+// logit before any sum, and a floor that no alternative lies below: the top-th largest of its 64 groups' largest.
+template <typename T, int WAVES, int HELD>
+__global__ void __launch_bounds__(64 * WAVES) logprobs_kernel(LogprobArgs a) {
+  constexpr int ROUND = 128 * WAVES;  // pieces
   constexpr int PV = 16 / (int)sizeof(T), NV = 2 * PV;  // values of a piece, of a lane's round
-  __shared__ Sums sums_of[4];
-  __shared__ float list_v[4][kTopMost];
-  __shared__ int list_id[4][kTopMost];
+  __shared__ Sums sums_of[WAVES];
+  __shared__ float list_v[WAVES][kTopMost];
+  __shared__ int list_id[WAVES][kTopMost];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t row = blockIdx.x / a.splits;
   const int split = (int)(blockIdx.x - row * a.splits);
@@ -187,7 +243,7 @@ __global__ void __launch_bounds__(256) logprobs_kernel(LogprobArgs a) {
   const float ninf = -__builtin_huge_valf(), c = a.inv_t * kLog2E;
   // pieces start at multiples of 16 bytes: the first one `skip` values before the row
   const int skip = (int)(((uintptr_t)l & 15) / sizeof(T)), V = (int)a.V;
-  const int pieces = (int)((a.V + skip + PV - 1) / PV), per = ((pieces + a.splits - 1) / a.splits + 511) / 512 * 512;
+  const int pieces = (int)((a.V + skip + PV - 1) / PV), per = ((pieces + a.splits - 1) / a.splits + ROUND - 1) / ROUND * ROUND;
   const int first = split * per, last = min(pieces, first + per);
   const int32_t t = a.targets ? a.targets[row] : -1;
   const bool given = t >= 0 && t < V;
@@ -200,10 +256,9 @@ __global__ void __launch_bounds__(256) logprobs_kernel(LogprobArgs a) {
   Sums s = no_sums();
   float R = 0.0f, E = 0.0f, gate = ninf;  // a lane's sums; logits below `gate` have 2^t < 1
   TopList best;
-  float least = ninf;                     // the last alternative
+  float least = ninf, floor = ninf;       // the last alternative; none lies below `floor`
   int least_id = kNone;
-  u32x4 raw[2];
-  auto load = [&](int p0) __attribute__((always_inline)) {
+  auto load = [&](u32x4 (&raw)[2], int p0) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int p = p0 + 64 * u + lane, i0 = p * PV - skip;
@@ -222,16 +277,15 @@ __global__ void __launch_bounds__(256) logprobs_kernel(LogprobArgs a) {
       }
     }
   };
-  int p0 = first + wave * 128;
-  if (p0 < last) load(p0);
-  for (; p0 < last; p0 += 512) {
-    float v[NV];
+  auto values = [&](const u32x4 (&raw)[2], float (&v)[NV]) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(raw[i >> 2][i & 3]);
       else v[i] = __uint_as_float((i & 1) ? raw[i >> 3][(i >> 1) & 3] & 0xFFFF0000u : raw[i >> 3][(i >> 1) & 3] << 16);
     }
-    if (p0 + 512 < last) load(p0 + 512);
+  };
+  auto gate_at = [&](float m) __attribute__((always_inline)) { return m - (0x1p-18f / c + fabsf(m) * 0x1p-22f); };
+  auto add_up = [&](int p0, const float (&v)[NV]) __attribute__((always_inline)) {
     float lm = v[0];
 #pragma unroll
     for (int i = 1; i < NV; ++i) lm = fmaxf(lm, v[i]);
@@ -244,7 +298,7 @@ __global__ void __launch_bounds__(256) logprobs_kernel(LogprobArgs a) {
         R = f * (R + mine);
         s.ones = 0;
         s.m = most;
-        gate = most - (0x1p-18f / c + fabsf(most) * 0x1p-22f);
+        gate = gate_at(most);
       }
       const float at = s.m > ninf ? s.m : 0.0f;
 #pragma unroll
@@ -284,37 +338,127 @@ __global__ void __launch_bounds__(256) logprobs_kernel(LogprobArgs a) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) s.rank += __popcll(__ballot(v[i] >= bar));
     }
-    if (a.top > 0) {
-      while (__any(lm >= least && lm > ninf)) {
-        int k = NV;  // the first of this lane's values that is its largest
+  };
+  // The round's alternatives into the wave's list.
+  auto select = [&](int p0, float (&v)[NV]) __attribute__((always_inline)) {
+    float lm = v[0];
 #pragma unroll
-        for (int i = NV - 1; i >= 0; --i) k = v[i] == lm ? i : k;
-        const int id = (p0 + 64 * (k / PV) + lane) * PV - skip + k % PV;
-        const bool better = lm > ninf && before(lm, id, least, least_id);
-        const uint64_t which = __ballot(better);
-        if (which == 0) break;
-        bool gone = better;
-        if (__popcll(which) > kFewInserts) {  // every such lane's largest at once
-          TopList some;
-          if (better) some.v = lm, some.id = id;
-          some.sort();
-          best.merge(some.v, some.id);
-        } else {
-          const float most = wave_max(better ? lm : ninf);
-          const int from = lane_of_max(better ? lm : ninf, id, most);
-          best.insert(most, __builtin_amdgcn_readlane(id, from));
-          gone = lane == from;
+    for (int i = 1; i < NV; ++i) lm = fmaxf(lm, v[i]);
+    while (__any(lm >= least && lm > ninf)) {
+      int k = NV;  // the first of this lane's values that is its largest
+#pragma unroll
+      for (int i = NV - 1; i >= 0; --i) k = v[i] == lm ? i : k;
+      const int id = (p0 + 64 * (k / PV) + lane) * PV - skip + k % PV;
+      const bool better = lm > ninf && before(lm, id, least, least_id);
+      const uint64_t which = __ballot(better);
+      if (which == 0) break;
+      bool gone = better;
+      if (__popcll(which) > kFewInserts) {  // every such lane's largest at once
+        TopList some;
+        if (better) some.v = lm, some.id = id;
+        some.sort();
+        best.merge(some.v, some.id);
+      } else {
+        const float most = wave_max(better ? lm : ninf);
+        const int from = lane_of_max(better ? lm : ninf, id, most);
+        best.insert(most, __builtin_amdgcn_readlane(id, from));
+        gone = lane == from;
+      }
+      least = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(best.v), a.top - 1));
+      least_id = __builtin_amdgcn_readlane(best.id, a.top - 1);
+      if (HELD && !before(least, least_id, floor, kNone)) least = floor, least_id = kNone;
+      if (gone) {
+        lm = ninf;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          v[i] = i == k ? ninf : v[i];
+          lm = fmaxf(lm, v[i]);
         }
-        least = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(best.v), a.top - 1));
-        least_id = __builtin_amdgcn_readlane(best.id, a.top - 1);
-        if (gone) {
-          lm = ninf;
+      }
+    }
+  };
+  const int p0 = first + wave * 128;
+  float v[NV];
+  if constexpr (HELD == 0) {
+    u32x4 raw[2];
+    if (p0 < last) load(raw, p0);
+    for (int p = p0; p < last; p += ROUND) {
+      values(raw, v);
+      if (p + ROUND < last) load(raw, p + ROUND);
+      add_up(p, v);
+      if (a.top > 0) select(p, v);
+    }
+  } else {
+    static_assert(WAVES * 4 == 64, "64 groups of 16 lanes");
+    __shared__ float groups[64], found_v[kFound];
+    __shared__ int found_id[kFound], found;
+    u32x4 raw[HELD][2];
+    float most = ninf;
+    if (threadIdx.x == 0) found = 0;
+#pragma unroll
+    for (int h = 0; h < HELD; ++h)
+      if (p0 + h * ROUND < last) load(raw[h], p0 + h * ROUND);
+#pragma unroll
+    for (int h = 0; h < HELD; ++h)
+      if (p0 + h * ROUND < last) {
+        values(raw[h], v);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) most = fmaxf(most, v[i]);
+      }
+    most = fmaxf(most, lane_xor<1>(most));
+    most = fmaxf(most, lane_xor<2>(most));
+    most = fmaxf(most, lane_xor<4>(most));
+    most = fmaxf(most, lane_xor<8>(most));
+    if ((lane & 15) == 0) groups[wave * 4 + (lane >> 4)] = most;
+    __syncthreads();
+    const float mine = groups[lane];
+    s.m = wave_max(mine);
+    gate = gate_at(s.m);
+    if (a.top > 0) {
+      floor = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sorted(mine)), a.top - 1));
+      least = floor;
+    }
+#pragma unroll
+    for (int h = 0; h < HELD; ++h)
+      if (p0 + h * ROUND < last) {
+        values(raw[h], v);
+        add_up(p0 + h * ROUND, v);
+        if (a.top > 0) {  // what reaches the floor, in any order
 #pragma unroll
           for (int i = 0; i < NV; ++i) {
-            v[i] = i == k ? ninf : v[i];
-            lm = fmaxf(lm, v[i]);
+            const bool in = v[i] >= floor && v[i] > ninf;
+            const uint64_t which = __ballot(in);
+            if (which == 0) continue;
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&found, __popcll(which));
+            at = __builtin_amdgcn_readfirstlane(at) + __popcll(which & ((1ull << lane) - 1));
+            if (in && at < kFound) {
+              found_v[at] = v[i];
+              found_id[at] = (p0 + h * ROUND + 64 * (i / PV) + lane) * PV - skip + i % PV;
+            }
           }
         }
+      }
+    if (a.top > 0) {
+      __syncthreads();
+      const int n = found;
+      if (n <= kFound) {
+        if (wave == 0)
+          for (int j = 0; j < n; j += 64) {
+            TopList some;
+            if (j + lane < n) some.v = found_v[j + lane], some.id = found_id[j + lane];
+            some.sort();
+            if (j == 0) best = some;
+            else best.merge(some.v, some.id);
+          }
+      } else {  // many equal ones
+#pragma unroll
+        for (int h = 0; h < HELD; ++h)
+          if (p0 + h * ROUND < last) {
+            values(raw[h], v);
+            select(p0 + h * ROUND, v);
+          }
+        merge_waves<WAVES>(best, wave, list_v, list_id);
       }
     }
   }
@@ -326,12 +470,17 @@ __global__ void __launch_bounds__(256) logprobs_kernel(LogprobArgs a) {
   s.R = R;
   s.E = E;
   if (lane == 0) sums_of[wave] = s;
-  if (a.top > 0) merge_waves<4>(best, wave, list_v, list_id);
+  if (HELD == 0 && a.top > 0) merge_waves<WAVES>(best, wave, list_v, list_id);
   else __syncthreads();
   if (wave != 0) return;
-  s = sums_of[0];
+  if constexpr (WAVES == 4) {
+    s = sums_of[0];
 #pragma unroll
-  for (int w = 1; w < 4; ++w) join(s, sums_of[w], c);
+    for (int w = 1; w < 4; ++w) join(s, sums_of[w], c);
+  } else {
+    s = lane < WAVES ? sums_of[lane] : no_sums();
+    join_lanes<WAVES>(s, c);
+  }
   // what the first piece holds before the row counted as masked logits of lower ids
   if (split == 0 && lt == ninf) s.rank -= skip;
   if (a.splits == 1) {
@@ -376,33 +525,27 @@ __global__ void __launch_bounds__(512) logprobs_join_kernel(LogprobArgs a) {
     merge_waves<WAVES>(best, wave, list_v, list_id);
   }
   if (wave != 0) return;
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {  // lane i takes lane i + o, in a fixed order
-    Sums b;
-    b.m = __shfl_down(s.m, o);
-    b.R = __shfl_down(s.R, o);
-    b.E = __shfl_down(s.E, o);
-    b.ones = __shfl_down(s.ones, o);
-    b.rank = __shfl_down(s.rank, o);
-    if (lane < o) join(s, b, c);
-  }
-  s.m = __shfl(s.m, 0);
-  s.R = __shfl(s.R, 0);
-  s.E = __shfl(s.E, 0);
-  s.ones = __shfl(s.ones, 0);
-  s.rank = __shfl(s.rank, 0);
+  join_lanes<kSplitsMost>(s, c);
   const int32_t t = a.targets ? a.targets[row] : -1;
   const bool given = t >= 0 && t < a.V;
   const float lt = given ? logit(static_cast<const T*>(a.logits) + row * a.stride, t) : 0.0f;
   finish_row(a, row, s, best, given, lt);
 }
 
-// Parts of a row: enough workgroups to fill the card four times over (a workgroup
-// holds 16 KB of loads in flight), a part being a round of its four waves at least.
-static int logprob_splits(int dtype, int64_t tokens, int64_t vocab) {
-  const int64_t rounds = (vocab + (dtype == FP4_DT_F32 ? 2047 : 4095)) / (dtype == FP4_DT_F32 ? 2048 : 4096);
+// Few rows: 16 waves a workgroup with up to four rounds in registers, a row of more in parts of two as long as there are
+// fewer workgroups than compute units.  Else four waves, and parts that fill the card four times over.
+constexpr int kHeld = 4;
+struct LogprobShape {
+  bool held;
+  int splits;
+};
+static LogprobShape logprob_shape(int dtype, int64_t tokens, int64_t vocab) {
+  const int64_t rounds = (vocab + 7) / (dtype == FP4_DT_F32 ? 4 : 8) / 512 + 1, held = (rounds + 3) / 4;  // of 4 waves, of 16
+  const int64_t room = std::max<int64_t>(1, 256 / std::max<int64_t>(tokens, 1));
+  const int64_t parts = held <= kHeld ? 1 : std::min<int64_t>({(held + 1) / 2, room, kSplitsMost});
+  if (tokens < 768 && (held + parts - 1) / parts <= kHeld) return {true, (int)parts};
   const int64_t wanted = (1024 + tokens - 1) / std::max<int64_t>(tokens, 1);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({rounds, wanted, kSplitsMost}));
+  return {false, (int)std::max<int64_t>(1, std::min<int64_t>({rounds, wanted, kSplitsMost}))};
 }
 static size_t logprob_bytes(int64_t tokens, int splits, int top) { return splits == 1 ? 0 : sizeof(float) * (size_t)tokens * splits * (8 + 2 * top); }
 
@@ -518,7 +661,7 @@ extern "C" {
 int token_logprobs_workspace_size(int dtype, int64_t tokens, int64_t vocab, int top, size_t* bytes) {
   if (!bytes) return fail(FP4_ERR_INVALID_ARG, "null size pointer");
   FP4_CHECK(validate_logprobs(dtype, tokens, vocab, vocab, top, 1.0f));
-  *bytes = logprob_bytes(tokens, logprob_splits(dtype, tokens, vocab), top);
+  *bytes = logprob_bytes(tokens, logprob_shape(dtype, tokens, vocab).splits, top);
   return FP4_OK;
 }
 
@@ -531,7 +674,8 @@ int token_logprobs(const void* logits, int dtype, int64_t tokens, int64_t vocab,
   if ((uintptr_t)logits % (dtype == FP4_DT_F32 ? 4 : 2) || (uintptr_t)targets % 4 || (uintptr_t)logprobs % 4 || (uintptr_t)ranks % 4 ||
       (uintptr_t)top_ids % 4 || (uintptr_t)top_logprobs % 4 || (uintptr_t)stats % 4)
     return fail(FP4_ERR_INVALID_ARG, "logprobs: misaligned pointer");
-  const int splits = logprob_splits(dtype, tokens, vocab);
+  const LogprobShape shape = logprob_shape(dtype, tokens, vocab);
+  const int splits = shape.splits;
   const size_t need = logprob_bytes(tokens, splits, top);
   if (need) {
     if (!workspace || workspace_bytes < need) return fail(FP4_ERR_WORKSPACE, "logprobs: workspace of %zu bytes, %zu needed", workspace_bytes, need);
@@ -540,8 +684,13 @@ int token_logprobs(const void* logits, int dtype, int64_t tokens, int64_t vocab,
   hipStream_t st = as_stream(stream);
   const LogprobArgs a{logits, stride, vocab, targets, 1.0f / temperature, top, splits, logprobs, ranks, top_ids, top_logprobs, stats, static_cast<float*>(workspace)};
   const dim3 grid((unsigned)(tokens * splits));
-  if (dtype == FP4_DT_F32) hipLaunchKernelGGL(logprobs_kernel<float>, grid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL(logprobs_kernel<uint16_t>, grid, dim3(256), 0, st, a);
+  if (!shape.held) {
+    if (dtype == FP4_DT_F32) hipLaunchKernelGGL((logprobs_kernel<float, 4, 0>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((logprobs_kernel<uint16_t, 4, 0>), grid, dim3(256), 0, st, a);
+  } else {
+    if (dtype == FP4_DT_F32) hipLaunchKernelGGL((logprobs_kernel<float, 16, kHeld>), grid, dim3(1024), 0, st, a);
+    else hipLaunchKernelGGL((logprobs_kernel<uint16_t, 16, kHeld>), grid, dim3(1024), 0, st, a);
+  }
   FP4_CHECK(check_launch("token_logprobs"));
   if (splits == 1) return FP4_OK;
   if (dtype == FP4_DT_F32) hipLaunchKernelGGL(logprobs_join_kernel<float>, dim3((unsigned)tokens), dim3(512), 0, st, a);
