@@ -516,7 +516,9 @@ int fp4_matmul_grad(int w_fmt, const void* dy, int dy_dtype, const uint8_t* w, c
  * alternatives; slots left over get id -1 and -inf.  A row with every token masked
  * has logprob -inf and stats (-inf, -1, 0).  NaN or +inf in a row makes its logprobs,
  * Z and H NaN; a NaN is never an alternative and comes before nothing.  Sums are f32.
- * Results repeat bit for bit and do not depend on other rows.
+ * Results repeat bit for bit and do not depend on other rows; the order of a row's
+ * sums, and with it their last bits, goes by how many rows there are and by the row's
+ * alignment to 16 bytes.
  * Errors: vocab < 1, stride < vocab -> FP4_ERR_SHAPE; unknown dtype, top, temperature,
  * null or misaligned pointer (its type's) -> FP4_ERR_INVALID_ARG; 2^30 logits a row,
  * 2^24 rows, more logits than 2^46 -> FP4_ERR_UNSUPPORTED; FP4_ERR_WORKSPACE.

@@ -32,7 +32,7 @@ def w64(w, fmt):
     if fmt == "nvfp4":
         s = w["scales"].view(torch.float8_e4m3fn).double().reshape(v.shape[0], v.shape[1], -1) * w["tensor_scale"].double().reshape(-1, 1, 1)
     else:
-        s = torch.pow(torch.tensor(2.0, dtype=torch.float64, device=c.device), w["scales"].double() - 127)
+        s = torch.tensor([2.0 ** (i - 127) for i in range(256)], dtype=torch.float64, device=c.device)[w["scales"].int()]  # (a device's pow is not exact)
     return v * s.repeat_interleave(BLOCK[fmt], -1)
 
 
