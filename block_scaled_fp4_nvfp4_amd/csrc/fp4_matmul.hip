@@ -802,9 +802,6 @@ static int launch_fp4(const Fp4MatmulArgs& a, int64_t batch, int kind, int split
 
 // The few-rows kernel's blocks of 16 rows for a product, 0 where tiles are to take it.
 static int few_blocks(int64_t m, int64_t n, int64_t k, int terms) {
-#ifdef FP4_FEWM
-  if (m > FP4_FEWM) return 0;
-#endif
   if (m > (terms == 3 ? 128 : 64)) return 0;
   for (int ms = terms == 3 || m <= 16 ? 1 : m <= 32 ? 2 : 4; ms > 0; ms /= 2)
     if (few_shape(k, terms, ms).waves) return ms;

@@ -648,7 +648,8 @@ static int validate_logprobs(int dtype, int64_t tokens, int64_t vocab, int64_t s
   if (vocab >= (int64_t)1 << 30 || tokens >= (int64_t)1 << 24 || stride >= (int64_t)1 << 40 || (double)tokens * stride > 0x1p46)
     return fail(FP4_ERR_UNSUPPORTED, "logprobs: 2^30 logits a row, 2^24 rows or more than 2^46 logits");
   if (top < 0 || top > kTopMost) return fail(FP4_ERR_INVALID_ARG, "logprobs: top = %d, 0 to %d expected", top, kTopMost);
-  if (!(temperature > 0.0f && temperature < __builtin_huge_valf())) return fail(FP4_ERR_INVALID_ARG, "logprobs: temperature %g", (double)temperature);
+  // below, 1 / T times log2(e) may be infinite, and 0 times it NaN
+  if (!(temperature >= 0x1p-126f && temperature < __builtin_huge_valf())) return fail(FP4_ERR_INVALID_ARG, "logprobs: temperature %g", (double)temperature);
   return FP4_OK;
 }
 

@@ -87,6 +87,12 @@ def test_logprob_refusals(L, f):
     assert f(L, T=0, logits=None) == 0
 
 
+@pytest.mark.parametrize("f", [_lp, _lg], ids=["logprobs", "gradient"])
+def test_logprob_least_temperature(L, f):
+    assert f(L, temp=2.0 ** -127) == -1 and f(L, temp=1e-45) == -1   # 1 / T or its product with log2(e) overflows
+    assert f(L, temp=2.0 ** -126, T=0) == 0 and f(L, temp=3.4e38, T=0) == 0
+
+
 def test_logprob_refusals_of_outputs(L):
     assert _lp(L, top=65) == -1 and _lp(L, top=-1) == -1
     assert _lp(L, top=3) == -1 and _lp(L, top=3, ids=FAKE) == -1 and _lp(L, top=3, tl=FAKE) == -1
