@@ -436,7 +436,10 @@ __device__ __forceinline__ void read_turned(const uint8_t* p, bf16x8_t (&f)[NS])
 // half of the LDS that the step before last used.  Weights are the A operand of
 // the MFMA, so that a lane's four sums are four consecutive outputs of one row.
 // The gradient sums over W's rows: its tile lies in LDS as W does and is turned by
-// the transposing reads.
+// the transposing reads.  Large products are bound by how far the CU's parts overlap:
+// at 8192 x 10240 x 2560 (NVFP4, 256 x 256) 390 us, 1.1 PFLOP/s, where the MFMAs alone
+// take 247, no loads of codes 340 and no decoding and writing of them 375; small ones
+// by a step's latency, 0.4 to 0.5 us.
 template <int R, int WM, int WN, int MS, int NS, bool GRAD>
 struct Fp4Tile {
   static constexpr int WAVES = WM * WN, TH = 64 * WAVES, BM = 16 * MS * WM, BO = 16 * NS * WN;
@@ -447,13 +450,13 @@ struct Fp4Tile {
   static constexpr int XD = BM / 8 < WAVES ? 1 : BM / 8 / WAVES;   // DMA instructions of a wave a step
   static constexpr int YROW = BO * 2 + 16;                         // bytes of a row of bf16 results on their way out
   static constexpr int LDS = R * XB + 2 * WB > BM * YROW ? R * XB + 2 * WB : BM * YROW;
-  static_assert(CPT == 1 || CPT == 2 || CPT == 4, "a thread's codes");
+  static_assert(CPT == 1 || CPT == 2, "a thread's codes");
   static_assert((BO * 4) % TH == 0 && ((BM / 8) % WAVES == 0 || WAVES % (BM / 8) == 0), "whole chunks");
   static_assert(R == 2 || R == 4, "the steps that the loop has written out");
   static_assert(LDS <= 160 * 1024, "LDS");
 };
 
-template <int FMT, bool GRAD, int TERMS, int R, int WM, int WN, int MS, int NS>
+template <int FMT, bool GRAD, int TERMS, bool WIDE, int R, int WM, int WN, int MS, int NS>
 __global__ void __launch_bounds__(64 * WM * WN, 2) fp4_tile_kernel(Fp4MatmulArgs a, int mt, int ot) {
   using C = Fp4Tile<R, WM, WN, MS, NS, GRAD>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[C::LDS];
@@ -488,36 +491,50 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp4_tile_kernel(Fp4MatmulArgs
   // this thread's blocks of 16 codes: consecutive ones of one row of the weight tile
   constexpr int PER_ROW = GRAD ? C::BO / 16 : 4, CPT = C::CPT;
   const int trow = tid * CPT / PER_ROW, tblk = tid * CPT % PER_ROW;
-  // R steps' codes and scales as they were loaded
-  u32x2 code[R][CPT];
-  uint32_t scale[R][CPT];
-  uint32_t ok[R][CPT];  // all bits of what is inside
+  // Steps' codes and scales as they were loaded, one load each (8192 x 10240 x 2560: 400 us; 436 with two loads of codes
+  // and two of scales, whose lines the L1 then passes twice as often), scales byte by byte where pairs are not aligned.
+  // The large tiles (R = 2) load two steps' codes at a time, which lie in the same lines (390 us).
+  constexpr int SB = FMT == FP4_FMT_NVFP4 ? CPT : (CPT + 1) / 2, SL = WIDE ? 1 : SB;  // bytes of scales, loads of them
+  constexpr int CR = R == 2 ? 4 : R;  // steps whose codes are held or on their way
+  uint32_t code[CR][2 * CPT], scale[CR][SL];
   const uint32_t wrow = (uint32_t)(a.K / 2), srow = (uint32_t)(a.K / (FMT == FP4_FMT_NVFP4 ? 16 : 32));  // bytes of a row
-  const uint8_t* wbase = w + (GRAD ? o0 / 2 : o0 * wrow);
-  const uint8_t* sbase = ws + (GRAD ? o0 / (FMT == FP4_FMT_NVFP4 ? 16 : 32) : o0 * srow);
+  const uint32_t at_code = trow * wrow + tblk * 8, at_scale = trow * srow + (FMT == FP4_FMT_NVFP4 ? tblk : tblk >> 1);
+  const int blocks = (int)min((int64_t)1 << 30, a.K / 16 - (GRAD ? o0 / 16 : 0)) - tblk;  // of a row from this thread's first on
   auto load_w = [&](int step, int set) __attribute__((always_inline)) {
-    // rows and blocks past the end: others of the same step are loaded instead, and not used
-    const int64_t first_row = GRAD ? (int64_t)step * kBK : o0, first_blk = GRAD ? o0 / 16 : (int64_t)step * 4;
-    const int rows_left = (int)min((int64_t)(GRAD ? kBK : C::BO), a.N - first_row), blks_left = (int)min((int64_t)PER_ROW, a.K / 16 - first_blk);
-    const uint8_t* wp = wbase + (GRAD ? first_row * wrow : (int64_t)step * 32);
-    const uint8_t* sp = sbase + (GRAD ? first_row * srow : (int64_t)step * (FMT == FP4_FMT_NVFP4 ? 4 : 2));
-    const uint32_t row = min(trow, rows_left - 1);
+    // rows past the last one are left out by the buffers' bounds; blocks past a row's end are others, or left out
+    const int64_t first_row = GRAD ? (int64_t)step * kBK : o0;
+    const uint32_t rows = (uint32_t)min((int64_t)(GRAD ? kBK : C::BO), a.N - first_row);
+    const uint32_t cs = GRAD ? (uint32_t)(o0 / 2) : 0, ss = GRAD ? (uint32_t)(o0 / (FMT == FP4_FMT_NVFP4 ? 16 : 32)) : 0;  // where the tile starts in a row
+    const auto wb = buffer_of(w + first_row * wrow + cs, rows * wrow - cs);
+    const auto sb = buffer_of(ws + first_row * srow + ss, rows * srow - ss);
+    const uint32_t cat = GRAD ? 0 : step * 32, sat = GRAD ? 0 : step * (FMT == FP4_FMT_NVFP4 ? 4 : 2);
+    if constexpr (CPT == 1) {
+      const auto v = __builtin_amdgcn_raw_buffer_load_b64(wb, at_code, cat, 0);
 #pragma unroll
-    for (int c = 0; c < CPT; ++c) {
-      ok[set][c] = trow < rows_left && tblk + c < blks_left ? 0xFFFFFFFFu : 0;
-      const uint32_t at = tblk + c < blks_left ? tblk + c : 0;
-      code[set][c] = *reinterpret_cast<const u32x2*>(wp + (row * wrow + at * 8));
-      scale[set][c] = sp[row * srow + (FMT == FP4_FMT_NVFP4 ? at : at >> 1)];
+      for (int i = 0; i < 2; ++i) code[set][i] = v[i];
+    } else {
+      const auto v = __builtin_amdgcn_raw_buffer_load_b128(wb, at_code, cat, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) code[set][i] = v[i];
     }
+    if constexpr (SB / SL == 2) scale[set][0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(sb, at_scale, sat, 0);
+    else
+#pragma unroll
+      for (int i = 0; i < SL; ++i) scale[set][i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(sb, at_scale + i, sat, 0);
   };
   uint8_t* wlds = lds + R * C::XB;
   // The `part`-th of 2 CPT parts of the decoding: 8 codes, one 16-byte piece of the tile.
   float sc = 0.0f;
-  auto decode_w = [&](int set, int part, int half) __attribute__((always_inline)) {
+  uint32_t ok = 0;
+  auto decode_w = [&](int step, int set, int part, int half) __attribute__((always_inline)) {
     const int c = part >> 1, h = part & 1;
     // what is past the end counts 0 (an infinity or NaN there would reach sums whose x is 0)
-    if (h == 0) sc = block_scale<FMT>(scale[set][c] & ok[set][c], pow2);
-    const uint32_t d = code[set][c][h] & ok[set][c];
+    if (h == 0) {
+      ok = (GRAD ? 0 : 4 * step) + c < blocks ? 0xFFFFFFFFu : 0;
+      const int i = FMT == FP4_FMT_NVFP4 ? c : c >> 1;  // its byte of the scales
+      sc = block_scale<FMT>((SL == SB ? scale[set][SL == SB ? i : 0] : scale[set][0] >> 8 * i & 255) & ok, pow2);
+    }
+    const uint32_t d = code[set][2 * c + h] & ok;
     const int piece = 2 * (tblk + c) + h;
     uint8_t* to = wlds + half * C::WB + trow * C::WROW + 16 * (GRAD ? piece : piece ^ ((trow >> 1) & 7));
     st16(to, u32x4{decode2<FMT, 0>(d, sc), decode2<FMT, 1>(d, sc), decode2<FMT, 2>(d, sc), decode2<FMT, 3>(d, sc)});
@@ -551,14 +568,21 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp4_tile_kernel(Fp4MatmulArgs
   };
   // One step's products of one term of x, and on the way later steps' x and weights.  P: the set of the step's codes.
   auto body = [&](int step, auto P_, auto TERM_) __attribute__((always_inline)) {
-    constexpr int P = decltype(P_)::value, TERM = decltype(TERM_)::value, NEXT = (P + 1) % R;
+    constexpr int P = decltype(P_)::value, TERM = decltype(TERM_)::value, NEXT = (P + 1) % CR;
     const int half = (step - first) & 1;
     // This term's x has arrived and its weights are written; what was asked for after that x may still be on its
-    // way: its DMA, and of a step's codes and scales two loads at least, however the compiler merges them (none is
-    // dropped, since all are used at the end, and none passes a barrier).
+    // way: its DMA, and of a step's codes and scales two loads at least (none is dropped, since all are used at the
+    // end, and none passes a barrier).
     __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0((R - 2) * (C::XD + (TERMS == 1 ? 2 : 0))));
     asm volatile("s_barrier" ::: "memory");
-    if (TERM == 0) load_w(min(step + R, last), P);
+    if (TERM == 0) {
+      if constexpr (CR == R) {
+        load_w(min(step + R, last), P);
+      } else if constexpr (P & 1) {
+        load_w(min(step + CR - 1, last), P - 1);
+        load_w(min(step + CR, last), P);
+      }
+    }
     load_next_x();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
@@ -578,7 +602,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp4_tile_kernel(Fp4MatmulArgs
       if (TERM == 0) {
 #pragma unroll
         for (int part = 0; part < 2 * CPT; ++part)
-          if (i == (part * 2 * MS) / (2 * CPT)) decode_w(NEXT, part, half ^ 1);
+          if (i == (part * 2 * MS) / (2 * CPT)) decode_w(min(step + 1, last), NEXT, part, half ^ 1);
       }
 #pragma unroll
       for (int s = 0; s < NS; ++s) acc[i % MS][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[i / MS][s], xf[i % 3], acc[i % MS][s], 0, 0, 0);
@@ -601,22 +625,26 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp4_tile_kernel(Fp4MatmulArgs
     load_w(min(first + 1 + i, last), i + 1);
     load_next_x();
   }
+  if constexpr (CR != R) {
+    load_w(min(first + 2, last), 2);
+    load_w(min(first + 3, last), 3);
+  }
   asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int part = 0; part < 2 * CPT; ++part) decode_w(0, part, 0);
-  for (int step = first; step <= last; step += R) {
+  for (int part = 0; part < 2 * CPT; ++part) decode_w(first, 0, part, 0);
+  for (int step = first; step <= last; step += CR) {
     step_of(step, std::integral_constant<int, 0>());
     if (step + 1 <= last) step_of(step + 1, std::integral_constant<int, 1>());
-    if constexpr (R >= 4) {
+    if constexpr (CR >= 4) {
       if (step + 2 <= last) step_of(step + 2, std::integral_constant<int, 2>());
       if (step + 3 <= last) step_of(step + 3, std::integral_constant<int, 3>());
     }
   }
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+  for (int i = 0; i < CR; ++i)
 #pragma unroll
-    for (int c = 0; c < CPT; ++c) asm volatile("" ::"v"(code[i][c]), "v"(scale[i][c]));
+    for (int c = 0; c < 2 * CPT; ++c) asm volatile("" ::"v"(code[i][c]), "v"(scale[i][c % SL]));
   __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0(0));  // no DMA outlives the workgroup
   if (a.y_f32 || a.parts) {
     const bool part = a.parts != nullptr;  // sums of some of the steps: joined, and scaled, by fp4_join_kernel
@@ -726,7 +754,14 @@ static int launch_tile(const Fp4MatmulArgs& a, int64_t batch, int splits, hipStr
   using C = Fp4Tile<R, WM, WN, MS, NS, GRAD>;
   const int64_t mt = (a.M + C::BM - 1) / C::BM, ot = (a.O + C::BO - 1) / C::BO, grid = (mt * ot + 7) / 8 * 8;
   if (grid * C::TH > kMost) return fail(FP4_ERR_UNSUPPORTED, "fp4_matmul: too many rows or outputs");
-  hipLaunchKernelGGL((fp4_tile_kernel<FMT, GRAD, TERMS, R, WM, WN, MS, NS>), dim3((unsigned)grid, (unsigned)splits, (unsigned)batch), dim3(C::TH), 0, st, a, (int)mt, (int)ot);
+  const dim3 wgs3((unsigned)grid, (unsigned)splits, (unsigned)batch);
+  // a thread's two NVFP4 scales as one load
+  constexpr bool PAIRS = FMT == FP4_FMT_NVFP4 && C::CPT == 2;
+  if (!PAIRS || (a.K % 32 == 0 && (uintptr_t)a.ws % 2 == 0)) {
+    hipLaunchKernelGGL((fp4_tile_kernel<FMT, GRAD, TERMS, true, R, WM, WN, MS, NS>), wgs3, dim3(C::TH), 0, st, a, (int)mt, (int)ot);
+  } else if constexpr (PAIRS) {
+    hipLaunchKernelGGL((fp4_tile_kernel<FMT, GRAD, TERMS, false, R, WM, WN, MS, NS>), wgs3, dim3(C::TH), 0, st, a, (int)mt, (int)ot);
+  }
   FP4_CHECK(check_launch("fp4_matmul"));
   if (splits == 1) return FP4_OK;
   const int64_t wgs = (a.M * a.O * batch + 1023) / 1024;
