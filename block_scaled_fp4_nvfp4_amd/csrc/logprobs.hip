@@ -226,6 +226,7 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& a, int64_t row, co
 // new one and counts the exponentials that are 1.  Alternatives: a round with
 // nothing above the wave's last one costs a comparison; else the lanes' largest values
 // are taken out and inserted, or where they are many sorted and merged into the list.
+// 4096 x 65536 bf16 in 101 us, 5.3 TB/s of logits.
 //
 // HELD rounds at most (0: any number): all are loaded at once and stay in registers, so that the workgroup knows its largest
 // logit before any sum, and a floor that no alternative lies below: the top-th largest of its 64 groups' largest.
@@ -533,7 +534,10 @@ __global__ void __launch_bounds__(512) logprobs_join_kernel(LogprobArgs a) {
 }
 
 // Few rows: 16 waves a workgroup with up to four rounds in registers, a row of more in parts of two as long as there are
-// fewer workgroups than compute units.  Else four waves, and parts that fill the card four times over.
+// fewer workgroups than compute units.  Else four waves, and parts that fill the card four times over.  Measured (us, graph
+// replays, registers and else): 1 x 32000 bf16 top 5 11.4 and 12.1, 16 x 131000 f32 top 20 14.9 and 19.8, 300 x 50000 bf16
+// top 20 28.6 and 42.2, 1 x 131072 bf16 16.2 both, 100 x 50000 f32 without alternatives 12.6 and 11.5, 16 x 131072 f32 top 64
+// 27.6 and 23.9: what loses little is left to one rule.
 constexpr int kHeld = 4;
 struct LogprobShape {
   bool held;
@@ -562,7 +566,7 @@ struct LogprobGradArgs {
 
 // 2^t (A + B t) for all logits, the target's apart.  Bound by the bytes: pieces of
 // 16 bytes where the rows of both sides lie alike, single values at their ends and
-// where they do not.
+// where they do not.  4096 x 65536 bf16 in 213 us, 5.0 TB/s read and written: a copy's rate.
 template <typename T, bool ENTROPY>
 __global__ void __launch_bounds__(256) logprobs_grad_kernel(LogprobGradArgs a) {
   constexpr int PV = 16 / (int)sizeof(T);
@@ -586,7 +590,8 @@ __global__ void __launch_bounds__(256) logprobs_grad_kernel(LogprobGradArgs a) {
     return __builtin_amdgcn_exp2f(z) * f;
   };
   auto target = [&](float v) __attribute__((always_inline)) {  // 1 - p_t without the subtraction
-    const float z = (v - m) * a.inv_t, q = scale * (glp * (R - expm1f(z)));
+    // divided by Z before 1 / T is applied: their quotient `scale` may be a subnormal of few bits where this is not
+    const float z = (v - m) * a.inv_t, q = none ? 0.0f : glp * ((R - expm1f(z)) / Z) * a.inv_t;
     if constexpr (!ENTROPY) return q;
     const float f = gH * (fmaxf(z, -200.0f) + (H - logZ));
     return fmaf(-scale * f, __expf(z), q);
@@ -648,8 +653,8 @@ static int validate_logprobs(int dtype, int64_t tokens, int64_t vocab, int64_t s
   if (vocab >= (int64_t)1 << 30 || tokens >= (int64_t)1 << 24 || stride >= (int64_t)1 << 40 || (double)tokens * stride > 0x1p46)
     return fail(FP4_ERR_UNSUPPORTED, "logprobs: 2^30 logits a row, 2^24 rows or more than 2^46 logits");
   if (top < 0 || top > kTopMost) return fail(FP4_ERR_INVALID_ARG, "logprobs: top = %d, 0 to %d expected", top, kTopMost);
-  // below, 1 / T times log2(e) may be infinite, and 0 times it NaN
-  if (!(temperature >= 0x1p-126f && temperature < __builtin_huge_valf())) return fail(FP4_ERR_INVALID_ARG, "logprobs: temperature %g", (double)temperature);
+  // far below, 1 / T and what is made of it overflow, and 0 times that is NaN
+  if (!(temperature >= 0x1p-100f && temperature < __builtin_huge_valf())) return fail(FP4_ERR_INVALID_ARG, "logprobs: temperature %g", (double)temperature);
   return FP4_OK;
 }
 

@@ -508,7 +508,7 @@ int fp4_matmul_grad(int w_fmt, const void* dy, int dy_dtype, const uint8_t* w, c
  *  logits       bf16 or f32 (`dtype`), row t at logits + t * stride (in values).
  *  targets      int32 [tokens]; one outside [0, vocab) is no token: logprob 0, rank
  *               -1.  NULL if neither logprobs nor ranks is asked for.
- *  temperature  2^-126 or more, finite.
+ *  temperature  2^-100 or more, finite.
  *  logprobs, ranks, stats  out, each optional (may be NULL); top_ids, top_logprobs out,
  *               needed if top > 0 (top <= 64, which may exceed vocab).
  *  workspace    as fp4_matmul's, of token_logprobs_workspace_size bytes.

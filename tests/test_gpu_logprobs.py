@@ -262,3 +262,32 @@ def test_no_rows():
     r = fp.token_logprobs(torch.empty(0, 50, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda"), top=3)
     assert r["top_ids"].shape == (0, 3) and r["logprobs"].shape == (0,)
     assert fp.token_logprobs_grad(torch.empty(0, 50, device="cuda"), None, r["stats"], None).shape == (0, 50)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V", [(2, 1001), (3, 70001), (800, 3001)])
+def test_temperatures_at_the_ends(dtype, T, V):
+    """The least temperature leaves the largest logit alone, a huge one makes all tokens alike."""
+    print_case(f"logprobs T={T} V={V} {dtype}, temperatures 2^-100 and 2^126")
+    g = gen(V)
+    logits = _logits(g, T, V, DT[dtype]).clamp(-50, 50)
+    best = torch.randint(0, V, (T,), device="cuda", generator=g)
+    other = (best + 1) % V
+    rows = torch.arange(T, device="cuda")
+    logits[rows, best] = 64.0
+    glp, gH = torch.ones(T, device="cuda"), torch.full((T,), -0.5, device="cuda")
+    cold = 2.0 ** -100
+    r = _m().token_logprobs(logits, best.int(), top=2, temperature=cold)
+    assert bool((r["logprobs"] == 0).all()) and bool((r["entropy"] == 0).all()) and bool((r["ranks"] == 0).all())
+    assert torch.equal(r["top_ids"][:, 0].long(), best) and bool((r["top_logprobs"][:, 1] <= -14 * 2.0 ** 100 * (1 - 2.0 ** -20)).all())
+    d = _m().token_logprobs_grad(logits, best.int(), r["stats"], glp, gH, cold)
+    assert bool((d == 0).all())
+    # another target: -p_best / T at the largest logit, 1 / T at the target
+    d = _m().token_logprobs_grad(logits, other.int(), r["stats"], glp, gH, cold).float()
+    assert bool((d[rows, best] == -1 / cold).all()) and bool((d[rows, other] == 1 / cold).all()) and int((d != 0).sum()) == 2 * T
+    r = _m().token_logprobs(logits, best.int(), temperature=2.0 ** 126)
+    lnv = math.log(V)
+    # every exponential is 1 and Z - 1 exact; log1p and one rounding
+    assert float((r["logprobs"] + lnv).abs().max()) <= 4 * 2.0 ** -24 * lnv and float((r["entropy"] - lnv).abs().max()) <= 4 * 2.0 ** -24 * lnv
+    d = _m().token_logprobs_grad(logits, best.int(), r["stats"], glp, gH, 2.0 ** 126)
+    assert bool((d.abs() <= 2.0 ** -126).all())
