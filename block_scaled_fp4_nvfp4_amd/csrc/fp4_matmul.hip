@@ -113,9 +113,9 @@ __device__ __forceinline__ bf16x8_t as_bf16x8(u32x4 v) { return __builtin_bit_ca
 // ------------------------------------------------------------ few rows
 
 constexpr int kFewK = 256;   // a wave's step: 128 bytes of codes of each of 16 rows of W
-constexpr int kRing = 4;     // steps on their way to a wave
+constexpr int kRing = 4;     // steps on their way to a wave (2, 3 and 6 measured the same)
 constexpr int kSlot = 2304;  // bytes of a step: 2 KB of codes, scales
-constexpr int kDirectRows = 4;
+constexpr int kDirectRows = 4;  // up to these x's fragments come straight from memory: 1 x 2560 x 2560 5.3 us (6.3 by DMA), 16 x 131072 x 2560 42.5 (41.0)
 // Waves that multiply: seven and the adding one have 256 registers each, eight and it 168.
 constexpr int few_waves(int ms, int u, int terms) { return ms * u * terms > 2 ? 7 : 8; }
 constexpr int few_per_simd(int ms, int u, int terms) { return ms * u * terms == 2 ? 4 : ms * u * terms == 1 ? 6 : ms * u * terms == 3 ? 3 : 2; }
@@ -175,7 +175,8 @@ struct XPiece {
 // into the MFMAs as their A operand.  A strip's partial sums meet in LDS.  Where rows
 // of codes or scales are not whole pieces of DMA (DMA false), they are loaded
 // straight into registers, without a step ahead.  Bound by W's bytes, or by latency
-// where they are few.
+// where they are few: 16 x 131072 x 2560 MXFP4 in 39 us, 4.8 TB/s (the rings alone take
+// 31); 1 x 2560 x 2560 NVFP4 in 5.6.  Strips in pairs or runs of neighbours took 43 to 45.
 template <int FMT, int TERMS, int MS, int U, bool DMA>
 __global__ void __launch_bounds__(64 * (few_waves(MS, U, TERMS) + 1), few_per_simd(MS, U, TERMS)) fp4_few_kernel(Fp4FewArgs a) {
   constexpr int SLOT = kSlot, RING = DMA ? kRing * SLOT : 8192, BLOCKS = FMT == FP4_FMT_NVFP4 ? 16 : 8;  // scales of a row and step
@@ -835,7 +836,9 @@ static int launch_fp4(const Fp4MatmulArgs& a, int64_t batch, int kind, int split
 
 // ------------------------------------------------------------ the calls
 
-// The few-rows kernel's blocks of 16 rows for a product, 0 where tiles are to take it.
+// The few-rows kernel's blocks of 16 rows for a product, 0 where tiles are to take it.  Measured (us, few-rows kernel and
+// tiles): 32 x 10240 x 2560 12.4 and 22, 64 x 10240 x 2560 15.9 and 22.9, 77 x 2560 x 2560 17 and 15.4, 256 x 10240 x 2560
+// 28.8 and 22.2; 64 x 2560 x 2560 f32 12.1 and 50.
 static int few_blocks(int64_t m, int64_t n, int64_t k, int terms) {
   if (m > (terms == 3 ? 128 : 64)) return 0;
   for (int ms = terms == 3 || m <= 16 ? 1 : m <= 32 ? 2 : 4; ms > 0; ms /= 2)

@@ -219,6 +219,25 @@ def test_nothing_outside_is_read_or_written(grad, m, n, k):
     check_product(out, x, _wt(w, "nvfp4", grad), 1)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("grad", [False, True], ids=["product", "gradient"])
+@pytest.mark.parametrize("m,n,kb", [(3, 300, 80), (100, 260, 80), (700, 2560, 40), (1100, 2050, 33)])
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_scales_at_any_address(fmt, grad, m, n, kb, off):
+    """Scales are bytes: they may start anywhere."""
+    k = kb * BLOCK[fmt]
+    print_case(f"{'grad' if grad else 'matmul'} {fmt} m={m} n={n} k={k} scales + {off}")
+    g = gen(m + off)
+    xv, w = _x(g, 1, m, n if grad else k, torch.bfloat16), raw_weight(g, fmt, 1, n, k)
+    s = w["scales"]
+    buf = torch.full((s.numel() + 16,), 0x7F, device="cuda", dtype=torch.uint8)  # NVFP4's NaN around them
+    shifted = buf[off:off + s.numel()].view(s.shape)
+    shifted.copy_(s.view(torch.uint8))
+    assert shifted.data_ptr() % 4 == off
+    y = _call(grad)(xv, {**w, "scales": shifted}, fmt, out_dtype=torch.float32)
+    check_product(y, xv, _wt(w, fmt, grad), 1)
+
+
 def test_empty_products():
     fp = _m()
     g = gen(0)
