@@ -100,10 +100,12 @@ __device__ __forceinline__ uint32_t decode2(uint32_t codes, float scale) {
 }
 
 // A tensor scale S as pow2 mant: the power of two goes into the weights (which stay
-// bf16's normal numbers), the rest is applied to the sums.  S = 0 makes weights of 0,
-// so that no sum of large x is infinite before it is multiplied by 0.
+// bf16's normal numbers), the rest, 1 or more, is applied to the sums, which are
+// no larger than the results then.  (Below 2^-100 mant is less than 1, and the results are
+// far below f32's end.)  S = 0 makes weights of 0, so that no sum of large x is infinite
+// before it is multiplied by 0.
 __device__ __forceinline__ void split_scale(float S, float& pow2, float& mant) {
-  const int e = min(100, max(-100, __builtin_amdgcn_frexp_expf(S)));
+  const int e = min(100, max(-100, __builtin_amdgcn_frexp_expf(S) - 1));
   pow2 = S == 0.0f ? 0.0f : ldexpf(1.0f, e);
   mant = ldexpf(S, -e);
 }

@@ -465,8 +465,9 @@ int fp8_block_matmul(const void* x, int x_dtype, const float* x_scales, const ui
  *               Calls in flight at once, captured graphs among them, need one each.
  * Operands are exact (bf16 x and decoded weights as they are, f32 x as three bf16
  * terms, which lose what lies below 2^-133) and sums are f32, of products with S's
- * power of two in them: nothing overflows or vanishes that does not in the result.  Weights beyond f32's range
- * (MXFP4 scales of 2^126 and more) are infinite, as fp4_dequantize has them.  Every
+ * power of two in them, so that a result is infinite or NaN only where it or a partial
+ * sum of it leaves f32's range, and loses no more below it than f32 sums do.  Weights
+ * beyond f32's range (MXFP4 scales of 2^126 and more) are infinite, as fp4_dequantize has them.  Every
  * buffer is contiguous; any m >= 0 and n >= 0.  A result does not depend on other
  * rows of x or other matrices' values, and repeats bit for bit.
  * Errors: k % B, k == 0 -> FP4_ERR_SHAPE; unknown format or dtype, null or
