@@ -581,8 +581,13 @@ __global__ void __launch_bounds__(256) logprobs_grad_kernel(LogprobGradArgs a) {
   const int32_t t = a.d_logprobs ? a.targets[row] : -1;
   const bool given = t >= 0 && t < V;
   const float glp = given ? a.d_logprobs[row] : 0.0f, gH = ENTROPY && a.d_entropy ? a.d_entropy[row] : 0.0f;
-  const float logZ = none ? 0.0f : log1pf(R), scale = none ? 0.0f : a.inv_t / Z, c = a.inv_t * kLog2E;
-  const float A = -scale * (ENTROPY ? glp + gH * (H - logZ) : glp), B = -scale * gH * kLn2;
+  const float logZ = none ? 0.0f : log1pf(R), c = a.inv_t * kLog2E;
+  // f / (Z T) by the mantissas first and the powers of two last: 1 / (Z T) alone may be a subnormal of few bits
+  auto by_row = [&](float f) __attribute__((always_inline)) {
+    const float q = __builtin_amdgcn_frexp_mantf(f) * __builtin_amdgcn_frexp_mantf(a.inv_t) / Z;
+    return none ? 0.0f : ldexpf(q, __builtin_amdgcn_frexp_expf(f) + __builtin_amdgcn_frexp_expf(a.inv_t));
+  };
+  const float A = -by_row(ENTROPY ? glp + gH * (H - logZ) : glp), B = ENTROPY ? -by_row(gH) * kLn2 : 0.0f;
   auto value = [&](float v) __attribute__((always_inline)) {
     const float z = (v - m) * c;
     float f = A;
@@ -590,11 +595,10 @@ __global__ void __launch_bounds__(256) logprobs_grad_kernel(LogprobGradArgs a) {
     return __builtin_amdgcn_exp2f(z) * f;
   };
   auto target = [&](float v) __attribute__((always_inline)) {  // 1 - p_t without the subtraction
-    // divided by Z before 1 / T is applied: their quotient `scale` may be a subnormal of few bits where this is not
-    const float z = (v - m) * a.inv_t, q = none ? 0.0f : glp * ((R - expm1f(z)) / Z) * a.inv_t;
+    const float z = (v - m) * a.inv_t, q = none ? 0.0f : scale_by((R - expm1f(z)) / Z, glp, a.inv_t);
     if constexpr (!ENTROPY) return q;
     const float f = gH * (fmaxf(z, -200.0f) + (H - logZ));
-    return fmaf(-scale * f, __expf(z), q);
+    return fmaf(-by_row(f), __expf(z), q);
   };
   auto one = [&](int i) __attribute__((always_inline)) {
     const float v = logit(l, i), g = i == t ? target(v) : value(v);

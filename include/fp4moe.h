@@ -535,8 +535,8 @@ int token_logprobs(const void* logits, int dtype, int64_t tokens, int64_t vocab,
  * d_entropy[t] H[t]) with respect to the logits, p_j = e^z_j / Z:
  *   d_logits[j] = (d_logprobs ([j = target] - p_j) - d_entropy p_j (ln p_j + H)) / temperature
  *  stats        of token_logprobs on the same logits and temperature.
- *  d_logprobs, d_entropy  f32 [tokens], each optional (NULL: zeros); targets may be
- *               NULL without d_logprobs.
+ *  d_logprobs, d_entropy  f32 [tokens], each optional (NULL: zeros), whose quotients by
+ *               the temperature f32 holds; targets may be NULL without d_logprobs.
  *  d_logits     out, logits' type, row t at d_logits + t * d_stride; may be logits itself
  *               (with d_stride == stride), no other overlap.
  * Masked tokens other than the target, rows with every token masked and, of
