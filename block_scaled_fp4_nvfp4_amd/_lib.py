@@ -308,6 +308,14 @@ def _device_tensor(t: torch.Tensor, dev: torch.device, name: str) -> int:
     return t.data_ptr()
 
 
+def _no_graph(how: str, *tensors):
+    """Refuses tensors that autograd records: the calls with gradients of their own are not part of its graph, and a
+    result without one would leave its gradient out of a training step silently."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError(f"an operand that requires a gradient: {how}, under torch.no_grad() or in a torch.autograd.Function, or "
+                         "detach the operand")
+
+
 def fp8_matmul(x, w: dict, out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
                workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """fp8_block_matmul: y = x . W^T in block FP8.
@@ -385,6 +393,7 @@ def _fp4_product(x, w, fmt, grad, out_dtype, out, workspace):
     code, out_code = _dtype_code(x), _SIZES.get(out_dtype)
     if out_code is None:
         raise TypeError(f"unsupported dtype {out_dtype}")
+    _no_graph("call fp4_matmul and fp4_matmul_grad by hand", x, ts, out)
     b, m, c = _dims(x)
     wb, n, k = _dims(codes)
     k *= 2
@@ -426,7 +435,9 @@ def fp4_matmul(x: torch.Tensor, w: dict, fmt: str, out_dtype: torch.dtype = torc
     Returns y [M, N] or [B, M, N] in out_dtype (bf16 or f32), in `out` if given
     (not x's or w's memory), rounded once from f32 sums of exact operands.
     workspace: a uint8 device tensor of fp4_matmul_workspace_size bytes;
-    allocated here when not given."""
+    allocated here when not given.
+    Not recorded by autograd: with gradients enabled, an operand that requires
+    one is refused (fp4_matmul_grad is the backward of a torch.autograd.Function)."""
     return _fp4_product(x, w, fmt, False, out_dtype, out, workspace)
 
 
@@ -435,7 +446,8 @@ def fp4_matmul_grad(dy: torch.Tensor, w: dict, fmt: str, out_dtype: torch.dtype 
     """fp4_matmul_grad: dx = dy . W, the gradient of fp4_matmul(x, w, fmt) with
     respect to x.  dy: contiguous bf16 / f32 device tensor [M, N] or [B, M, N]; w
     as there; returns dx [M, K] or [B, M, K].  workspace:
-    fp4_matmul_workspace_size(..., grad=True) bytes."""
+    fp4_matmul_workspace_size(..., grad=True) bytes.  Not recorded by autograd, as
+    there."""
     return _fp4_product(dy, w, fmt, True, out_dtype, out, workspace)
 
 
@@ -482,7 +494,10 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor], top: i
     and, with top > 0, int32 top_ids and f32 top_logprobs [T, top]: the most
     likely tokens, ties to the lower id; slots left over -1 and -inf.
     workspace: a uint8 device tensor of token_logprobs_workspace_size bytes;
-    allocated here when not given."""
+    allocated here when not given.
+    Not recorded by autograd: with gradients enabled, logits that require one are
+    refused (token_logprobs_grad is the backward of a torch.autograd.Function)."""
+    _no_graph("call token_logprobs and token_logprobs_grad by hand", logits)
     ptr, T, V, stride = _logit_rows(logits, "logits")
     code, dev = _dtype_code(logits), logits.device
     tp = _per_token(targets, torch.int32, T, dev, "targets")
@@ -515,7 +530,9 @@ def token_logprobs_grad(logits: torch.Tensor, targets: Optional[torch.Tensor], s
     d_entropy * entropy) with respect to the logits.  logits, targets and
     temperature as in token_logprobs, stats from it; d_logprobs, d_entropy f32
     [T] or None.  Returns d_logits [T, V] of the logits' type, in `out` if given
-    (rows at any stride; logits itself is allowed)."""
+    (rows at any stride; logits itself is allowed).  Not recorded by autograd, as
+    there."""
+    _no_graph("gradients of this gradient are not offered: call it", logits, stats, d_logprobs, d_entropy, out)
     ptr, T, V, stride = _logit_rows(logits, "logits")
     code, dev = _dtype_code(logits), logits.device
     if out is None:
