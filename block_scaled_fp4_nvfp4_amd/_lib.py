@@ -280,25 +280,37 @@ def _raw_stream(index: int) -> int:
 
 
 def _on_device(index: int, fn, *args):
-    """fn(*args) with `index` the current device; the library launches on the current device."""
-    if torch.cuda.current_device() == index:
+    """fn(*args) with `index` the current device; the library launches on the current device.  (Its tensors are there, so
+    that torch.cuda.current_device(), which starts the GPU first if need be, has nothing to add and takes twice as long.)"""
+    if torch._C._cuda_getDevice() == index:
         return fn(*args)
     with torch.cuda.device(index):
         return fn(*args)
 
 
-try:  # torch's allocation without its dispatcher: 0.7 us for 1.6, of calls that take 7
+try:  # torch's allocation without its dispatcher: 0.8 us for 1.7, of calls that take 8
+    from torch._C import _get_deterministic_algorithms, _len_torch_dispatch_stack
     from torch._C._dynamo.guards import _empty_strided_cuda
 except ImportError:
     _empty_strided_cuda = None
 
 
-def _empty(shape: tuple, dtype: torch.dtype, dev: torch.device) -> torch.Tensor:
-    """torch.empty of at most three dimensions on a GPU."""
-    if _empty_strided_cuda is None or torch.cuda.current_device() != dev.index:
-        return torch.empty(shape, dtype=dtype, device=dev)
+def _short_empty(shape: tuple, dtype: torch.dtype) -> torch.Tensor:
+    """torch.empty of at most three dimensions on the current GPU."""
     n = len(shape)
-    return _empty_strided_cuda(shape, (1,) if n == 1 else (shape[1], 1) if n == 2 else (shape[1] * shape[2], shape[2], 1), dtype)
+    try:
+        return _empty_strided_cuda(shape, (1,) if n == 1 else (shape[1], 1) if n == 2 else (shape[1] * shape[2], shape[2], 1), dtype)
+    except TypeError:  # it takes other arguments
+        return torch.empty(shape, dtype=dtype, device="cuda")
+
+
+def _allocator(dev: torch.device):
+    """empty(shape, dtype) on `dev` for the results of one call: torch.empty itself where a dispatch mode or the fill of
+    empty tensors (torch.use_deterministic_algorithms) has to see them."""
+    if (_empty_strided_cuda is None or _len_torch_dispatch_stack() or _get_deterministic_algorithms()
+            or torch._C._cuda_getDevice() != dev.index):
+        return lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)
+    return _short_empty
 
 
 def _device_tensor(t: torch.Tensor, dev: torch.device, name: str) -> int:
@@ -308,10 +320,10 @@ def _device_tensor(t: torch.Tensor, dev: torch.device, name: str) -> int:
     return t.data_ptr()
 
 
-def _no_graph(how: str, *tensors):
-    """Refuses tensors that autograd records: the calls with gradients of their own are not part of its graph, and a
-    result without one would leave its gradient out of a training step silently."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+def _no_graph(how: str):
+    """Refuses an operand that requires a gradient while autograd records: the calls with gradients of their own are not part
+    of its graph, and a result without one would leave its gradient out of a training step silently."""
+    if torch.is_grad_enabled():
         raise ValueError(f"an operand that requires a gradient: {how}, under torch.no_grad() or in a torch.autograd.Function, or "
                          "detach the operand")
 
@@ -393,7 +405,8 @@ def _fp4_product(x, w, fmt, grad, out_dtype, out, workspace):
     code, out_code = _dtype_code(x), _SIZES.get(out_dtype)
     if out_code is None:
         raise TypeError(f"unsupported dtype {out_dtype}")
-    _no_graph("call fp4_matmul and fp4_matmul_grad by hand", x, ts, out)
+    if x.requires_grad or (ts is not None and ts.requires_grad) or (out is not None and out.requires_grad):
+        _no_graph("call fp4_matmul and fp4_matmul_grad by hand")
     b, m, c = _dims(x)
     wb, n, k = _dims(codes)
     k *= 2
@@ -405,9 +418,9 @@ def _fp4_product(x, w, fmt, grad, out_dtype, out, workspace):
     dev = x.device
     if dev.type != "cuda":
         raise ValueError(f"device tensors expected, got {dev}")
-    shape = (m, k if grad else n) if x.dim() == 2 else (b, m, k if grad else n)
+    shape, empty = (m, k if grad else n) if x.dim() == 2 else (b, m, k if grad else n), _allocator(dev)
     if out is None:
-        out = _empty(shape, out_dtype, dev)
+        out = empty(shape, out_dtype)
     elif out.dtype != out_dtype or tuple(out.shape) != shape:
         raise ValueError(f"out {out.dtype} {tuple(out.shape)}, {out_dtype} {shape} expected")
     if workspace is not None:
@@ -415,7 +428,7 @@ def _fp4_product(x, w, fmt, grad, out_dtype, out, workspace):
     else:
         ws_bytes = fp4_matmul_workspace_size(x.dtype, b, m, n, k, fmt, grad)
         if ws_bytes:
-            workspace = _empty((ws_bytes,), torch.uint8, dev)
+            workspace = empty((ws_bytes,), torch.uint8)
     call = lib().fp4_matmul_grad if grad else lib().fp4_matmul
     _check(_on_device(dev.index, call, FMT[fmt], _device_tensor(x, dev, name), code, _device_tensor(codes, dev, "W"),
                       _device_tensor(scales, dev, "W scales"), None if ts is None else _device_tensor(ts, dev, "W tensor scale"),
@@ -497,26 +510,27 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor], top: i
     allocated here when not given.
     Not recorded by autograd: with gradients enabled, logits that require one are
     refused (token_logprobs_grad is the backward of a torch.autograd.Function)."""
-    _no_graph("call token_logprobs and token_logprobs_grad by hand", logits)
+    if logits.requires_grad:
+        _no_graph("call token_logprobs and token_logprobs_grad by hand")
     ptr, T, V, stride = _logit_rows(logits, "logits")
     code, dev = _dtype_code(logits), logits.device
     tp = _per_token(targets, torch.int32, T, dev, "targets")
-    f32, i32 = torch.float32, torch.int32
-    stats = _empty((T, 3), f32, dev)
+    f32, i32, empty = torch.float32, torch.int32, _allocator(dev)
+    stats = empty((T, 3), f32)
     r = {"entropy": stats.select(1, 2), "stats": stats}
     lp = ranks = ids = tops = None
     if tp is not None:
-        lp, ranks = _empty((T,), f32, dev), _empty((T,), i32, dev)
+        lp, ranks = empty((T,), f32), empty((T,), i32)
         r["logprobs"], r["ranks"] = lp, ranks
     if top > 0:
-        ids, tops = _empty((T, top), i32, dev), _empty((T, top), f32, dev)
+        ids, tops = empty((T, top), i32), empty((T, top), f32)
         r["top_ids"], r["top_logprobs"] = ids, tops
     if workspace is not None:
         ws_bytes = workspace.numel() * workspace.element_size()
     else:
         ws_bytes = token_logprobs_workspace_size(logits.dtype, T, V, top)
         if ws_bytes:
-            workspace = _empty((ws_bytes,), torch.uint8, dev)
+            workspace = empty((ws_bytes,), torch.uint8)
     _check(_on_device(dev.index, lib().token_logprobs, ptr, code, T, V, stride, tp, temperature, top, _ptr(lp), _ptr(ranks),
                       _ptr(ids), _ptr(tops), _ptr(stats), None if workspace is None else _device_tensor(workspace, dev, "workspace"),
                       ws_bytes, _raw_stream(dev.index)))
@@ -532,11 +546,13 @@ def token_logprobs_grad(logits: torch.Tensor, targets: Optional[torch.Tensor], s
     [T] or None.  Returns d_logits [T, V] of the logits' type, in `out` if given
     (rows at any stride; logits itself is allowed).  Not recorded by autograd, as
     there."""
-    _no_graph("gradients of this gradient are not offered: call it", logits, stats, d_logprobs, d_entropy, out)
+    if (logits.requires_grad or stats.requires_grad or (d_logprobs is not None and d_logprobs.requires_grad)
+            or (d_entropy is not None and d_entropy.requires_grad) or (out is not None and out.requires_grad)):
+        _no_graph("gradients of this gradient are not offered: call it")
     ptr, T, V, stride = _logit_rows(logits, "logits")
     code, dev = _dtype_code(logits), logits.device
     if out is None:
-        out = _empty((T, V), logits.dtype, dev)
+        out = _allocator(dev)((T, V), logits.dtype)
     elif out.dtype != logits.dtype or tuple(out.shape) != (T, V) or out.device != dev:
         raise ValueError(f"out {out.dtype} {tuple(out.shape)} on {out.device}, {logits.dtype} {(T, V)} on {dev} expected")
     optr, _, _, ostride = _logit_rows(out, "out")
