@@ -751,12 +751,13 @@ __global__ void __launch_bounds__(256) fp4_join_kernel(const float* __restrict__
 
 constexpr int64_t kMost = 0xFFFFFFFF;  // threads of a launch along x
 constexpr int64_t kMostMatrices = 65535;
+constexpr int tile_threads(int rows) { return rows == 256 ? 512 : 256; }
 
 template <int FMT, bool GRAD, int TERMS, int R, int WM, int WN, int MS, int NS>
 static int launch_tile(const Fp4MatmulArgs& a, int64_t batch, int splits, hipStream_t st) {
   using C = Fp4Tile<R, WM, WN, MS, NS, GRAD>;
+  static_assert(C::TH == tile_threads(C::BM), "what the plan counts");
   const int64_t mt = (a.M + C::BM - 1) / C::BM, ot = (a.O + C::BO - 1) / C::BO, grid = (mt * ot + 7) / 8 * 8;
-  if (grid * C::TH > kMost) return fail(FP4_ERR_UNSUPPORTED, "fp4_matmul: too many rows or outputs");
   const dim3 wgs3((unsigned)grid, (unsigned)splits, (unsigned)batch);
   // a thread's two NVFP4 scales as one load
   constexpr bool PAIRS = FMT == FP4_FMT_NVFP4 && C::CPT == 2;
@@ -921,7 +922,13 @@ static int plan_fp4(int w_fmt, int x_dtype, bool grad, int64_t batch, int64_t m,
   if (!p.few) choose_tile(m, p.out, p.ld / kBK, batch, (int)p.terms, p);
   p.row_bytes = p.rows ? ((size_t)(2 * p.terms) * (size_t)(batch * m * p.ld) + 255) / 256 * 256 : 0;
   p.bytes = p.row_bytes + (p.splits > 1 ? sizeof(float) * (size_t)p.splits * (size_t)(batch * m * p.out) : 0);
-  if (p.rows && batch * m * (p.ld / 8) > kMost) return fail(FP4_ERR_UNSUPPORTED, "fp4_matmul: too many rows");
+  // what no launch holds: workgroups of 256 threads that copy rows, of a tile (whose count is rounded up to a multiple of 8)
+  if (p.rows && (batch * m * (p.ld / 8) + 255) / 256 * 256 > kMost) return fail(FP4_ERR_UNSUPPORTED, "fp4_matmul: too many rows");
+  if (!p.few) {
+    const Fp4TileModel& t = kTiles[p.kind];
+    const int64_t tiles = ((m + t.bm - 1) / t.bm) * ((p.out + t.bo - 1) / t.bo);
+    if ((tiles + 7) / 8 * 8 * tile_threads(t.bm) > kMost) return fail(FP4_ERR_UNSUPPORTED, "fp4_matmul: too many rows or outputs");
+  }
   return FP4_OK;
 }
 
