@@ -982,6 +982,16 @@ int fp4_matmul_workspace_size(int w_fmt, int x_dtype, int64_t batch, int64_t m, 
   return FP4_OK;
 }
 
+// Not part of the interface: which kernel a call takes, for the tests that look at every one of them.  plan: blocks of 16
+// rows of the few-rows kernel (0: tiles), a tile's rows, its outputs, workgroups that share its steps, whether x is copied.
+int fp4_matmul_plan(int w_fmt, int x_dtype, int grad, int64_t batch, int64_t m, int64_t n, int64_t k, int* plan) {
+  Fp4Plan p;
+  FP4_CHECK(plan_fp4(w_fmt, x_dtype, grad != 0, batch, m, n, k, p));
+  const int chosen[] = {p.few, p.few ? 0 : kTiles[p.kind].bm, p.few ? 0 : kTiles[p.kind].bo, p.few ? 1 : p.splits, p.rows};
+  std::copy(chosen, chosen + 5, plan);
+  return FP4_OK;
+}
+
 int fp4_matmul(int w_fmt, const void* x, int x_dtype, const uint8_t* w, const void* w_scales, const float* tensor_scale, int64_t batch, int64_t m,
                int64_t n, int64_t k, void* y, int y_dtype, void* workspace, size_t workspace_bytes, void* stream) {
   return run_fp4(w_fmt, x, x_dtype, false, w, w_scales, tensor_scale, batch, m, n, k, y, y_dtype, workspace, workspace_bytes, stream);
