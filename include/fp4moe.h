@@ -516,7 +516,9 @@ int fp4_matmul_grad(int w_fmt, const void* dy, int dy_dtype, const uint8_t* w, c
  * A logit of -inf is a masked token: it has probability 0 and is never among the
  * alternatives; slots left over get id -1 and -inf.  A row with every token masked
  * has logprob -inf and stats (-inf, -1, 0).  NaN or +inf in a row makes its logprobs,
- * Z and H NaN; a NaN is never an alternative and comes before nothing.  Sums are f32.
+ * Z and H NaN; a NaN is never an alternative and comes before nothing.  Sums are f32;
+ * differences l - M are formed in f32, and an e^z below 2^-126 counts as 0 in Z, H and the
+ * gradients.
  * Results repeat bit for bit and do not depend on other rows; the order of a row's
  * sums, and with it their last bits, goes by how many rows there are and by the row's
  * alignment to 16 bytes.
