@@ -311,6 +311,17 @@ __global__ void __launch_bounds__(64 * (few_waves(MS, U, TERMS) + 1), few_per_si
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int q = 0; q < 4; ++q) piece[h][q].terms(k0 + 128 * h + 32 * g + 8 * q < a.K, xf[u][h][q][s]);
+        if constexpr (DMA && TERMS == 3) {
+          // f32's terms stay as they are now: split anew in every strip, as the compiler has it otherwise, they do not fit
+          // the registers (1 x 2560 x 2560 37 us, 8.3 so; 16 x 131072 x 2560 104 and 70)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int t = 0; t < TERMS; ++t) asm volatile("" : "+v"(xf[u][h][q][s][t]));
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     if (DMA && !direct) {
 #pragma unroll
@@ -839,9 +850,12 @@ static int launch_fp4(const Fp4MatmulArgs& a, int64_t batch, int kind, int split
 
 // ------------------------------------------------------------ the calls
 
-// The few-rows kernel's blocks of 16 rows for a product, 0 where tiles are to take it.  Measured (us, few-rows kernel and
-// tiles): 32 x 10240 x 2560 12.4 and 22, 64 x 10240 x 2560 15.9 and 22.9, 77 x 2560 x 2560 17 and 15.4, 256 x 10240 x 2560
-// 28.8 and 22.2; 64 x 2560 x 2560 f32 12.1 and 50.
+// The few-rows kernel's blocks of 16 rows for a product, 0 where tiles are to take it.  Measured (us, graph replays, NVFP4,
+// few-rows kernel and tiles): 1 x 2560 x 2560 5.8 and 11.6, 16 x 131072 x 2560 50 and 77, 32 x 10240 x 2560 12.9 and 18.3,
+// 64 x 10240 x 2560 16.3 and 22.3, 64 x 2560 x 7168 17 and 22, 77 x 2560 x 2560 17 and 15.4, 256 x 10240 x 2560 28.8 and 22.2;
+// f32 1 x 2560 x 2560 8.2 and 16.2, 64 x 2560 x 2560 14.3 and 19.6, 128 x 2560 x 3520 18.7 and 28.1.  Blocks of rows that
+// pass a wide W four times or more lose (64 x 10240 x 5120 35 and 27, 64 x 131072 x 5120 364 and 194, MXFP4 204 and 186;
+// f32 64 x 131072 x 2560 239 and 185, 128 x 131072 x 2560 468 and 244): the rule goes by rows and K alone.
 static int few_blocks(int64_t m, int64_t n, int64_t k, int terms) {
   if (m > (terms == 3 ? 128 : 64)) return 0;
   for (int ms = terms == 3 || m <= 16 ? 1 : m <= 32 ? 2 : 4; ms > 0; ms /= 2)
