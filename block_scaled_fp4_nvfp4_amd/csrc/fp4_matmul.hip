@@ -877,9 +877,10 @@ struct Fp4TileModel {
   int bm, bo, slots;
   double fixed, lone, loaded;
 };
-// This card's, fitted at 40 and 160 steps.  Measured (us, graph replays) in this order, without splits: dx of 16 x 10240 ->
+// A whole card's of 256 compute units, fitted at 40 and 160 steps before the codes came in wide loads (256 x 256 takes about
+// 1.9 a step at full load since then, not 2.15); which tile is the fastest is still what they say, below.  Measured (us, graph replays) in this order, without splits: dx of 16 x 10240 ->
 // 2560 80, 86, 77, 137, 276; y of 300 x 2560 -> 2560 36, 25, 18, 38, 76; of 1024 x 2560 -> 2560 85, 54, 33, 38, 77;
-// 8192 x 2560 -> 10240 - , - , 764, 586, 435 (all before the codes came in wide loads).  Since then, the last three each
+// 8192 x 2560 -> 10240 - , - , 764, 586, 435 (all before the wide loads).  Since then, the last three each
 // with its best split: y of 1024 x 2560 -> 2560 33, 34, 39; of 2048 x 4096 -> 4096 124, 80, 82; of 600 x 2560 -> 10240 70,
 // 51, 57; of 1024 x 2560 -> 10240 103, 77, 69; dx of 4096 x 2560 -> 2560 113, 79, 73: the model takes the fastest of each.
 constexpr Fp4TileModel kTiles[] = {{16, 128, 768, 3.0, 0.50, 1.25}, {32, 128, 768, 3.0, 0.54, 1.40}, {64, 64, 768, 3.0, 0.37, 0.72},
